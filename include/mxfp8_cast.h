@@ -63,7 +63,14 @@ enum {
   MX_ERR_ALIGN = -3,   /* a pointer is not suitably aligned */
   MX_ERR_CUDA = -4,    /* a CUDA call failed (see mx_last_cuda_error) */
   MX_ERR_GROUPS = -5,  /* invalid group count, or (device status) invalid offsets */
-  MX_ERR_DEVICE = -6   /* a pointer is not device memory of the current device */
+  MX_ERR_DEVICE = -6,  /* a pointer is not device memory of the current device */
+  MX_ERR_TYPE = -7     /* an element type argument is none of MX_BF16, MX_F32 */
+};
+
+/* Element types of arguments that may have either. */
+enum {
+  MX_BF16 = 0,
+  MX_F32 = 1
 };
 
 /* Fused dim0 + dim1 cast with both scale sets in blocked layout; one read of
@@ -239,6 +246,29 @@ int mx_cast_tensorwise(const void* x, int64_t n, void* q, float* scale, float* a
  *   q       M x K bytes, e4m3                                 [out]
  *   scale   M bf16 values                                     [out] */
 int mx_cast_rowwise(const void* x, int64_t M, int64_t K, void* q, void* scale, void* stream);
+
+/* Product of two MX operands, accumulated in fp32 on the tensor cores:
+ *   out[m][n] = sum_k A[m][k] B[n][k],  A[m][k] = qa[m][k] 2^(sa[m][k/32] - 127)
+ * and B likewise, rounded once to the output type.  The pages name the
+ * block-scaled GEMM as the reader of the casts' outputs (pytorch/ao PR #3416,
+ * Changes list: the blocked format for grouped GEMM) and leave it to libraries;
+ * here it closes the loop.  A linear layer y = x W^T (x T x K, W N x K) is
+ *   forward          (q0, s0) of x    with (q0, s0) of W    -> y  (T x N)
+ *   input gradient   (q0, s0) of dy   with (q1, s1) of W    -> dx (T x K)
+ *   weight gradient  (q1, s1) of dy   with (q1, s1) of x    -> dW (N x K)
+ * so that (q1, s1) of x, half the size of x, is all that the layer saves for
+ * its backward pass.
+ *   qa      M x K bytes, e4m3, blocks of 32 along rows      [in]
+ *   sa_blk  mx_blocked_bytes(M, K/32) bytes, e8m0           [in]
+ *   qb      N x K bytes, e4m3                               [in]
+ *   sb_blk  mx_blocked_bytes(N, K/32) bytes, e8m0           [in]
+ *   M, N    >= 1 (any); K % 32 == 0, K >= 32; all <= 2^31 - 256
+ *   out     M x N values of out_type (MX_BF16 or MX_F32)    [out]
+ * A NaN scale (0xFF) or element makes the results that use it NaN; sums
+ * beyond the output type's range give infinity.  A call gives the same bits
+ * every time. */
+int mx_matmul(const void* qa, const void* sa_blk, const void* qb, const void* sb_blk, int64_t M,
+              int64_t N, int64_t K, void* out, int32_t out_type, void* stream);
 
 /* Size helpers (host only, no CUDA calls).  Return -1 for invalid sizes. */
 int64_t mx_blocked_bytes(int64_t R, int64_t C);

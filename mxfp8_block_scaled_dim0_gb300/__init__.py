@@ -29,6 +29,7 @@ MX_ERR_ALIGN = -3
 MX_ERR_CUDA = -4
 MX_ERR_GROUPS = -5
 MX_ERR_DEVICE = -6
+MX_ERR_TYPE = -7
 
 # Every function the header declares, for load checks.
 ABI_SYMBOLS = (
@@ -39,6 +40,7 @@ ABI_SYMBOLS = (
     "mx_selftest_bounds",
     "mx_strerror", "mx_last_cuda_error", "mx_watchdog",
     "mx_selftest_watchdog", "mx_selftest_arm_stall", "mx_cast_dim0_dim1_noalloc",
+    "mx_matmul",
 )
 
 
@@ -76,6 +78,7 @@ def _lib():
             "mx_dequant_blocked": ([P, I64, I64, P, P, P], ctypes.c_int),
             "mx_cast_tensorwise": ([P, I64, P, P, P, P], ctypes.c_int),
             "mx_cast_rowwise": ([P, I64, I64, P, P, P], ctypes.c_int),
+            "mx_matmul": ([P, P, P, P, I64, I64, I64, P, I32, P], ctypes.c_int),
             "mx_blocked_bytes": ([I64, I64], I64),
             "mx_grouped_m_scale_bytes": ([I64, I64, I32, I32], I64),
             "mx_3d_scale_bytes": ([I64, I64, I64], I64),
@@ -163,6 +166,8 @@ BYTES = tuple(d for d in (torch.uint8, getattr(torch, "float8_e4m3fn", None),
 I32 = (torch.int32,)
 I64 = (torch.int64,)
 F32 = (torch.float32,)
+# Element types of arguments that may have either, as the C ABI numbers them.
+TYPES = {torch.bfloat16: 0, torch.float32: 1}
 
 
 def _dev_tensor(t, name, nbytes=None, dtypes=None, ndim=None):
@@ -328,6 +333,25 @@ def mx_cast_rowwise(x, q, scale, stream=None):
     _call("mx_cast_rowwise", _device(x, q, scale), stream, _ptr(x), M, K, _ptr(q), _ptr(scale))
 
 
+def mx_matmul(qa, sa_blk, qb, sb_blk, out, stream=None):
+    """out (M x N, bf16 or float32) = A B^T of MX operands: qa (M x K) and qb
+    (N x K) bytes with their blocked scales."""
+    _dev_tensor(qa, "qa", dtypes=BYTES, ndim=2)
+    _dev_tensor(qb, "qb", dtypes=BYTES, ndim=2)
+    M, K = qa.shape
+    N = qb.shape[0]
+    if qb.shape[1] != K:
+        raise ValueError("qa and qb must have equal rows, got %d and %d values" % (K, qb.shape[1]))
+    _dev_tensor(sa_blk, "sa_blk", mx_blocked_bytes(M, K // 32), BYTES)
+    _dev_tensor(sb_blk, "sb_blk", mx_blocked_bytes(N, K // 32), BYTES)
+    _dev_tensor(out, "out", dtypes=tuple(TYPES), ndim=2)
+    if tuple(out.shape) != (M, N):
+        raise ValueError("out must have shape %s, got %s" % ((M, N), tuple(out.shape)))
+    dev = _device(qa, sa_blk, qb, sb_blk, out)
+    _call("mx_matmul", dev, stream, _ptr(qa), _ptr(sa_blk), _ptr(qb), _ptr(sb_blk), M, N, K,
+          _ptr(out), TYPES[out.dtype])
+
+
 def mx_selftest_watchdog(wait_ns=50_000_000, stream=None):
     """Run the bounded-wait failure path on the device (no fault): a warp
     waits on a barrier that never completes and gives up after wait_ns."""
@@ -482,3 +506,10 @@ def cast_rowwise(x, stream=None):
     scale = torch.empty(M, dtype=torch.bfloat16, device=x.device)
     mx_cast_rowwise(x, q, scale, stream)
     return q, scale
+
+
+def matmul(qa, sa_blk, qb, sb_blk, out_dtype=torch.bfloat16, stream=None):
+    """A B^T of MX operands as a (M, N) tensor of out_dtype."""
+    out = torch.empty((qa.shape[0], qb.shape[0]), dtype=out_dtype, device=qa.device)
+    mx_matmul(qa, sa_blk, qb, sb_blk, out, stream)
+    return out

@@ -22,7 +22,8 @@ LIB = os.path.join(PKG, "libmxfp8_cast.so")
 # the tests run parity cases through it.
 OBJ_DIR_BOUNDS = os.path.join(PKG, "_build_bounds")
 LIB_BOUNDS = os.path.join(PKG, "libmxfp8_cast_bounds.so")
-SOURCES = ["mx_cast.cu", "mx_blocked.cu", "mx_dequant.cu", "mx_scaled.cu", "mx_abi.cu"]
+SOURCES = ["mx_cast.cu", "mx_blocked.cu", "mx_dequant.cu", "mx_scaled.cu", "mx_matmul.cu",
+           "mx_abi.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

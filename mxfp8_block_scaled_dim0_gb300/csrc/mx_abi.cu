@@ -57,10 +57,10 @@ struct MapKey {
   const void* base;
   uint64_t inner, outer, stride;
   uint32_t bin, bout;
-  int dt, l2;
+  int dt, l2, swizzle;
   bool operator==(const MapKey& o) const {
     return base == o.base && inner == o.inner && outer == o.outer && stride == o.stride &&
-           bin == o.bin && bout == o.bout && dt == o.dt && l2 == o.l2;
+           bin == o.bin && bout == o.bout && dt == o.dt && l2 == o.l2 && swizzle == o.swizzle;
   }
 };
 
@@ -75,11 +75,13 @@ struct MapCache {
 thread_local MapCache t_maps;
 
 // 2D tiled map: inner dimension `inner` (elements), `outer` rows `stride`
-// bytes apart, box `bin` x `bout`, 128-byte swizzle.
+// bytes apart, box `bin` x `bout`, 128-byte swizzle unless said otherwise.
 int encode_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t inner,
               uint64_t outer, uint64_t stride, uint32_t bin, uint32_t bout,
-              CUtensorMapL2promotion l2) {
-  const MapKey k = {base, inner, outer, stride, bin, bout, static_cast<int>(dt), static_cast<int>(l2)};
+              CUtensorMapL2promotion l2,
+              CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
+  const MapKey k = {base, inner, outer, stride, bin, bout, static_cast<int>(dt),
+                    static_cast<int>(l2), static_cast<int>(swizzle)};
   for (int i = 0; i < MapCache::kEntries; ++i) {
     if (t_maps.used[i] && t_maps.key[i] == k) {
       *m = t_maps.map[i];
@@ -93,7 +95,7 @@ int encode_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t
   const cuuint32_t box[2] = {bin, bout};
   const cuuint32_t estr[2] = {1, 1};
   CUresult r = fn(m, dt, 2, const_cast<void*>(base), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, l2,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, l2,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return cuda_fail(static_cast<int>(cudaErrorInvalidValue));
   const int slot = t_maps.next;
@@ -243,6 +245,7 @@ const char* mx_strerror(int code) {
     case MX_ERR_ALIGN: return "misaligned pointer (16-byte alignment required)";
     case MX_ERR_CUDA: return "CUDA call failed (see mx_last_cuda_error)";
     case MX_ERR_GROUPS: return "invalid group count or group offsets";
+    case MX_ERR_TYPE: return "unknown element type";
     case MX_ERR_DEVICE: return "pointer is not device memory of the current CUDA device";
     default: return "unknown error";
   }
@@ -259,12 +262,16 @@ int mx_watchdog(int clear) {
   int d = 0;
   rc = mx::read_dequant_watchdog(&d, clear != 0);
   if (rc) return cuda_fail(rc);
-  return v | w | d;
+  int m = 0;
+  rc = mx::read_matmul_watchdog(&m, clear != 0);
+  if (rc) return cuda_fail(rc);
+  return v | w | d | m;
 }
 
 int mx_bounds_check(int clear) {
-  const int parts[4] = {mx::out_of_bounds_cast(clear != 0), mx::out_of_bounds_blocked(clear != 0),
-                        mx::out_of_bounds_dequant(clear != 0), mx::out_of_bounds_scaled(clear != 0)};
+  const int parts[] = {mx::out_of_bounds_cast(clear != 0), mx::out_of_bounds_blocked(clear != 0),
+                       mx::out_of_bounds_dequant(clear != 0), mx::out_of_bounds_scaled(clear != 0),
+                       mx::out_of_bounds_matmul(clear != 0)};
   int sum = 0;
   for (int v : parts) {
     if (v == -1) return -1;                     // release build: no checks compiled in
@@ -410,6 +417,38 @@ int mx_cast_rowwise(const void* x, int64_t M, int64_t K, void* q, void* scale, v
   return launch_rc(mx::launch_cast_rowwise(static_cast<const uint16_t*>(x), M, K,
                                            static_cast<uint8_t*>(q), static_cast<uint16_t*>(scale),
                                            sms, static_cast<cudaStream_t>(stream)));
+}
+
+int mx_matmul(const void* qa, const void* sa_blk, const void* qb, const void* sb_blk, int64_t M,
+              int64_t N, int64_t K, void* out, int32_t out_type, void* stream) {
+  if (!qa || !sa_blk || !qb || !sb_blk || !out) return MX_ERR_NULL;
+  if (out_type != MX_BF16 && out_type != MX_F32) return MX_ERR_TYPE;
+  if (M < 1 || N < 1 || K < 32 || K % 32 != 0 || M > kMaxDim || N > kMaxDim || K > kMaxDim)
+    return MX_ERR_SHAPE;
+  if (!aligned(qa, 16) || !aligned(sa_blk, 16) || !aligned(qb, 16) || !aligned(sb_blk, 16) ||
+      !aligned(out, 16))
+    return MX_ERR_ALIGN;
+  if (int rc = check_device({qa, sa_blk, qb, sb_blk, out})) return rc;
+  int sms = 0;
+  if (int rc = current_sm_count(&sms)) return rc;
+  mx::MatmulMaps maps;
+  const int64_t tiles_k = cdiv(K, 128);
+  if (int rc = encode_2d(&maps.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, qa, K, M, K, 128, 128,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
+    return rc;
+  if (int rc = encode_2d(&maps.b, CU_TENSOR_MAP_DATA_TYPE_UINT8, qb, K, N, K, 128, 128,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
+    return rc;
+  if (int rc = encode_2d(&maps.sa, CU_TENSOR_MAP_DATA_TYPE_UINT32, sa_blk, tiles_k * 128,
+                         cdiv(M, 128), tiles_k * 512, 128, 1, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_NONE))
+    return rc;
+  if (int rc = encode_2d(&maps.sb, CU_TENSOR_MAP_DATA_TYPE_UINT32, sb_blk, tiles_k * 128,
+                         cdiv(N, 128), tiles_k * 512, 128, 1, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_NONE))
+    return rc;
+  return launch_rc(mx::launch_matmul(maps, M, N, K, out, out_type == MX_F32, sms,
+                                     static_cast<cudaStream_t>(stream)));
 }
 
 int mx_scales_to_blocked(const void* s, int64_t R, int64_t C, void* out, void* stream) {

@@ -110,6 +110,15 @@ int launch_group_offsets(const int32_t* offs, int G, int64_t M, int64_t* row_off
                          int64_t* col_offs, int32_t* status, cudaStream_t stream);
 int launch_scales_to_blocked(const uint8_t* s, int64_t R, int64_t C, uint8_t* out,
                              cudaStream_t stream);
+// MX product (mx_matmul.cu).  qa and qb: boxes of 128 bytes x 128 rows, 128B
+// swizzle; sa and sb: their blocked scales as rows of 128x4 tiles (32-bit words),
+// boxes of one 512-byte tile.
+struct MatmulMaps {
+  CUtensorMap a, b, sa, sb;
+};
+int launch_matmul(const MatmulMaps& maps, int64_t M, int64_t N, int64_t K, void* out, bool out_f32,
+                  int num_sms, cudaStream_t stream);
+int read_matmul_watchdog(int* out, bool clear);
 int read_watchdog(int* out, bool clear);
 // Stores refused by the bounds-checked build, per translation unit (cleared
 // on request); -1 in a release build.
@@ -117,6 +126,7 @@ int out_of_bounds_cast(bool clear);
 int out_of_bounds_blocked(bool clear);
 int out_of_bounds_dequant(bool clear);
 int out_of_bounds_scaled(bool clear);
+int out_of_bounds_matmul(bool clear);
 // -1 in a release build (nothing launched), else 0 or a cudaError_t value.
 int launch_bounds_selftest(void* buf, cudaStream_t stream);
 int read_scaled_watchdog(int* out, bool clear);   // the rowwise kernel's word (mx_scaled.cu)

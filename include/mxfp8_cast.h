@@ -270,6 +270,62 @@ int mx_cast_rowwise(const void* x, int64_t M, int64_t K, void* q, void* scale, v
 int mx_matmul(const void* qa, const void* sa_blk, const void* qb, const void* sb_blk, int64_t M,
               int64_t N, int64_t K, void* out, int32_t out_type, void* stream);
 
+/* Layer norm of bf16 rows, with its input saved in 8 bits for the backward
+ * pass.  The pages have no counterpart: the casts' formats put to use for what
+ * a training step keeps.
+ *   mean = (1/D) sum x, rstd = (eps + (1/D) sum (x - mean)^2)^(-1/2)
+ *   y    = (x - mean) rstd w + b, rounded once to bf16
+ *   x       bf16 (M x D)                                        [in]
+ *   w, b    D values of w_type (MX_BF16 or MX_F32); b may be NULL (no bias)
+ *                                                               [in]
+ *   M, D    M >= 1, 1 <= D <= 16384; with a saved input D % 32 == 0
+ *   eps     >= 0
+ *   y       bf16 (M x D)                                        [out]
+ *   mean, rstd  M floats each (4-byte aligned)                  [out]
+ *   q0, s0_blk  both NULL, or x saved: mx_cast_dim0's outputs for x, byte for
+ *           byte (M x D bytes; mx_blocked_bytes(M, D/32) bytes) [out]
+ * A row that holds Inf or NaN gives NaN. */
+int mx_layer_norm(const void* x, const void* w, const void* b, int32_t w_type, int64_t M, int64_t D,
+                  float eps, void* y, float* mean, float* rstd, void* q0, void* s0_blk,
+                  void* stream);
+
+/* Its backward pass, from x itself or from the saved input (x is then what
+ * (q0, s0_blk) stand for, mean and rstd still those of the forward pass):
+ *   xh = (x - mean) rstd, g = dy w
+ *   dx = rstd (g - (1/D) sum g - xh (1/D) sum g xh), rounded once to bf16
+ *   dw = sum over rows of dy xh, db = sum over rows of dy, summed in fp32 in a
+ *        fixed order, rounded once to w_type
+ *   dy      bf16 (M x D)                                        [in]
+ *   x       bf16 (M x D), or NULL with q0, s0_blk given         [in]
+ *   w       D values of w_type                                  [in]
+ *   dx      bf16 (M x D)                                        [out]
+ *   dw, db  D values of w_type; db may be NULL                  [out]
+ *   work    mx_layer_norm_backward_work_bytes(M, D) bytes of scratch, 16-byte
+ *           aligned; calls that overlap on the GPU need their own
+ * Other arguments and limits as mx_layer_norm. */
+int mx_layer_norm_backward(const void* dy, const void* x, const void* q0, const void* s0_blk,
+                           const void* w, int32_t w_type, const float* mean, const float* rstd,
+                           int64_t M, int64_t D, void* dx, void* dw, void* db, void* work,
+                           void* stream);
+
+/* Gated SiLU of bf16 rows [g | u], with its input saved in 8 bits.  The pages
+ * have no counterpart (see mx_layer_norm).
+ *   h = g u / (1 + exp(-g)), rounded once to bf16
+ *   gu      bf16 (M x 2F): g in columns [0, F), u in [F, 2F)    [in]
+ *   M, F    >= 1; with a saved input F % 32 == 0
+ *   h       bf16 (M x F)                                        [out]
+ *   q0, s0_blk  both NULL, or gu saved: mx_cast_dim0's outputs for gu, byte
+ *           for byte                                            [out] */
+int mx_swiglu(const void* gu, int64_t M, int64_t F, void* h, void* q0, void* s0_blk, void* stream);
+
+/* Its backward pass, from gu itself or from the saved input:
+ *   sg = 1 / (1 + exp(-g)), dg = dh u sg (1 + g (1 - sg)), du = dh g sg
+ *   dh      bf16 (M x F)                                        [in]
+ *   gu      bf16 (M x 2F), or NULL with q0, s0_blk given        [in]
+ *   dgu     bf16 (M x 2F): dg | du                              [out] */
+int mx_swiglu_backward(const void* dh, const void* gu, const void* q0, const void* s0_blk,
+                       int64_t M, int64_t F, void* dgu, void* stream);
+
 /* Size helpers (host only, no CUDA calls).  Return -1 for invalid sizes. */
 int64_t mx_blocked_bytes(int64_t R, int64_t C);
 /* dim 0: (M + 128*G) * ceil4(K/32); dim 1: ceil128(K) * (ceil(M/32) + 4*G). */
@@ -278,6 +334,9 @@ int64_t mx_grouped_m_scale_bytes(int64_t M, int64_t K, int32_t G, int32_t dim);
 int64_t mx_3d_scale_bytes(int64_t E, int64_t N, int64_t K);
 /* E * mx_blocked_bytes(N, K/32): dim0 scales of 3D weights. */
 int64_t mx_3d_dim0_scale_bytes(int64_t E, int64_t N, int64_t K);
+
+/* Scratch of mx_layer_norm_backward: partial sums of dw and db. */
+int64_t mx_layer_norm_backward_work_bytes(int64_t M, int64_t D);
 
 /* Text for an MX_* code (static storage). */
 const char* mx_strerror(int code);

@@ -40,7 +40,8 @@ ABI_SYMBOLS = (
     "mx_selftest_bounds",
     "mx_strerror", "mx_last_cuda_error", "mx_watchdog",
     "mx_selftest_watchdog", "mx_selftest_arm_stall", "mx_cast_dim0_dim1_noalloc",
-    "mx_matmul",
+    "mx_matmul", "mx_layer_norm", "mx_layer_norm_backward", "mx_layer_norm_backward_work_bytes",
+    "mx_swiglu", "mx_swiglu_backward",
 )
 
 
@@ -79,6 +80,13 @@ def _lib():
             "mx_cast_tensorwise": ([P, I64, P, P, P, P], ctypes.c_int),
             "mx_cast_rowwise": ([P, I64, I64, P, P, P], ctypes.c_int),
             "mx_matmul": ([P, P, P, P, I64, I64, I64, P, I32, P], ctypes.c_int),
+            "mx_layer_norm": ([P, P, P, I32, I64, I64, ctypes.c_float, P, P, P, P, P, P],
+                              ctypes.c_int),
+            "mx_layer_norm_backward": ([P, P, P, P, P, I32, P, P, I64, I64, P, P, P, P, P],
+                                       ctypes.c_int),
+            "mx_layer_norm_backward_work_bytes": ([I64, I64], I64),
+            "mx_swiglu": ([P, I64, I64, P, P, P, P], ctypes.c_int),
+            "mx_swiglu_backward": ([P, P, P, P, I64, I64, P, P], ctypes.c_int),
             "mx_blocked_bytes": ([I64, I64], I64),
             "mx_grouped_m_scale_bytes": ([I64, I64, I32, I32], I64),
             "mx_3d_scale_bytes": ([I64, I64, I64], I64),
@@ -212,6 +220,11 @@ def mx_3d_scale_bytes(E, N, K):
 @functools.lru_cache(maxsize=4096)
 def mx_3d_dim0_scale_bytes(E, N, K):
     return int(_lib().mx_3d_dim0_scale_bytes(E, N, K))
+
+
+@functools.lru_cache(maxsize=4096)
+def mx_layer_norm_backward_work_bytes(M, D):
+    return int(_lib().mx_layer_norm_backward_work_bytes(M, D))
 
 
 # ---- entry points (same names as the C ABI) ----------------------------------
@@ -350,6 +363,88 @@ def mx_matmul(qa, sa_blk, qb, sb_blk, out, stream=None):
     dev = _device(qa, sa_blk, qb, sb_blk, out)
     _call("mx_matmul", dev, stream, _ptr(qa), _ptr(sa_blk), _ptr(qb), _ptr(sb_blk), M, N, K,
           _ptr(out), TYPES[out.dtype])
+
+
+def _shaped(t, name, shape, dtypes):
+    _dev_tensor(t, name, dtypes=dtypes)
+    if tuple(t.shape) != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
+
+
+def _saved(q0, s0_blk, M, C):
+    """The 8-bit saved form of an (M, C) tensor; both parts or neither."""
+    if (q0 is None) != (s0_blk is None):
+        raise ValueError("q0 and s0_blk go together")
+    if q0 is not None:
+        _dev_tensor(q0, "q0", M * C, BYTES)
+        _dev_tensor(s0_blk, "s0_blk", mx_blocked_bytes(M, C // 32), BYTES)
+
+
+def mx_layer_norm(x, w, b, eps, y, mean, rstd, q0=None, s0_blk=None, stream=None):
+    """Layer norm of bf16 x (M x D) into caller buffers; with q0 and s0_blk its
+    input is saved in 8 bits.  b may be None."""
+    _dev_tensor(x, "x", dtypes=BF16, ndim=2)
+    M, D = x.shape
+    _shaped(w, "w", (D,), tuple(TYPES))
+    if b is not None:
+        _shaped(b, "b", (D,), (w.dtype,))
+    _shaped(y, "y", (M, D), BF16)
+    _shaped(mean, "mean", (M,), F32)
+    _shaped(rstd, "rstd", (M,), F32)
+    _saved(q0, s0_blk, M, D)
+    dev = _device(x, w, b, y, mean, rstd, q0, s0_blk)
+    _call("mx_layer_norm", dev, stream, _ptr(x), _ptr(w), _ptr(b), TYPES[w.dtype], M, D, eps,
+          _ptr(y), _ptr(mean), _ptr(rstd), _ptr(q0), _ptr(s0_blk))
+
+
+def mx_layer_norm_backward(dy, x, q0, s0_blk, w, mean, rstd, dx, dw, db, work, stream=None):
+    """Backward of mx_layer_norm from x, or with x None from (q0, s0_blk); db
+    may be None.  work: mx_layer_norm_backward_work_bytes(M, D) bytes."""
+    _dev_tensor(dy, "dy", dtypes=BF16, ndim=2)
+    M, D = dy.shape
+    if (x is None) == (q0 is None):
+        raise ValueError("give x, or q0 and s0_blk")
+    if x is not None:
+        _shaped(x, "x", (M, D), BF16)
+    _saved(q0, s0_blk, M, D)
+    _shaped(w, "w", (D,), tuple(TYPES))
+    _shaped(mean, "mean", (M,), F32)
+    _shaped(rstd, "rstd", (M,), F32)
+    _shaped(dx, "dx", (M, D), BF16)
+    _shaped(dw, "dw", (D,), (w.dtype,))
+    if db is not None:
+        _shaped(db, "db", (D,), (w.dtype,))
+    _dev_tensor(work, "work", mx_layer_norm_backward_work_bytes(M, D))
+    dev = _device(dy, x, q0, s0_blk, w, mean, rstd, dx, dw, db, work)
+    _call("mx_layer_norm_backward", dev, stream, _ptr(dy), _ptr(x), _ptr(q0), _ptr(s0_blk), _ptr(w),
+          TYPES[w.dtype], _ptr(mean), _ptr(rstd), M, D, _ptr(dx), _ptr(dw), _ptr(db), _ptr(work))
+
+
+def mx_swiglu(gu, h, q0=None, s0_blk=None, stream=None):
+    """Gated SiLU of bf16 gu (M x 2F) into h (M x F); with q0 and s0_blk its
+    input is saved in 8 bits."""
+    _dev_tensor(gu, "gu", dtypes=BF16, ndim=2)
+    M, F2 = gu.shape
+    if F2 % 2:
+        raise ValueError("gu must have an even number of columns, got %d" % F2)
+    _shaped(h, "h", (M, F2 // 2), BF16)
+    _saved(q0, s0_blk, M, F2)
+    _call("mx_swiglu", _device(gu, h, q0, s0_blk), stream, _ptr(gu), M, F2 // 2, _ptr(h), _ptr(q0),
+          _ptr(s0_blk))
+
+
+def mx_swiglu_backward(dh, gu, q0, s0_blk, dgu, stream=None):
+    """Backward of mx_swiglu from gu, or with gu None from (q0, s0_blk)."""
+    _dev_tensor(dh, "dh", dtypes=BF16, ndim=2)
+    M, F = dh.shape
+    if (gu is None) == (q0 is None):
+        raise ValueError("give gu, or q0 and s0_blk")
+    if gu is not None:
+        _shaped(gu, "gu", (M, 2 * F), BF16)
+    _saved(q0, s0_blk, M, 2 * F)
+    _shaped(dgu, "dgu", (M, 2 * F), BF16)
+    _call("mx_swiglu_backward", _device(dh, gu, q0, s0_blk, dgu), stream, _ptr(dh), _ptr(gu),
+          _ptr(q0), _ptr(s0_blk), M, F, _ptr(dgu))
 
 
 def mx_selftest_watchdog(wait_ns=50_000_000, stream=None):
@@ -513,3 +608,73 @@ def matmul(qa, sa_blk, qb, sb_blk, out_dtype=torch.bfloat16, stream=None):
     out = torch.empty((qa.shape[0], qb.shape[0]), dtype=out_dtype, device=qa.device)
     mx_matmul(qa, sa_blk, qb, sb_blk, out, stream)
     return out
+
+
+def layer_norm(x, w, b=None, eps=1e-5, save=False, stream=None):
+    """Layer norm of bf16 x (M, D).  Returns (y, mean, rstd), with save=True
+    (y, mean, rstd, q0, s0_blk): x saved in 8 bits for the backward pass."""
+    M, D = x.shape
+    y = torch.empty((M, D), dtype=torch.bfloat16, device=x.device)
+    mean = torch.empty(M, dtype=torch.float32, device=x.device)
+    rstd = torch.empty(M, dtype=torch.float32, device=x.device)
+    if not save:
+        mx_layer_norm(x, w, b, eps, y, mean, rstd, stream=stream)
+        return y, mean, rstd
+    q0 = torch.empty((M, D), dtype=torch.uint8, device=x.device)
+    s0 = _u8(mx_blocked_bytes(M, D // 32), x.device)
+    mx_layer_norm(x, w, b, eps, y, mean, rstd, q0, s0, stream)
+    return y, mean, rstd, q0, s0
+
+
+def _split_saved(saved):
+    """(tensor, None, None) of a bf16 tensor, (None, q0, s0_blk) of a pair."""
+    return (saved, None, None) if isinstance(saved, torch.Tensor) else (None, *saved)
+
+
+def layer_norm_backward(dy, saved, w, mean, rstd, bias=True, stream=None):
+    """saved: the forward pass's bf16 x, or the pair (q0, s0_blk).  Returns
+    (dx, dw, db), the last two in w's type; db is None with bias=False."""
+    x, q0, s0 = _split_saved(saved)
+    M, D = dy.shape
+    dx = torch.empty((M, D), dtype=torch.bfloat16, device=dy.device)
+    dw = torch.empty(D, dtype=w.dtype, device=dy.device)
+    db = torch.empty(D, dtype=w.dtype, device=dy.device) if bias else None
+    work = _work(mx_layer_norm_backward_work_bytes(M, D), dy.device, stream)
+    mx_layer_norm_backward(dy, x, q0, s0, w, mean, rstd, dx, dw, db, work, stream)
+    return dx, dw, db
+
+
+def _work(n, device, stream):
+    """Scratch that goes back to torch's allocator when the wrapper returns:
+    allocated on the stream that the call runs on, so that its next user runs
+    after the call."""
+    if stream is None or device.type != "cuda":
+        return _u8(n, device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return _u8(n, device)
+
+
+def swiglu(gu, save=False, stream=None):
+    """h = silu(g) u of bf16 gu = [g | u] (M, 2F).  Returns h (M, F), with
+    save=True (h, q0, s0_blk): gu saved in 8 bits for the backward pass."""
+    M, F2 = gu.shape
+    h = torch.empty((M, F2 // 2), dtype=torch.bfloat16, device=gu.device)
+    if not save:
+        mx_swiglu(gu, h, stream=stream)
+        return h
+    q0 = torch.empty((M, F2), dtype=torch.uint8, device=gu.device)
+    s0 = _u8(mx_blocked_bytes(M, F2 // 32), gu.device)
+    mx_swiglu(gu, h, q0, s0, stream)
+    return h, q0, s0
+
+
+def swiglu_backward(dh, saved, stream=None):
+    """saved: the forward pass's bf16 gu, or the pair (q0, s0_blk).  Returns
+    the gradient of gu (M, 2F)."""
+    gu, q0, s0 = _split_saved(saved)
+    M, F = dh.shape
+    dgu = torch.empty((M, 2 * F), dtype=torch.bfloat16, device=dh.device)
+    mx_swiglu_backward(dh, gu, q0, s0, dgu, stream)
+    return dgu

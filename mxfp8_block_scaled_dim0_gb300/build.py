@@ -23,7 +23,7 @@ LIB = os.path.join(PKG, "libmxfp8_cast.so")
 OBJ_DIR_BOUNDS = os.path.join(PKG, "_build_bounds")
 LIB_BOUNDS = os.path.join(PKG, "libmxfp8_cast_bounds.so")
 SOURCES = ["mx_cast.cu", "mx_blocked.cu", "mx_dequant.cu", "mx_scaled.cu", "mx_matmul.cu",
-           "mx_abi.cu"]
+           "mx_norm.cu", "mx_swiglu.cu", "mx_abi.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -237,6 +237,11 @@ int64_t mx_3d_dim0_scale_bytes(int64_t E, int64_t N, int64_t K) {
   return E * mx_blocked_bytes(N, K / 32);
 }
 
+int64_t mx_layer_norm_backward_work_bytes(int64_t M, int64_t D) {
+  if (M < 0 || D < 0) return -1;
+  return mx::norm_back_parts(M) * 8 * D;
+}
+
 const char* mx_strerror(int code) {
   switch (code) {
     case MX_OK: return "ok";
@@ -271,7 +276,8 @@ int mx_watchdog(int clear) {
 int mx_bounds_check(int clear) {
   const int parts[] = {mx::out_of_bounds_cast(clear != 0), mx::out_of_bounds_blocked(clear != 0),
                        mx::out_of_bounds_dequant(clear != 0), mx::out_of_bounds_scaled(clear != 0),
-                       mx::out_of_bounds_matmul(clear != 0)};
+                       mx::out_of_bounds_matmul(clear != 0), mx::out_of_bounds_norm(clear != 0),
+                       mx::out_of_bounds_swiglu(clear != 0)};
   int sum = 0;
   for (int v : parts) {
     if (v == -1) return -1;                     // release build: no checks compiled in
@@ -449,6 +455,72 @@ int mx_matmul(const void* qa, const void* sa_blk, const void* qb, const void* sb
     return rc;
   return launch_rc(mx::launch_matmul(maps, M, N, K, out, out_type == MX_F32, sms,
                                      static_cast<cudaStream_t>(stream)));
+}
+
+int mx_layer_norm(const void* x, const void* w, const void* b, int32_t w_type, int64_t M, int64_t D,
+                  float eps, void* y, float* mean, float* rstd, void* q0, void* s0_blk,
+                  void* stream) {
+  if (!x || !w || !y || !mean || !rstd || !q0 != !s0_blk) return MX_ERR_NULL;
+  if (w_type != MX_BF16 && w_type != MX_F32) return MX_ERR_TYPE;
+  if (M < 1 || D < 1 || M > kMaxDim || D > mx::kNormMaxWidth || (q0 && D % 32 != 0) ||
+      !(eps >= 0.0f))
+    return MX_ERR_SHAPE;
+  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(b, 16) || !aligned(y, 16) ||
+      !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(q0, 16) || !aligned(s0_blk, 16))
+    return MX_ERR_ALIGN;
+  if (int rc = check_device({x, w, b, y, mean, rstd, q0, s0_blk})) return rc;
+  int sms = 0;
+  if (int rc = current_sm_count(&sms)) return rc;
+  const mx::LayerNormArgs a = {x, w, b, w_type == MX_F32, M, D, eps, y, mean, rstd, q0, s0_blk};
+  return launch_rc(mx::launch_layer_norm(a, sms, static_cast<cudaStream_t>(stream)));
+}
+
+int mx_layer_norm_backward(const void* dy, const void* x, const void* q0, const void* s0_blk,
+                           const void* w, int32_t w_type, const float* mean, const float* rstd,
+                           int64_t M, int64_t D, void* dx, void* dw, void* db, void* work,
+                           void* stream) {
+  if (!dy || !w || !mean || !rstd || !dx || !dw || !work) return MX_ERR_NULL;
+  if (!q0 != !s0_blk || !x == !q0) return MX_ERR_NULL;
+  if (w_type != MX_BF16 && w_type != MX_F32) return MX_ERR_TYPE;
+  if (M < 1 || D < 1 || M > kMaxDim || D > mx::kNormMaxWidth || (q0 && D % 32 != 0))
+    return MX_ERR_SHAPE;
+  if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(q0, 16) || !aligned(s0_blk, 16) ||
+      !aligned(w, 16) || !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(dx, 16) ||
+      !aligned(dw, 16) || !aligned(db, 16) || !aligned(work, 16))
+    return MX_ERR_ALIGN;
+  if (int rc = check_device({dy, x, q0, s0_blk, w, mean, rstd, dx, dw, db, work})) return rc;
+  int sms = 0;
+  if (int rc = current_sm_count(&sms)) return rc;
+  const mx::LayerNormBackArgs a = {dy, x, q0, s0_blk, w, w_type == MX_F32, mean, rstd,
+                                   M, D, dx, dw, db, static_cast<float*>(work)};
+  return launch_rc(mx::launch_layer_norm_backward(a, sms, static_cast<cudaStream_t>(stream)));
+}
+
+int mx_swiglu(const void* gu, int64_t M, int64_t F, void* h, void* q0, void* s0_blk,
+              void* stream) {
+  if (!gu || !h || !q0 != !s0_blk) return MX_ERR_NULL;
+  if (M < 1 || F < 1 || M > kMaxDim || F > kMaxDim / 2 || (q0 && F % 32 != 0)) return MX_ERR_SHAPE;
+  if (!aligned(gu, 16) || !aligned(h, 16) || !aligned(q0, 16) || !aligned(s0_blk, 16))
+    return MX_ERR_ALIGN;
+  if (int rc = check_device({gu, h, q0, s0_blk})) return rc;
+  int sms = 0;
+  if (int rc = current_sm_count(&sms)) return rc;
+  const mx::SwigluArgs a = {gu, nullptr, h, q0, s0_blk, M, F};
+  return launch_rc(mx::launch_swiglu(a, sms, static_cast<cudaStream_t>(stream)));
+}
+
+int mx_swiglu_backward(const void* dh, const void* gu, const void* q0, const void* s0_blk,
+                       int64_t M, int64_t F, void* dgu, void* stream) {
+  if (!dh || !dgu || !q0 != !s0_blk || !gu == !q0) return MX_ERR_NULL;
+  if (M < 1 || F < 1 || M > kMaxDim || F > kMaxDim / 2 || (q0 && F % 32 != 0)) return MX_ERR_SHAPE;
+  if (!aligned(dh, 16) || !aligned(gu, 16) || !aligned(q0, 16) || !aligned(s0_blk, 16) ||
+      !aligned(dgu, 16))
+    return MX_ERR_ALIGN;
+  if (int rc = check_device({dh, gu, q0, s0_blk, dgu})) return rc;
+  int sms = 0;
+  if (int rc = current_sm_count(&sms)) return rc;
+  const mx::SwigluArgs a = {gu, dh, dgu, const_cast<void*>(q0), const_cast<void*>(s0_blk), M, F};
+  return launch_rc(mx::launch_swiglu_backward(a, sms, static_cast<cudaStream_t>(stream)));
 }
 
 int mx_scales_to_blocked(const void* s, int64_t R, int64_t C, void* out, void* stream) {

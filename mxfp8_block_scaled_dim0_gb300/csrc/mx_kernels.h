@@ -119,6 +119,56 @@ struct MatmulMaps {
 int launch_matmul(const MatmulMaps& maps, int64_t M, int64_t N, int64_t K, void* out, bool out_f32,
                   int num_sms, cudaStream_t stream);
 int read_matmul_watchdog(int* out, bool clear);
+// Layer norm (mx_norm.cu).  q / s null: the input is not saved; b null: no bias.
+struct LayerNormArgs {
+  const void* x;
+  const void* w;
+  const void* b;
+  bool w_f32;
+  int64_t M, D;
+  float eps;
+  void* y;
+  float* mean;
+  float* rstd;
+  void* q;
+  void* s;
+};
+// x null: the saved input q, s; db null: not wanted.  work: norm_back_parts(M)
+// partial sums of 2 D floats.
+struct LayerNormBackArgs {
+  const void* dy;
+  const void* x;
+  const void* q;
+  const void* s;
+  const void* w;
+  bool w_f32;
+  const float* mean;
+  const float* rstd;
+  int64_t M, D;
+  void* dx;
+  void* dw;
+  void* db;
+  float* work;
+};
+constexpr int64_t kNormMaxParts = 304;
+constexpr int64_t kNormMaxWidth = 16384;
+int64_t norm_back_parts(int64_t M);
+int launch_layer_norm(const LayerNormArgs& a, int num_sms, cudaStream_t stream);
+int launch_layer_norm_backward(const LayerNormBackArgs& a, int num_sms, cudaStream_t stream);
+// Gated SiLU (mx_swiglu.cu).  Forward: gu -> out = h, saved into q, s unless
+// null.  Backward: dh and gu, or q, s -> out = the gradient of gu.
+struct SwigluArgs {
+  const void* gu;
+  const void* dh;
+  void* out;
+  void* q;
+  void* s;
+  int64_t M, F;
+};
+int launch_swiglu(const SwigluArgs& a, int num_sms, cudaStream_t stream);
+int launch_swiglu_backward(const SwigluArgs& a, int num_sms, cudaStream_t stream);
+int out_of_bounds_norm(bool clear);
+int out_of_bounds_swiglu(bool clear);
 int read_watchdog(int* out, bool clear);
 // Stores refused by the bounds-checked build, per translation unit (cleared
 // on request); -1 in a release build.

@@ -34,3 +34,38 @@ def mx_values(q, s_blk):
     R, C = q.shape
     s = scale_values(s_blk.reshape(-1)[blocked_at(R, C // 32, q.device)])
     return (e4m3_values(q).reshape(R, C // 32, 32) * s[..., None]).reshape(R, C)
+
+
+def layer_norm(x, w, b, eps):
+    """(y, mean, rstd) in float64."""
+    x = x.to(F64)
+    mean = x.mean(-1)
+    rstd = ((x - mean[:, None]).square().mean(-1) + eps) ** -0.5
+    y = (x - mean[:, None]) * rstd[:, None] * w.to(F64)
+    return (y if b is None else y + b.to(F64)), mean, rstd
+
+
+def layer_norm_backward(dy, x, w, mean, rstd):
+    """(dx, dw, db) in float64, and the sums of magnitudes that bound the
+    rounding errors of each."""
+    dy, x, w = dy.to(F64), x.to(F64), w.to(F64)
+    mean, rstd = mean.to(F64)[:, None], rstd.to(F64)[:, None]
+    xh = (x - mean) * rstd
+    g = dy * w
+    c1, c2 = g.mean(-1, keepdim=True), (g * xh).mean(-1, keepdim=True)
+    dx = rstd * (g - c1 - xh * c2)
+    size = rstd * (g.abs() + g.abs().mean(-1, keepdim=True)
+                   + xh.abs() * (g * xh).abs().mean(-1, keepdim=True))
+    return (dx, (dy * xh).sum(0), dy.sum(0)), (size, (dy * xh).abs().sum(0), dy.abs().sum(0))
+
+
+def swiglu(gu):
+    g, u = gu.to(F64).chunk(2, -1)
+    return g / (1 + torch.exp(-g)) * u
+
+
+def swiglu_backward(dh, gu):
+    g, u = gu.to(F64).chunk(2, -1)
+    dh = dh.to(F64)
+    sg = 1 / (1 + torch.exp(-g))
+    return torch.cat([dh * u * sg * (1 + g * (1 - sg)), dh * g * sg], -1)

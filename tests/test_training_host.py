@@ -25,3 +25,48 @@ def test_matmul_refuses(lib):
         assert call(**bad) == mx.MX_ERR_SHAPE
     assert call(t=2) == mx.MX_ERR_TYPE and call(t=-1) == mx.MX_ERR_TYPE
     assert lib.mx_strerror(mx.MX_ERR_TYPE) != lib.mx_strerror(-99)
+
+
+def test_layer_norm_refuses(lib):
+    def call(x=A, w=A, b=A, t=1, M=8, D=64, eps=1e-5, y=A, mean=A, rstd=A, q=A, s=A):
+        return lib.mx_layer_norm(x, w, b, t, M, D, eps, y, mean, rstd, q, s, None)
+    for name in ("x", "w", "y", "mean", "rstd", "q", "s"):
+        assert call(**{name: None}) == mx.MX_ERR_NULL
+    for name in ("x", "w", "b", "y", "q", "s"):
+        assert call(**{name: B}) == mx.MX_ERR_ALIGN
+    assert call(mean=A + 2) == mx.MX_ERR_ALIGN
+    for bad in (dict(M=0), dict(D=0), dict(M=-5), dict(D=48), dict(D=16385), dict(M=1 << 31),
+                dict(eps=-1.0), dict(eps=float("nan")), dict(D=16400, q=None, s=None)):
+        assert call(**bad) == mx.MX_ERR_SHAPE
+    assert call(t=2) == mx.MX_ERR_TYPE
+
+
+def test_layer_norm_backward_refuses(lib):
+    def call(dy=A, x=None, q=A, s=A, w=A, t=0, mean=A, rstd=A, M=8, D=64, dx=A, dw=A, db=A, work=A):
+        return lib.mx_layer_norm_backward(dy, x, q, s, w, t, mean, rstd, M, D, dx, dw, db, work, None)
+    for name in ("dy", "q", "s", "w", "mean", "rstd", "dx", "dw", "work"):
+        assert call(**{name: None}) == mx.MX_ERR_NULL
+    assert call(q=None, s=None) == mx.MX_ERR_NULL      # no input at all
+    assert call(x=A) == mx.MX_ERR_NULL                 # two inputs
+    for name in ("dy", "q", "s", "w", "dx", "dw", "db", "work"):
+        assert call(**{name: B}) == mx.MX_ERR_ALIGN
+    for bad in (dict(M=0), dict(D=0), dict(D=48), dict(D=16416), dict(M=1 << 31)):
+        assert call(**bad) == mx.MX_ERR_SHAPE
+    assert call(t=7) == mx.MX_ERR_TYPE
+    assert mx.mx_layer_norm_backward_work_bytes(1, 8) == 64
+    assert mx.mx_layer_norm_backward_work_bytes(-1, 8) == -1
+
+
+def test_swiglu_refuses(lib):
+    def fwd(gu=A, M=8, F=64, h=A, q=A, s=A):
+        return lib.mx_swiglu(gu, M, F, h, q, s, None)
+
+    def back(dh=A, gu=None, q=A, s=A, M=8, F=64, out=A):
+        return lib.mx_swiglu_backward(dh, gu, q, s, M, F, out, None)
+    for name in ("gu", "h", "q", "s"):
+        assert fwd(**{name: None}) == mx.MX_ERR_NULL and fwd(**{name: B}) == mx.MX_ERR_ALIGN
+    for name in ("dh", "q", "s", "out"):
+        assert back(**{name: None}) == mx.MX_ERR_NULL and back(**{name: B}) == mx.MX_ERR_ALIGN
+    assert back(gu=A) == mx.MX_ERR_NULL and back(q=None, s=None) == mx.MX_ERR_NULL
+    for bad in (dict(M=0), dict(F=0), dict(F=48), dict(M=1 << 31), dict(F=1 << 30)):
+        assert fwd(**bad) == mx.MX_ERR_SHAPE and back(**bad) == mx.MX_ERR_SHAPE

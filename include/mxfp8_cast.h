@@ -64,13 +64,19 @@ enum {
   MX_ERR_CUDA = -4,    /* a CUDA call failed (see mx_last_cuda_error) */
   MX_ERR_GROUPS = -5,  /* invalid group count, or (device status) invalid offsets */
   MX_ERR_DEVICE = -6,  /* a pointer is not device memory of the current device */
-  MX_ERR_TYPE = -7     /* an element type argument is none of MX_BF16, MX_F32 */
+  MX_ERR_TYPE = -7     /* a type or order argument has none of its values */
 };
 
 /* Element types of arguments that may have either. */
 enum {
   MX_BF16 = 0,
   MX_F32 = 1
+};
+
+/* Storage orders of mx_matmul's operands. */
+enum {
+  MX_A_BY_COLUMN = 1,  /* qa is stored K x M */
+  MX_B_BY_COLUMN = 2   /* qb is stored K x N */
 };
 
 /* Fused dim0 + dim1 cast with both scale sets in blocked layout; one read of
@@ -263,12 +269,15 @@ int mx_cast_rowwise(const void* x, int64_t M, int64_t K, void* q, void* scale, v
  *   qb      N x K bytes, e4m3                               [in]
  *   sb_blk  mx_blocked_bytes(N, K/32) bytes, e8m0           [in]
  *   M, N    >= 1 (any); K % 32 == 0, K >= 32; all <= 2^31 - 256
+ *   orders  0, or MX_A_BY_COLUMN, MX_B_BY_COLUMN or both: that operand's bytes
+ *           are stored transposed (K x M, K x N; M, N then a multiple of 16),
+ *           its scales as always by row and 32 contraction steps
  *   out     M x N values of out_type (MX_BF16 or MX_F32)    [out]
  * A NaN scale (0xFF) or element makes the results that use it NaN; sums
  * beyond the output type's range give infinity.  A call gives the same bits
  * every time. */
 int mx_matmul(const void* qa, const void* sa_blk, const void* qb, const void* sb_blk, int64_t M,
-              int64_t N, int64_t K, void* out, int32_t out_type, void* stream);
+              int64_t N, int64_t K, int32_t orders, void* out, int32_t out_type, void* stream);
 
 /* Layer norm of bf16 rows, with its input saved in 8 bits for the backward
  * pass.  The pages have no counterpart: the casts' formats put to use for what

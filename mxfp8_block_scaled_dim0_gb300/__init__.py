@@ -79,7 +79,7 @@ def _lib():
             "mx_dequant_blocked": ([P, I64, I64, P, P, P], ctypes.c_int),
             "mx_cast_tensorwise": ([P, I64, P, P, P, P], ctypes.c_int),
             "mx_cast_rowwise": ([P, I64, I64, P, P, P], ctypes.c_int),
-            "mx_matmul": ([P, P, P, P, I64, I64, I64, P, I32, P], ctypes.c_int),
+            "mx_matmul": ([P, P, P, P, I64, I64, I64, I32, P, I32, P], ctypes.c_int),
             "mx_layer_norm": ([P, P, P, I32, I64, I64, ctypes.c_float, P, P, P, P, P, P],
                               ctypes.c_int),
             "mx_layer_norm_backward": ([P, P, P, P, P, I32, P, P, I64, I64, P, P, P, P, P],
@@ -346,11 +346,20 @@ def mx_cast_rowwise(x, q, scale, stream=None):
     _call("mx_cast_rowwise", _device(x, q, scale), stream, _ptr(x), M, K, _ptr(q), _ptr(scale))
 
 
+def _operand(q, name):
+    """A 2D byte operand that is contiguous, or the transpose of a contiguous
+    matrix: (tensor, whether it is the latter)."""
+    by_column = isinstance(q, torch.Tensor) and q.dim() == 2 and not q.is_contiguous() \
+        and q.t().is_contiguous()
+    _dev_tensor(q.t() if by_column else q, name, dtypes=BYTES, ndim=2)
+    return by_column
+
+
 def mx_matmul(qa, sa_blk, qb, sb_blk, out, stream=None):
     """out (M x N, bf16 or float32) = A B^T of MX operands: qa (M x K) and qb
-    (N x K) bytes with their blocked scales."""
-    _dev_tensor(qa, "qa", dtypes=BYTES, ndim=2)
-    _dev_tensor(qb, "qb", dtypes=BYTES, ndim=2)
+    (N x K) bytes with their blocked scales; either may be the transposed view
+    of a contiguous (K x M, K x N) matrix."""
+    orders = (1 if _operand(qa, "qa") else 0) | (2 if _operand(qb, "qb") else 0)
     M, K = qa.shape
     N = qb.shape[0]
     if qb.shape[1] != K:
@@ -361,7 +370,7 @@ def mx_matmul(qa, sa_blk, qb, sb_blk, out, stream=None):
     if tuple(out.shape) != (M, N):
         raise ValueError("out must have shape %s, got %s" % ((M, N), tuple(out.shape)))
     dev = _device(qa, sa_blk, qb, sb_blk, out)
-    _call("mx_matmul", dev, stream, _ptr(qa), _ptr(sa_blk), _ptr(qb), _ptr(sb_blk), M, N, K,
+    _call("mx_matmul", dev, stream, _ptr(qa), _ptr(sa_blk), _ptr(qb), _ptr(sb_blk), M, N, K, orders,
           _ptr(out), TYPES[out.dtype])
 
 

@@ -426,34 +426,48 @@ int mx_cast_rowwise(const void* x, int64_t M, int64_t K, void* q, void* scale, v
 }
 
 int mx_matmul(const void* qa, const void* sa_blk, const void* qb, const void* sb_blk, int64_t M,
-              int64_t N, int64_t K, void* out, int32_t out_type, void* stream) {
+              int64_t N, int64_t K, int32_t orders, void* out, int32_t out_type, void* stream) {
   if (!qa || !sa_blk || !qb || !sb_blk || !out) return MX_ERR_NULL;
-  if (out_type != MX_BF16 && out_type != MX_F32) return MX_ERR_TYPE;
+  if ((out_type != MX_BF16 && out_type != MX_F32) ||
+      (orders & ~(MX_A_BY_COLUMN | MX_B_BY_COLUMN)) != 0)
+    return MX_ERR_TYPE;
+  const bool a_mn = orders & MX_A_BY_COLUMN, b_mn = orders & MX_B_BY_COLUMN;
   if (M < 1 || N < 1 || K < 32 || K % 32 != 0 || M > kMaxDim || N > kMaxDim || K > kMaxDim)
     return MX_ERR_SHAPE;
+  if ((a_mn && M % 16 != 0) || (b_mn && N % 16 != 0)) return MX_ERR_SHAPE;
   if (!aligned(qa, 16) || !aligned(sa_blk, 16) || !aligned(qb, 16) || !aligned(sb_blk, 16) ||
       !aligned(out, 16))
     return MX_ERR_ALIGN;
   if (int rc = check_device({qa, sa_blk, qb, sb_blk, out})) return rc;
   int sms = 0;
   if (int rc = current_sm_count(&sms)) return rc;
+  const bool f32 = out_type == MX_F32;
+  const bool pairs = mx::matmul_pairs(M, N, f32, sms);
   mx::MatmulMaps maps;
   const int64_t tiles_k = cdiv(K, 128);
-  if (int rc = encode_2d(&maps.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, qa, K, M, K, 128, 128,
-                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
+  auto operand = [&](CUtensorMap* m, const void* q, int64_t rows, bool mn) {
+    return encode_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, q, mn ? rows : K, mn ? K : rows,
+                     mn ? rows : K, 128, 128, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+  };
+  auto scales = [&](CUtensorMap* m, const void* s, int64_t rows, uint32_t box) {
+    return encode_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, s, tiles_k * 128, cdiv(rows, 128),
+                     tiles_k * 512, 128, box, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_NONE);
+  };
+  if (int rc = operand(&maps.a, qa, M, a_mn)) return rc;
+  if (int rc = operand(&maps.b, qb, N, b_mn)) return rc;
+  if (int rc = scales(&maps.sa, sa_blk, M, 1)) return rc;
+  if (int rc = scales(&maps.sb, sb_blk, N, pairs ? 2 : 1)) return rc;
+  if (!pairs) {
+    maps.out = maps.a;
+  } else if (int rc = encode_2d(&maps.out,
+                                f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                    : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                                out, N, M, N * (f32 ? 4 : 2), f32 ? 32 : 64, 32,
+                                CU_TENSOR_MAP_L2_PROMOTION_NONE)) {
     return rc;
-  if (int rc = encode_2d(&maps.b, CU_TENSOR_MAP_DATA_TYPE_UINT8, qb, K, N, K, 128, 128,
-                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
-    return rc;
-  if (int rc = encode_2d(&maps.sa, CU_TENSOR_MAP_DATA_TYPE_UINT32, sa_blk, tiles_k * 128,
-                         cdiv(M, 128), tiles_k * 512, 128, 1, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-                         CU_TENSOR_MAP_SWIZZLE_NONE))
-    return rc;
-  if (int rc = encode_2d(&maps.sb, CU_TENSOR_MAP_DATA_TYPE_UINT32, sb_blk, tiles_k * 128,
-                         cdiv(N, 128), tiles_k * 512, 128, 1, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-                         CU_TENSOR_MAP_SWIZZLE_NONE))
-    return rc;
-  return launch_rc(mx::launch_matmul(maps, M, N, K, out, out_type == MX_F32, sms,
+  }
+  return launch_rc(mx::launch_matmul(maps, M, N, K, a_mn, b_mn, out, f32, sms,
                                      static_cast<cudaStream_t>(stream)));
 }
 

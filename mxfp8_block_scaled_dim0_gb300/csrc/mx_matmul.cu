@@ -13,6 +13,23 @@
 // them out in tensor memory, so scales go from global to shared to tensor
 // memory without a thread touching them.
 //
+// Either operand may instead be stored with its rows contiguous (K x M, K x N
+// bytes; the scales stay along the contraction): the tensor cores read it
+// through an MN-major descriptor.
+//
+// pair_matmul_kernel: persistent CTA pairs, a 256 x 256 tile of C at a time.
+// The pair's two SMs share one MMA (cta_group::2): each loads 128 rows of A and
+// 128 of B for every 128 contraction steps and holds 128 rows of the result,
+// so a byte of shared memory feeds twice the products that one CTA's tile
+// would.  Loads run five stages ahead of the MMAs.  Tensor memory (512 columns)
+// holds two results of 256 columns that overlap in 16, and the scales in the
+// last 16; the eight epilogue warps of a CTA read the overlap first, and the
+// next tile's MMAs begin while they store the rest.  For an fp32 result longer
+// sums are cut into runs of 4096 steps that the epilogue adds up in registers:
+// the tensor core's accumulator cuts bits off at every addition, an error
+// that grows with the run (3.7e-7 in the 2-norm at 4096 steps, 1.5e-6 at
+// 16640); a bf16 result does not notice either.
+//
 // tile_matmul_kernel: one 128 x 128 tile of C per cluster of S CTAs, the
 // contraction cut into S equal runs of 128-step blocks; each CTA leaves its
 // partial tile in its shared memory, and each then sums 128 / S of the tile's
@@ -42,6 +59,9 @@ struct MatmulParams {
   int m_tiles, n_tiles;
   int split;           // CTAs of a cluster along the contraction (tile kernel)
   int out_f32;
+  int a_mn, b_mn;      // operand stored with its rows contiguous
+  int run;             // blocks summed in tensor memory at a time (pair kernel)
+  int band;            // M-tiles of a band (pair kernel)
   Span sp_out;
   int64_t stall_at;
   uint64_t stall_ns;
@@ -110,8 +130,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         uint8_t* st = ring + s * kTileStageBytes;
         const int kb = kb0 + i;
         mbar_arrive_expect_tx(&full[s], kTileStageBytes);
-        tma_load_2d(st, &maps.a, kb * kBK, mt * kTile, &full[s]);
-        tma_load_2d(st + kBoxBytes, &maps.b, kb * kBK, nt * kTile, &full[s]);
+        tma_load_2d(st, &maps.a, p.a_mn ? mt * kTile : kb * kBK, p.a_mn ? kb * kBK : mt * kTile,
+                    &full[s]);
+        tma_load_2d(st + kBoxBytes, &maps.b, p.b_mn ? nt * kTile : kb * kBK,
+                    p.b_mn ? kb * kBK : nt * kTile, &full[s]);
         tma_load_2d(st + 2 * kBoxBytes, &maps.sa, kb * 128, mt, &full[s]);
         tma_load_2d(st + 2 * kBoxBytes + kSfBytes, &maps.sb, kb * 128, nt, &full[s]);
       }
@@ -122,7 +144,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
   } else if (warp == 1) {
     if (lane == 0) {
-      const uint32_t idesc = mxf8_idesc(128, 128);
+      const uint32_t idesc = mxf8_idesc(128, 128, p.a_mn, p.b_mn);
+      const uint32_t step_a = p.a_mn ? kStepMN : kStepK, step_b = p.b_mn ? kStepMN : kStepK;
       for (int i = 0; i < nkb; ++i) {
         const int s = i % kTileStages;
         if (!mbar_wait(&full[s], static_cast<uint32_t>((i / kTileStages) & 1), &abort_flag)) break;
@@ -130,10 +153,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const uint32_t st = smem_u32(ring + s * kTileStageBytes);
         tcgen05_cp_scales<1>(t_sfa, scale_desc(st + 2 * kBoxBytes));
         tcgen05_cp_scales<1>(t_sfb, scale_desc(st + 2 * kBoxBytes + kSfBytes));
-        const uint64_t da = kmajor_desc(st), db = kmajor_desc(st + kBoxBytes);
+        const uint64_t da = operand_desc(st), db = operand_desc(st + kBoxBytes);
         const int steps = kb0 + i == p.k_blocks - 1 ? p.last_steps : 4;
         for (int k = 0; k < steps; ++k)
-          mma_mxf8<1>(tmem, da + 2 * k, db + 2 * k, mxf8_idesc_step(idesc, k), t_sfa, t_sfb,
+          mma_mxf8<1>(tmem, da + step_a * k, db + step_b * k, mxf8_idesc_step(idesc, k), t_sfa, t_sfb,
                       i + k > 0);
         tcgen05_commit<1>(&empty[s]);
       }
@@ -195,11 +218,294 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (threadIdx.x == 0 && !ok) atomicOr(&g_matmul_watchdog, 1);
 }
 
+// ---- CTA pairs -------------------------------------------------------------------
+
+constexpr int kPairStages = 5;
+constexpr int kPairStageBytes = 2 * kBoxBytes + 3 * kSfBytes;
+constexpr int kPairStrideBytes = 34 * 1024;   // 1024-byte aligned boxes
+constexpr int kPairThreads = 320;             // loads, MMA, eight epilogue warps
+constexpr int kBufCols = 240;                 // second result's first column
+constexpr int kStageOut = 4096;               // bytes an epilogue warp stages
+constexpr int kPairSmem = kPairStages * kPairStrideBytes + 8 * kStageOut + 1024;
+constexpr uint32_t kSfaCol = 496, kSfbCol = 500;
+
+struct Tiles {
+  int m_tiles, n_tiles, band;
+  // Bands of `band` M-tiles, walked along N, M fastest inside a band.
+  __device__ __forceinline__ void at(int t, int& mt, int& nt) const {
+    const int per = band * n_tiles;
+    const int b = t / per, i = t - b * per;
+    const int rows = min(band, m_tiles - b * band);
+    nt = i / rows;
+    mt = b * band + (i - nt * rows);
+  }
+};
+
+__global__ void __launch_bounds__(kPairThreads, 1)
+    pair_matmul_kernel(const __grid_constant__ MatmulMaps maps, const MatmulParams p) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full[kPairStages], empty[kPairStages], ready[2], drained, done,
+      stall_bar;
+  __shared__ uint32_t tmem_base;
+  __shared__ int abort_flag, issued;
+  uint8_t* ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  uint8_t* stage_out = ring + kPairStages * kPairStrideBytes;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_rank());
+  const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
+  const int n_tiles = p.m_tiles * p.n_tiles;
+  const Tiles tiles{p.m_tiles, p.n_tiles, p.band};
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kPairStages; ++s) {
+      mbar_init(&full[s], 2);                 // both CTAs' loads, in the leader
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(&ready[0], 1);
+    mbar_init(&ready[1], 1);
+    mbar_init(&drained, 16);                  // the epilogue warps of both, in the leader
+    mbar_init(&done, 1);
+    mbar_init(&stall_bar, 1);
+    abort_flag = 0;
+    issued = 0;
+    fence_mbar_init();
+    prefetch_tmap(&maps.a);
+    prefetch_tmap(&maps.b);
+    prefetch_tmap(&maps.sa);
+    prefetch_tmap(&maps.sb);
+    prefetch_tmap(&maps.out);
+  }
+  if (warp == 1) tmem_alloc<2>(&tmem_base, 512);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  tcgen05_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tcgen05_fence_after();
+  const uint32_t tmem = tmem_base;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int i = 0;
+      bool ok = true;
+      for (int t = first; ok && t < n_tiles; t += stride) {
+        int mt, nt;
+        tiles.at(t, mt, nt);
+        const int m = (2 * mt + rank) * kTile, n = (2 * nt + rank) * kTile;
+        for (int kb = 0; kb < p.k_blocks; ++kb, ++i) {
+          const int s = i % kPairStages;
+          if (kDiagStall && blockIdx.x == 0 && i == p.stall_at) {
+            mbar_wait(&stall_bar, 0u, &abort_flag, p.stall_ns);
+            ok = false;
+            break;
+          }
+          if (i >= kPairStages &&
+              !mbar_wait(&empty[s], static_cast<uint32_t>((i / kPairStages - 1) & 1), &abort_flag)) {
+            ok = false;
+            break;
+          }
+          uint8_t* st = ring + s * kPairStrideBytes;
+          const uint32_t bar = map_to_rank(smem_u32(&full[s]), 0);
+          mbar_arrive_expect_tx_remote(bar, kPairStageBytes);
+          tma_load_2d_pair(st, &maps.a, p.a_mn ? m : kb * kBK, p.a_mn ? kb * kBK : m, bar);
+          tma_load_2d_pair(st + kBoxBytes, &maps.b, p.b_mn ? n : kb * kBK, p.b_mn ? kb * kBK : n,
+                           bar);
+          tma_load_2d_pair(st + 2 * kBoxBytes, &maps.sa, kb * 128, 2 * mt + rank, bar);
+          tma_load_2d_pair(st + 2 * kBoxBytes + kSfBytes, &maps.sb, kb * 128, 2 * nt, bar);
+        }
+      }
+      issued = i;
+    }
+  } else if (warp == 1) {
+    if (rank == 0 && lane == 0) {
+      const uint32_t idesc = mxf8_idesc(256, 256, p.a_mn, p.b_mn);
+      const uint32_t step_a = p.a_mn ? kStepMN : kStepK, step_b = p.b_mn ? kStepMN : kStepK;
+      int i = 0, item = 0;
+      bool ok = true;
+      for (int t = first; ok && t < n_tiles; t += stride) {
+        for (int k0 = 0; ok && k0 < p.k_blocks; k0 += p.run, ++item) {
+          if (item > 0 && !mbar_wait_cluster(&drained, static_cast<uint32_t>((item - 1) & 1), &abort_flag)) {
+            ok = false;
+            break;
+          }
+          tcgen05_fence_after();
+          const uint32_t d = tmem + ((item & 1) ? kBufCols : 0);
+          const int k1 = min(k0 + p.run, p.k_blocks);
+          for (int kb = k0; kb < k1; ++kb, ++i) {
+            const int s = i % kPairStages;
+            if (!mbar_wait_cluster(&full[s], static_cast<uint32_t>((i / kPairStages) & 1), &abort_flag)) {
+              ok = false;
+              break;
+            }
+            tcgen05_fence_after();
+            const uint32_t st = smem_u32(ring + s * kPairStrideBytes);
+            tcgen05_cp_scales<2>(tmem + kSfaCol, scale_desc(st + 2 * kBoxBytes));
+            tcgen05_cp_scales<2>(tmem + kSfbCol, scale_desc(st + 2 * kBoxBytes + kSfBytes));
+            tcgen05_cp_scales<2>(tmem + kSfbCol + 4, scale_desc(st + 2 * kBoxBytes + 2 * kSfBytes));
+            const uint64_t da = operand_desc(st), db = operand_desc(st + kBoxBytes);
+            const int steps = kb == p.k_blocks - 1 ? p.last_steps : 4;
+            for (int k = 0; k < steps; ++k)
+              mma_mxf8<2>(d, da + step_a * k, db + step_b * k, mxf8_idesc_step(idesc, k),
+                          tmem + kSfaCol, tmem + kSfbCol, kb > k0 || k > 0);
+            tcgen05_commit<2>(&empty[s]);
+          }
+          if (ok) tcgen05_commit<2>(&ready[item & 1]);
+        }
+      }
+      tcgen05_commit<2>(&done);
+      mbar_drain(&done, 0u, kWaitLimitNs);     // every MMA issued has finished
+    }
+  } else {
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    uint8_t* so = stage_out + (warp - 2) * kStageOut;
+    const uint32_t drained_bar = map_to_rank(smem_u32(&drained), 0);
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    float v[128];
+    int item = 0;
+    bool ok = true;
+    for (int t = first; ok && t < n_tiles; t += stride) {
+      int mt, nt;
+      tiles.at(t, mt, nt);
+      for (int k0 = 0; k0 < p.k_blocks; k0 += p.run, ++item) {
+        if (!mbar_wait(&ready[item & 1], static_cast<uint32_t>((item >> 1) & 1), &abort_flag)) {
+          ok = false;
+          break;
+        }
+        tcgen05_fence_after();
+        const uint32_t at = tmem + lanes + ((item & 1) ? kBufCols : 0) + half * 128;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          // Chunks 0 and 7 hold the overlap: first.
+          const int c = j == 0 ? 0 : j == 1 ? 7 : j - 1;
+          uint32_t w[16];
+          tmem_ld_16(at + 16 * c, w);
+          tmem_ld_wait();
+          if (j == 1) {
+            tcgen05_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(drained_bar);
+          }
+          if (k0 == 0) {
+#pragma unroll
+            for (int x = 0; x < 16; ++x) v[16 * c + x] = __uint_as_float(w[x]);
+          } else {
+#pragma unroll
+            for (int x = 0; x < 16; ++x) v[16 * c + x] += __uint_as_float(w[x]);
+          }
+        }
+      }
+      if (!ok) break;
+      // 32 rows x 128 columns through shared memory, 128 bytes of a row at a
+      // time, in the swizzled order the tensor map expects.
+      const int m = (2 * mt + rank) * kTile + quarter * 32;
+      const int n = 2 * nt * kTile + half * 128;
+      if (m >= p.M || n >= p.N) continue;
+      uint8_t* row = so + lane * 128;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        if (!p.out_f32 && x >= 2) break;
+        if (lane == 0) bulk_wait_read<0>();
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          uint4 o;
+          if (p.out_f32) {
+            o = make_uint4(__float_as_uint(v[32 * x + 4 * j]), __float_as_uint(v[32 * x + 4 * j + 1]),
+                           __float_as_uint(v[32 * x + 4 * j + 2]),
+                           __float_as_uint(v[32 * x + 4 * j + 3]));
+          } else {
+            const int b = 64 * (x & 1) + 8 * j;
+            o = make_uint4(bf16x2(v[b], v[b + 1]), bf16x2(v[b + 2], v[b + 3]),
+                           bf16x2(v[b + 4], v[b + 5]), bf16x2(v[b + 6], v[b + 7]));
+          }
+          *reinterpret_cast<uint4*>(row + ((j ^ (lane & 7)) << 4)) = o;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          const int c = n + x * (p.out_f32 ? 32 : 64);
+          if (c < p.N) tma_store_2d(&maps.out, c, m, so);
+          bulk_commit();
+        }
+      }
+    }
+    if (lane == 0) bulk_wait<0>();
+    tcgen05_fence_before();
+  }
+  __syncwarp();
+  __syncthreads();
+  cluster_sync();
+  // Gave up in either CTA: in the leader, make up the arrivals of stages that
+  // only one CTA loaded, so that what is in flight can be waited for.
+  const int peer_abort = ld_cluster_s32(map_to_rank(smem_u32(&abort_flag), rank ^ 1));
+  const bool failed = abort_flag != 0 || peer_abort != 0;
+  if (failed) {
+    if (rank == 0 && threadIdx.x == 0) {
+      const int other = ld_cluster_s32(map_to_rank(smem_u32(&issued), 1));
+      const int lo = min(issued, other), hi = max(issued, other);
+      for (int j = lo; j < hi; ++j) mbar_arrive(&full[j % kPairStages]);
+      for (int j = max(0, hi - kPairStages); j < hi; ++j)
+        mbar_drain(&full[j % kPairStages], static_cast<uint32_t>((j / kPairStages) & 1),
+                   100000000ull);
+    }
+    __syncthreads();
+  }
+  cluster_sync();
+  tcgen05_fence_after();
+  if (warp == 1) tmem_dealloc<2>(tmem, 512);
+  if (threadIdx.x == 0 && failed) atomicOr(&g_matmul_watchdog, 1);
+}
+
+// The pair kernel takes outputs that a tensor map can describe, of enough
+// 256 x 256 tiles to keep the GPU's pairs busy.
+bool use_pairs(int64_t M, int64_t N, bool out_f32, int num_sms) {
+  if ((N * (out_f32 ? 4 : 2)) % 16 != 0) return false;
+  const int64_t tiles = ((M + 255) / 256) * ((N + 255) / 256);
+  return tiles * 4 >= num_sms;
+}
+
 }  // namespace
 
-int launch_matmul(const MatmulMaps& maps, int64_t M, int64_t N, int64_t K, void* out, bool out_f32,
-                  int num_sms, cudaStream_t stream) {
+bool matmul_pairs(int64_t M, int64_t N, bool out_f32, int num_sms) {
+  return use_pairs(M, N, out_f32, num_sms);
+}
+
+static int launch_pairs(const MatmulMaps& maps, MatmulParams p, int num_sms, cudaStream_t stream) {
+  p.m_tiles = static_cast<int>((p.M + 255) / 256);
+  p.n_tiles = static_cast<int>((p.N + 255) / 256);
+  p.run = p.out_f32 ? 32 : p.k_blocks;
+  p.band = 8;
+  static DeviceCache attr_cache;
+  const int attr = attr_cache.get([] {
+    return static_cast<int>(cudaFuncSetAttribute(
+        pair_matmul_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem));
+  });
+  if (attr != 0) return attr;
+  const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
+  const int64_t pairs = tiles < num_sms / 2 ? tiles : num_sms / 2;
+  if (tiles > 0x3fffffff) return static_cast<int>(cudaErrorInvalidConfiguration);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
+  cfg.blockDim = dim3(kPairThreads);
+  cfg.dynamicSmemBytes = kPairSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = 2;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  return static_cast<int>(cudaLaunchKernelEx(&cfg, pair_matmul_kernel, maps, p));
+}
+
+int launch_matmul(const MatmulMaps& maps, int64_t M, int64_t N, int64_t K, bool a_mn,
+                  bool b_mn, void* out, bool out_f32, int num_sms, cudaStream_t stream) {
   MatmulParams p = {};
+  p.a_mn = a_mn;
+  p.b_mn = b_mn;
   p.out = out;
   p.M = M;
   p.N = N;
@@ -210,6 +516,7 @@ int launch_matmul(const MatmulMaps& maps, int64_t M, int64_t N, int64_t K, void*
   const Stall stall = take_stall();
   p.stall_at = stall.at;
   p.stall_ns = stall.ns;
+  if (use_pairs(M, N, out_f32, num_sms)) return launch_pairs(maps, p, num_sms, stream);
   p.m_tiles = static_cast<int>((M + kTile - 1) / kTile);
   p.n_tiles = static_cast<int>((N + kTile - 1) / kTile);
   const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles;

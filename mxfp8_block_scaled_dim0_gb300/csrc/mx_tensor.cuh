@@ -35,6 +35,63 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   return v;
 }
 
+// Arrivals on a barrier of another CTA of the cluster (`bar` from map_to_rank).
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive_expect_tx_remote(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar),
+               "r"(bytes)
+               : "memory");
+}
+
+// mbar_wait for a barrier on which another CTA of the cluster arrives.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity,
+                                                  volatile int* abort_flag) {
+  if (mbar_try_wait_cluster(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+      if (mbar_try_wait_cluster(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      *abort_flag = 1;
+      return false;
+    }
+  }
+}
+
+__device__ __forceinline__ int ld_cluster_s32(uint32_t addr) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// Tile load of a CTA pair: into this CTA's shared memory, completing on the
+// barrier `bar` (a cluster address) of either CTA of the pair.
+__device__ __forceinline__ void tma_load_2d_pair(void* smem_dst, const CUtensorMap* m, int32_t x,
+                                                 int32_t y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+
 // ---- tensor memory -------------------------------------------------------------
 
 // A whole warp allocates / frees `cols` columns (a power of two, 32..512) of
@@ -88,16 +145,31 @@ __device__ __forceinline__ void tmem_ld_32(uint32_t addr, uint32_t (&v)[32]) {
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld_16(uint32_t addr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+        "=r"(v[14]), "=r"(v[15])
+      : "r"(addr)
+      : "memory");
+}
+
 __device__ __forceinline__ void tmem_ld_wait() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
 // ---- descriptors ---------------------------------------------------------------
 
-// Shared-memory matrix descriptor of a K-major operand box: rows of 128 bytes,
-// 128-byte swizzle, groups of eight rows 1024 bytes apart.  `addr` is 1024-byte
-// aligned, or that plus 32 k bytes for the k-th 32-step slice.
-__device__ __forceinline__ uint64_t kmajor_desc(uint32_t addr) {
+// Shared-memory matrix descriptor of an operand box of 128 x 128 bytes: rows of
+// 128 bytes, 128-byte swizzle, groups of eight rows 1024 bytes apart; the rows
+// run along the operand's rows (K-major) or along the contraction (MN-major).
+// `addr` is 1024-byte aligned; the k-th 32-step slice starts 32 k bytes later
+// (K-major) or 32 k rows later (MN-major): kStepK and kStepMN in the
+// descriptor's units of 16 bytes.
+constexpr uint32_t kStepK = 32 >> 4, kStepMN = 32 * 128 >> 4;
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
   return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (uint64_t{1024 >> 4} << 32) |
          (uint64_t{1} << 46) | (uint64_t{2} << 61);
 }
@@ -110,9 +182,10 @@ __device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
 }
 
 // Instruction descriptor of a kind::mxf8f6f4 product of shape m x n: both
-// operands e4m3 and K-major, scales ue8m0.
-__device__ __forceinline__ constexpr uint32_t mxf8_idesc(int m, int n) {
-  return (static_cast<uint32_t>(n >> 3) << 17) | (1u << 23) | (static_cast<uint32_t>(m >> 4) << 24);
+// operands e4m3, each K-major or MN-major, scales ue8m0.
+__device__ __forceinline__ uint32_t mxf8_idesc(int m, int n, bool a_mn, bool b_mn) {
+  return (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
+         (1u << 23) | (static_cast<uint32_t>(m >> 4) << 24);
 }
 
 // The same with byte `k` of each 32-bit scale word (the k-th of four 32-step

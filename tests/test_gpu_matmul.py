@@ -82,10 +82,26 @@ def test_matches_64_bits(M, N, K, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=["bf16", "f32"])
-@pytest.mark.parametrize("M,N,K", [(32, 32, 16640), (4096, 2304, 160), (3000, 5000, 4192)])
+@pytest.mark.parametrize("M,N,K", [(32, 32, 16640), (4096, 2304, 160), (3000, 5000, 4192),
+                                   (2304, 4352, 8224)])
 def test_long_and_wide(M, N, K, dtype):
     a, b = operand(M, K, K), operand(N, K, K + 1)
     check(a, b, product(a, b, dtype))
+
+
+@pytest.mark.parametrize("by_column", ["a", "b", "ab"])
+@pytest.mark.parametrize("M,N,K", [(16, 16, 32), (144, 272, 96), (128, 1040, 544), (2064, 2320, 352),
+                                   (16, 5120, 2080)])
+def test_operands_stored_by_column(M, N, K, by_column):
+    a, b = operand(M, K, M + N + K), operand(N, K, M + N + K + 1)
+    want = product(a, b, torch.float32)
+    if "a" in by_column:
+        a = (a[0].t().contiguous().t(), a[1])
+    if "b" in by_column:
+        b = (b[0].t().contiguous().t(), b[1])
+    got = product(a, b, torch.float32)
+    check(a, b, got)
+    assert torch.equal(got, want)
 
 
 def test_long_sum_of_equal_terms():
@@ -213,7 +229,7 @@ def test_refusals():
     with pytest.raises(TypeError, match="out"):
         mx.mx_matmul(*a, *b, out.half())
     with pytest.raises(ValueError, match="contiguous"):
-        mx.mx_matmul(a[0].t().contiguous().t(), a[1], *b, out)
+        mx.mx_matmul(torch.zeros((64, 128), dtype=torch.uint8, device="cuda")[:, :64], a[1], *b, out)
     with pytest.raises(ValueError, match="sb_blk holds"):
         mx.mx_matmul(*a, b[0], b[1][:100], out)
     with pytest.raises(ValueError, match="CUDA"):

@@ -15,15 +15,17 @@ def lib():
 
 
 def test_matmul_refuses(lib):
-    def call(qa=A, sa=A, qb=A, sb=A, M=64, N=64, K=64, out=A, t=0):
-        return lib.mx_matmul(qa, sa, qb, sb, M, N, K, out, t, None)
+    def call(qa=A, sa=A, qb=A, sb=A, M=64, N=64, K=64, orders=0, out=A, t=0):
+        return lib.mx_matmul(qa, sa, qb, sb, M, N, K, orders, out, t, None)
     for name in ("qa", "sa", "qb", "sb", "out"):
         assert call(**{name: None}) == mx.MX_ERR_NULL
         assert call(**{name: B}) == mx.MX_ERR_ALIGN
     for bad in (dict(M=0), dict(N=0), dict(N=-1), dict(K=0), dict(K=48), dict(K=-32),
                 dict(M=1 << 31), dict(N=1 << 31), dict(K=1 << 31)):
         assert call(**bad) == mx.MX_ERR_SHAPE
-    assert call(t=2) == mx.MX_ERR_TYPE and call(t=-1) == mx.MX_ERR_TYPE
+    assert call(orders=1, M=40) == mx.MX_ERR_SHAPE and call(orders=2, N=24) == mx.MX_ERR_SHAPE
+    for bad in (dict(t=2), dict(t=-1), dict(orders=4), dict(orders=-1)):
+        assert call(**bad) == mx.MX_ERR_TYPE
     assert lib.mx_strerror(mx.MX_ERR_TYPE) != lib.mx_strerror(-99)
 
 

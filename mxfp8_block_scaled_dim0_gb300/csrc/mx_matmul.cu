@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const uint32_t t_sfa = tmem + 128, t_sfb = tmem + 132;
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       int i = 0;
       for (; i < nkb; ++i) {
         const int s = i % kTileStages;
@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           mbar_drain(&full[j % kTileStages], static_cast<uint32_t>((j / kTileStages) & 1));
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (elect_one()) {
       const uint32_t idesc = mxf8_idesc(128, 128, p.a_mn, p.b_mn);
       const uint32_t step_a = p.a_mn ? kStepMN : kStepK, step_b = p.b_mn ? kStepMN : kStepK;
       for (int i = 0; i < nkb; ++i) {
@@ -155,9 +155,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         tcgen05_cp_scales<1>(t_sfb, scale_desc(st + 2 * kBoxBytes + kSfBytes));
         const uint64_t da = operand_desc(st), db = operand_desc(st + kBoxBytes);
         const int steps = kb0 + i == p.k_blocks - 1 ? p.last_steps : 4;
-        for (int k = 0; k < steps; ++k)
-          mma_mxf8<1>(tmem, da + step_a * k, db + step_b * k, mxf8_idesc_step(idesc, k), t_sfa, t_sfb,
-                      i + k > 0);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (k < steps)
+            mma_mxf8<1>(tmem, da + step_a * k, db + step_b * k, mxf8_idesc_step(idesc, k), t_sfa,
+                        t_sfb, i + k > 0);
         tcgen05_commit<1>(&empty[s]);
       }
       tcgen05_commit<1>(&done);
@@ -259,7 +261,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kPairStages; ++s) {
-      mbar_init(&full[s], 2);                 // both CTAs' loads, in the leader
+      mbar_init(&full[s], 1);                 // in the leader, for both CTAs' loads
       mbar_init(&empty[s], 1);
     }
     mbar_init(&ready[0], 1);
@@ -285,7 +287,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   const uint32_t tmem = tmem_base;
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       int i = 0;
       bool ok = true;
       for (int t = first; ok && t < n_tiles; t += stride) {
@@ -306,7 +308,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           }
           uint8_t* st = ring + s * kPairStrideBytes;
           const uint32_t bar = map_to_rank(smem_u32(&full[s]), 0);
-          mbar_arrive_expect_tx_remote(bar, kPairStageBytes);
+          // The leader alone announces both CTAs' bytes: a remote arrival per
+          // stage, with its release over the cluster, took as long as the
+          // stage's MMAs twice over (969 us against 428 us at 16640 x 8192 x 5120).
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kPairStageBytes);
           tma_load_2d_pair(st, &maps.a, p.a_mn ? m : kb * kBK, p.a_mn ? kb * kBK : m, bar);
           tma_load_2d_pair(st + kBoxBytes, &maps.b, p.b_mn ? n : kb * kBK, p.b_mn ? kb * kBK : n,
                            bar);
@@ -317,7 +322,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       issued = i;
     }
   } else if (warp == 1) {
-    if (rank == 0 && lane == 0) {
+    if (rank == 0 && elect_one()) {
       const uint32_t idesc = mxf8_idesc(256, 256, p.a_mn, p.b_mn);
       const uint32_t step_a = p.a_mn ? kStepMN : kStepK, step_b = p.b_mn ? kStepMN : kStepK;
       int i = 0, item = 0;
@@ -344,9 +349,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             tcgen05_cp_scales<2>(tmem + kSfbCol + 4, scale_desc(st + 2 * kBoxBytes + 2 * kSfBytes));
             const uint64_t da = operand_desc(st), db = operand_desc(st + kBoxBytes);
             const int steps = kb == p.k_blocks - 1 ? p.last_steps : 4;
-            for (int k = 0; k < steps; ++k)
-              mma_mxf8<2>(d, da + step_a * k, db + step_b * k, mxf8_idesc_step(idesc, k),
-                          tmem + kSfaCol, tmem + kSfbCol, kb > k0 || k > 0);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (k < steps)
+                mma_mxf8<2>(d, da + step_a * k, db + step_b * k, mxf8_idesc_step(idesc, k),
+                            tmem + kSfaCol, tmem + kSfbCol, kb > k0 || k > 0);
             tcgen05_commit<2>(&empty[s]);
           }
           if (ok) tcgen05_commit<2>(&ready[item & 1]);
@@ -435,15 +442,21 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   __syncwarp();
   __syncthreads();
   cluster_sync();
-  // Gave up in either CTA: in the leader, make up the arrivals of stages that
-  // only one CTA loaded, so that what is in flight can be waited for.
+  // Gave up in either CTA: in the leader, settle the stages that only one CTA
+  // loaded (bytes announced for the peer that will not come; the peer's bytes
+  // that were not announced), so that what is in flight can be waited for.
   const int peer_abort = ld_cluster_s32(map_to_rank(smem_u32(&abort_flag), rank ^ 1));
   const bool failed = abort_flag != 0 || peer_abort != 0;
   if (failed) {
     if (rank == 0 && threadIdx.x == 0) {
       const int other = ld_cluster_s32(map_to_rank(smem_u32(&issued), 1));
       const int lo = min(issued, other), hi = max(issued, other);
-      for (int j = lo; j < hi; ++j) mbar_arrive(&full[j % kPairStages]);
+      for (int j = lo; j < hi; ++j) {
+        if (issued > other)
+          mbar_complete_tx(&full[j % kPairStages], kPairStageBytes);
+        else
+          mbar_arrive_expect_tx(&full[j % kPairStages], kPairStageBytes);
+      }
       for (int j = max(0, hi - kPairStages); j < hi; ++j)
         mbar_drain(&full[j % kPairStages], static_cast<uint32_t>((j / kPairStages) & 1),
                    100000000ull);

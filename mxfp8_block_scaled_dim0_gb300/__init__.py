@@ -156,13 +156,14 @@ def _call(name, dev, stream, *args):
     """Call entry point `name` with device index `dev` current (the library
     launches on the current device) and the stream appended: by default the
     current stream of that device."""
-    fn = getattr(_lib(), name)
+    fn = getattr(_LIB or _lib(), name)
     if torch.cuda.current_device() == dev:
-        rc = fn(*args, _stream(stream, dev))
+        rc = fn(*args, _raw_stream(dev) if stream is None else _stream(stream, dev))
     else:
         with torch.cuda.device(dev):
             rc = fn(*args, _stream(stream, dev))
-    _check(rc, name)
+    if rc != MX_OK:
+        raise MXError(rc, name)
 
 
 # dtypes each kind of argument may have.  The C ABI sees only pointers, so
@@ -349,8 +350,10 @@ def mx_cast_rowwise(x, q, scale, stream=None):
 def _operand(q, name):
     """A 2D byte operand that is contiguous, or the transpose of a contiguous
     matrix: (tensor, whether it is the latter)."""
-    by_column = isinstance(q, torch.Tensor) and q.dim() == 2 and not q.is_contiguous() \
-        and q.t().is_contiguous()
+    if not isinstance(q, torch.Tensor) or q.dim() != 2 or q.is_contiguous():
+        _dev_tensor(q, name, dtypes=BYTES, ndim=2)
+        return False
+    by_column = q.t().is_contiguous()
     _dev_tensor(q.t() if by_column else q, name, dtypes=BYTES, ndim=2)
     return by_column
 
@@ -381,7 +384,7 @@ def _shaped(t, name, shape, dtypes):
 
 
 def _saved(q0, s0_blk, M, C):
-    """The 8-bit saved form of an (M, C) tensor; both parts or neither."""
+    """Checks the 8-bit saved form of an (M, C) tensor; both parts or neither."""
     if (q0 is None) != (s0_blk is None):
         raise ValueError("q0 and s0_blk go together")
     if q0 is not None:
@@ -612,27 +615,49 @@ def cast_rowwise(x, stream=None):
     return q, scale
 
 
-def matmul(qa, sa_blk, qb, sb_blk, out_dtype=torch.bfloat16, stream=None):
-    """A B^T of MX operands as a (M, N) tensor of out_dtype."""
-    out = torch.empty((qa.shape[0], qb.shape[0]), dtype=out_dtype, device=qa.device)
-    mx_matmul(qa, sa_blk, qb, sb_blk, out, stream)
-    return out
+# The training operators below are called per layer, on tensors that may take the
+# GPU a few microseconds, so the wrappers check their inputs once, by the cheapest
+# tests that tell a good one (a bad one goes to the checks above, which raise),
+# and hand the outputs that they allocate straight to the library.
+
+_BF16, _F32, _U8 = torch.bfloat16, torch.float32, torch.uint8
 
 
-def layer_norm(x, w, b=None, eps=1e-5, save=False, stream=None):
-    """Layer norm of bf16 x (M, D).  Returns (y, mean, rstd), with save=True
-    (y, mean, rstd, q0, s0_blk): x saved in 8 bits for the backward pass."""
-    M, D = x.shape
-    y = torch.empty((M, D), dtype=torch.bfloat16, device=x.device)
-    mean = torch.empty(M, dtype=torch.float32, device=x.device)
-    rstd = torch.empty(M, dtype=torch.float32, device=x.device)
-    if not save:
-        mx_layer_norm(x, w, b, eps, y, mean, rstd, stream=stream)
-        return y, mean, rstd
-    q0 = torch.empty((M, D), dtype=torch.uint8, device=x.device)
-    s0 = _u8(mx_blocked_bytes(M, D // 32), x.device)
-    mx_layer_norm(x, w, b, eps, y, mean, rstd, q0, s0, stream)
-    return y, mean, rstd, q0, s0
+def _rows(t, name):
+    """(rows, columns) of a contiguous 2D bf16 tensor."""
+    if isinstance(t, torch.Tensor) and t.dtype is _BF16 and t.dim() == 2 and t.is_contiguous():
+        return t.shape
+    return _dev_tensor(t, name, dtypes=BF16, ndim=2).shape
+
+
+def _like(t, name, shape, dtype):
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.is_contiguous()):
+        _shaped(t, name, tuple(shape), (dtype,))
+
+
+def _width_param(t, name, D):
+    if not (isinstance(t, torch.Tensor) and t.dtype in TYPES and t.shape == (D,)
+            and t.is_contiguous()):
+        _shaped(t, name, (D,), tuple(TYPES))
+    return t.dtype
+
+
+def _one_device(t, *others):
+    dev = t.get_device()
+    if dev < 0 or any(o is not None and o.get_device() != dev for o in others):
+        return _device(t, *others)
+    return dev
+
+
+def _on_stream(stream, t):
+    """Context for a call on `stream` (a torch.cuda.Stream or a raw handle): it
+    becomes the current stream, so that what the call allocates is that
+    stream's and goes back to the allocator in its order."""
+    _stream(stream, _device(t))
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=t.device)
+    return torch.cuda.stream(stream)
 
 
 def _split_saved(saved):
@@ -640,50 +665,114 @@ def _split_saved(saved):
     return (saved, None, None) if isinstance(saved, torch.Tensor) else (None, *saved)
 
 
+def matmul(qa, sa_blk, qb, sb_blk, out_dtype=torch.bfloat16, stream=None):
+    """A B^T of MX operands as a (M, N) tensor of out_dtype."""
+    if stream is not None:
+        with _on_stream(stream, qa):
+            return matmul(qa, sa_blk, qb, sb_blk, out_dtype)
+    orders = _operand(qa, "qa") | _operand(qb, "qb") << 1
+    M, K = qa.shape
+    N = qb.shape[0]
+    if qb.shape[1] != K:
+        raise ValueError("qa and qb must have equal rows, got %d and %d values" % (K, qb.shape[1]))
+    _dev_tensor(sa_blk, "sa_blk", mx_blocked_bytes(M, K // 32), BYTES)
+    _dev_tensor(sb_blk, "sb_blk", mx_blocked_bytes(N, K // 32), BYTES)
+    if out_dtype not in TYPES:
+        raise TypeError("out_dtype must be one of %s, got %s"
+                        % (", ".join(str(d) for d in TYPES), out_dtype))
+    dev = _one_device(qa, sa_blk, qb, sb_blk)
+    out = torch.empty((M, N), dtype=out_dtype, device=qa.device)
+    _call("mx_matmul", dev, None, qa.data_ptr(), sa_blk.data_ptr(), qb.data_ptr(),
+          sb_blk.data_ptr(), M, N, K, orders, out.data_ptr(), TYPES[out_dtype])
+    return out
+
+
+def layer_norm(x, w, b=None, eps=1e-5, save=False, stream=None):
+    """Layer norm of bf16 x (M, D).  Returns (y, mean, rstd), with save=True
+    (y, mean, rstd, q0, s0_blk): x saved in 8 bits for the backward pass."""
+    if stream is not None:
+        with _on_stream(stream, x):
+            return layer_norm(x, w, b, eps, save)
+    M, D = _rows(x, "x")
+    wt = _width_param(w, "w", D)
+    if b is not None:
+        _like(b, "b", (D,), wt)
+    dev = _one_device(x, w, b)
+    y = torch.empty_like(x)
+    mean = torch.empty(M, dtype=_F32, device=x.device)
+    rstd = torch.empty_like(mean)
+    bp = None if b is None else b.data_ptr()
+    if not save:
+        _call("mx_layer_norm", dev, None, x.data_ptr(), w.data_ptr(), bp, TYPES[wt], M, D, eps,
+              y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), None, None)
+        return y, mean, rstd
+    q0 = torch.empty((M, D), dtype=_U8, device=x.device)
+    s0 = torch.empty(mx_blocked_bytes(M, D // 32), dtype=_U8, device=x.device)
+    _call("mx_layer_norm", dev, None, x.data_ptr(), w.data_ptr(), bp, TYPES[wt], M, D, eps,
+          y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), q0.data_ptr(), s0.data_ptr())
+    return y, mean, rstd, q0, s0
+
+
 def layer_norm_backward(dy, saved, w, mean, rstd, bias=True, stream=None):
     """saved: the forward pass's bf16 x, or the pair (q0, s0_blk).  Returns
     (dx, dw, db), the last two in w's type; db is None with bias=False."""
+    if stream is not None:
+        with _on_stream(stream, dy):
+            return layer_norm_backward(dy, saved, w, mean, rstd, bias)
     x, q0, s0 = _split_saved(saved)
-    M, D = dy.shape
-    dx = torch.empty((M, D), dtype=torch.bfloat16, device=dy.device)
-    dw = torch.empty(D, dtype=w.dtype, device=dy.device)
-    db = torch.empty(D, dtype=w.dtype, device=dy.device) if bias else None
-    work = _work(mx_layer_norm_backward_work_bytes(M, D), dy.device, stream)
-    mx_layer_norm_backward(dy, x, q0, s0, w, mean, rstd, dx, dw, db, work, stream)
+    M, D = _rows(dy, "dy")
+    if x is not None:
+        _like(x, "x", (M, D), _BF16)
+    else:
+        _saved(q0, s0, M, D)
+    wt = _width_param(w, "w", D)
+    _like(mean, "mean", (M,), _F32)
+    _like(rstd, "rstd", (M,), _F32)
+    dev = _one_device(dy, x, q0, s0, w, mean, rstd)
+    dx, dw = torch.empty_like(dy), torch.empty_like(w)
+    db = torch.empty_like(w) if bias else None
+    work = torch.empty(mx_layer_norm_backward_work_bytes(M, D), dtype=_U8, device=dy.device)
+    _call("mx_layer_norm_backward", dev, None, dy.data_ptr(), _ptr(x), _ptr(q0), _ptr(s0),
+          w.data_ptr(), TYPES[wt], mean.data_ptr(), rstd.data_ptr(), M, D, dx.data_ptr(),
+          dw.data_ptr(), _ptr(db), work.data_ptr())
     return dx, dw, db
-
-
-def _work(n, device, stream):
-    """Scratch that goes back to torch's allocator when the wrapper returns:
-    allocated on the stream that the call runs on, so that its next user runs
-    after the call."""
-    if stream is None or device.type != "cuda":
-        return _u8(n, device)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
-    with torch.cuda.stream(stream):
-        return _u8(n, device)
 
 
 def swiglu(gu, save=False, stream=None):
     """h = silu(g) u of bf16 gu = [g | u] (M, 2F).  Returns h (M, F), with
     save=True (h, q0, s0_blk): gu saved in 8 bits for the backward pass."""
-    M, F2 = gu.shape
-    h = torch.empty((M, F2 // 2), dtype=torch.bfloat16, device=gu.device)
+    if stream is not None:
+        with _on_stream(stream, gu):
+            return swiglu(gu, save)
+    M, F2 = _rows(gu, "gu")
+    if F2 % 2:
+        raise ValueError("gu must have an even number of columns, got %d" % F2)
+    dev = _one_device(gu)
+    h = torch.empty((M, F2 // 2), dtype=_BF16, device=gu.device)
     if not save:
-        mx_swiglu(gu, h, stream=stream)
+        _call("mx_swiglu", dev, None, gu.data_ptr(), M, F2 // 2, h.data_ptr(), None, None)
         return h
-    q0 = torch.empty((M, F2), dtype=torch.uint8, device=gu.device)
-    s0 = _u8(mx_blocked_bytes(M, F2 // 32), gu.device)
-    mx_swiglu(gu, h, q0, s0, stream)
+    q0 = torch.empty((M, F2), dtype=_U8, device=gu.device)
+    s0 = torch.empty(mx_blocked_bytes(M, F2 // 32), dtype=_U8, device=gu.device)
+    _call("mx_swiglu", dev, None, gu.data_ptr(), M, F2 // 2, h.data_ptr(), q0.data_ptr(),
+          s0.data_ptr())
     return h, q0, s0
 
 
 def swiglu_backward(dh, saved, stream=None):
     """saved: the forward pass's bf16 gu, or the pair (q0, s0_blk).  Returns
     the gradient of gu (M, 2F)."""
+    if stream is not None:
+        with _on_stream(stream, dh):
+            return swiglu_backward(dh, saved)
     gu, q0, s0 = _split_saved(saved)
-    M, F = dh.shape
-    dgu = torch.empty((M, 2 * F), dtype=torch.bfloat16, device=dh.device)
-    mx_swiglu_backward(dh, gu, q0, s0, dgu, stream)
+    M, F = _rows(dh, "dh")
+    if gu is not None:
+        _like(gu, "gu", (M, 2 * F), _BF16)
+    else:
+        _saved(q0, s0, M, 2 * F)
+    dev = _one_device(dh, gu, q0, s0)
+    dgu = torch.empty((M, 2 * F), dtype=_BF16, device=dh.device)
+    _call("mx_swiglu_backward", dev, None, dh.data_ptr(), _ptr(gu), _ptr(q0), _ptr(s0), M, F,
+          dgu.data_ptr())
     return dgu

@@ -270,7 +270,10 @@ int mx_watchdog(int clear) {
   int m = 0;
   rc = mx::read_matmul_watchdog(&m, clear != 0);
   if (rc) return cuda_fail(rc);
-  return v | w | d | m;
+  int n = 0;
+  rc = mx::read_norm_watchdog(&n, clear != 0);
+  if (rc) return cuda_fail(rc);
+  return v | w | d | m | n;
 }
 
 int mx_bounds_check(int clear) {

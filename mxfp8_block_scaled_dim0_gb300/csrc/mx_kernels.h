@@ -170,6 +170,7 @@ struct SwigluArgs {
 };
 int launch_swiglu(const SwigluArgs& a, int num_sms, cudaStream_t stream);
 int launch_swiglu_backward(const SwigluArgs& a, int num_sms, cudaStream_t stream);
+int read_norm_watchdog(int* out, bool clear);
 int out_of_bounds_norm(bool clear);
 int out_of_bounds_swiglu(bool clear);
 int read_watchdog(int* out, bool clear);

@@ -145,21 +145,135 @@ __device__ __forceinline__ uint2 ld_q8(const uint8_t* p) {
   return v;
 }
 
+// ---- pairs of fp32 values (one instruction a pair) --------------------------------
+
+using f32x2 = unsigned long long;
+
+__device__ __forceinline__ f32x2 pair(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+
+__device__ __forceinline__ void unpair(f32x2 v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// The two bf16 halves of a word.
+__device__ __forceinline__ f32x2 bf_pair(uint32_t w) { return pair(bf_lo(w), bf_hi(w)); }
+
+__device__ __forceinline__ uint32_t pack_pair(f32x2 v) {
+  float lo, hi;
+  unpair(v, lo, hi);
+  return pack_bf16(lo, hi);
+}
+
+__device__ __forceinline__ float sum_pair(f32x2 v) {
+  float lo, hi;
+  unpair(v, lo, hi);
+  return lo + hi;
+}
+
+__device__ __forceinline__ void get_pairs(const uint4& w, f32x2* v) {
+  v[0] = bf_pair(w.x);
+  v[1] = bf_pair(w.y);
+  v[2] = bf_pair(w.z);
+  v[3] = bf_pair(w.w);
+}
+
+__device__ __forceinline__ uint4 pack_pairs(const f32x2* v) {
+  return make_uint4(pack_pair(v[0]), pack_pair(v[1]), pack_pair(v[2]), pack_pair(v[3]));
+}
+
+// Eight parameters (fp32 or bf16) as pairs; read by every row, so through L1.
+__device__ __forceinline__ void load_param_pairs(const float* p, f32x2* v) {
+  const ulonglong2 a = __ldg(reinterpret_cast<const ulonglong2*>(p));
+  const ulonglong2 b = __ldg(reinterpret_cast<const ulonglong2*>(p) + 1);
+  v[0] = a.x;
+  v[1] = a.y;
+  v[2] = b.x;
+  v[3] = b.y;
+}
+
+__device__ __forceinline__ void load_param_pairs(const uint16_t* p, f32x2* v) {
+  get_pairs(__ldg(reinterpret_cast<const uint4*>(p)), v);
+}
+
+__device__ __forceinline__ uint32_t e4m3_pair(f32x2 v) {
+  float lo, hi;
+  unpair(v, lo, hi);
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// mx_cast_piece for values that are at hand as pairs too (v: those of w).
+__device__ __forceinline__ uint2 mx_cast_pairs(const uint4& w, const f32x2* v, uint32_t& sbyte) {
+  uint32_t m = absmax2(absmax2(w.x, w.y), absmax2(w.z, w.w));
+  m = max(mag_lo(m), mag_hi(m));
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  float mult;
+  mx_scale(m, sbyte, mult);
+  const f32x2 m2 = pair(mult, mult);
+  return make_uint2(e4m3_pair(mul2(v[0], m2)) | (e4m3_pair(mul2(v[1], m2)) << 16),
+                    e4m3_pair(mul2(v[2], m2)) | (e4m3_pair(mul2(v[3], m2)) << 16));
+}
+
+// Eight saved values as pairs.
+__device__ __forceinline__ void mx_get_pairs(const uint2& q, uint32_t sbyte, f32x2* v) {
+  const float m = scale_mult(sbyte);
+  const f32x2 m2 = pair(m, m);
+  const uint32_t w[4] = {q.x & 0xFFFFu, q.x >> 16, q.y & 0xFFFFu, q.y >> 16};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float lo, hi;
+    e4m3x2_get(w[j], lo, hi);
+    v[j] = mul2(pair(lo, hi), m2);
+  }
+}
+
+// ---- sums over a group of warps ------------------------------------------------
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
-// Sums over a group of `warps` warps that meet at named barrier `id`.  `red`
-// holds two slots of 32 pairs, used in turn (`phase`), so that one barrier a
-// sum is enough: a slot is written again only after the other slot's barrier,
-// which every thread reaches after its reads of this one.  The order of the
-// additions is fixed.
+// Sums over a group of `warps` <= 32 warps that meet at named barrier `id`.
+// `red` holds two slots of 32 pairs, zero at the start and used in turn, so that
+// one barrier a sum is enough: a slot is written again only after the other
+// slot's barrier, which every thread reaches after its reads of this one.  Every
+// thread adds the warps' sums up itself, four at a time; the order is fixed.
 struct Group {
   float2* red;
   int id, warps, warp, lane;
   int phase;
+  __device__ __forceinline__ void meet() const {
+    if (warps == 1)
+      __syncwarp();
+    else
+      asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(32 * warps) : "memory");
+  }
   __device__ __forceinline__ float2 sum2(float a, float b) {
     a = warp_sum(a);
     b = warp_sum(b);
@@ -167,11 +281,31 @@ struct Group {
     float2* r = red + 32 * phase;
     phase ^= 1;
     if (lane == 0) r[warp] = make_float2(a, b);
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(32 * warps) : "memory");
-    const float2 v = lane < warps ? r[lane] : make_float2(0.0f, 0.0f);
-    return make_float2(warp_sum(v.x), warp_sum(v.y));
+    meet();
+    a = b = 0.0f;
+    for (int w = 0; w < warps; w += 4) {
+      const float4 u = *reinterpret_cast<const float4*>(r + w);
+      const float4 v = *reinterpret_cast<const float4*>(r + w + 2);
+      a += (u.x + u.z) + (v.x + v.z);
+      b += (u.y + u.w) + (v.y + v.w);
+    }
+    return make_float2(a, b);
   }
-  __device__ __forceinline__ float sum(float a) { return sum2(a, 0.0f).x; }
+  // One sum; the slots are used as 32 single values.
+  __device__ __forceinline__ float sum(float a) {
+    a = warp_sum(a);
+    if (warps == 1) return a;
+    float* r = reinterpret_cast<float*>(red + 32 * phase);
+    phase ^= 1;
+    if (lane == 0) r[warp] = a;
+    meet();
+    a = 0.0f;
+    for (int w = 0; w < warps; w += 4) {
+      const float4 u = *reinterpret_cast<const float4*>(r + w);
+      a += (u.x + u.y) + (u.z + u.w);
+    }
+    return a;
+  }
 };
 
 }  // namespace mx

@@ -18,6 +18,7 @@ namespace mx {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kOdd = 4;                // pieces of a lane, rows that are no multiple of 8
 
 struct SwigluParams {
   const uint16_t* gu;
@@ -25,101 +26,254 @@ struct SwigluParams {
   uint16_t* out;        // h, or the gradient of gu
   uint8_t* q;
   uint8_t* s;
-  int64_t M, rows, tasks;
+  int64_t M, rows;      // rows: M, or M padded to 128 where scales are written
   int F, runs;          // runs: warps' pieces of a row
   int s_cols4;          // scales of a row, padded to four
   Span sp_out, sp_q, sp_s;
 };
 
-__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+// 1 / (1 + exp(-g)).  exp(-g) overflows to infinity below g = -88.7, which gives
+// 0; a sigmoid under 2^-126 is flushed to 0.
+__device__ __forceinline__ float sigmoid(float g) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return r;
+}
 
-template <int VEC, bool SAVE>
+__device__ __forceinline__ f32x2 sigmoid2(f32x2 g) {
+  float lo, hi;
+  unpair(g, lo, hi);
+  return pair(sigmoid(lo), sigmoid(hi));
+}
+
+// A warp's place: row r, piece `run` of the row, walked in steps of the whole
+// grid without a division.
+struct Place {
+  int64_t r, dr;
+  int run, drun, runs;
+  __device__ __forceinline__ Place(int64_t warp, int64_t warps, int runs_) : runs(runs_) {
+    r = warp / runs;
+    run = static_cast<int>(warp - r * runs);
+    dr = warps / runs;
+    drun = static_cast<int>(warps - dr * runs);
+  }
+  __device__ __forceinline__ void next() {
+    r += dr;
+    run += drun;
+    if (run >= runs) {
+      run -= runs;
+      ++r;
+    }
+  }
+};
+
+// Rows whose halves are a multiple of 8 values: pieces of eight, as pairs; U
+// pieces' loads are issued before any is worked on.
+template <bool SAVE, int U>
+__global__ void __launch_bounds__(kThreads) swiglu_rows8_kernel(const SwigluParams p) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x & 31;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
+  Place at(static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5), warps, p.runs);
+  while (at.r < p.rows) {
+    Piece<8> pg[U], pu[U];
+    int64_t r[U];
+    int c[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      r[k] = at.r;
+      c[k] = (at.run * 32 + lane) * 8;
+      at.next();
+      pg[k].zero();
+      pu[k].zero();
+      if (r[k] < p.M && c[k] < p.F) {
+        const uint16_t* x = p.gu + r[k] * 2 * p.F + c[k];
+        pg[k].load(x);
+        pu[k].load(x + p.F);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      if (k > 0 && r[k] >= p.rows) break;
+      const bool live = r[k] < p.M && c[k] < p.F;
+      f32x2 g[4], u[4];
+      get_pairs(pg[k].w, g);
+      get_pairs(pu[k].w, u);
+      if constexpr (SAVE) {
+        uint32_t sg, su;
+        const uint2 qg = mx_cast_pairs(pg[k].w, g, sg);
+        const uint2 qu = mx_cast_pairs(pu[k].w, u, su);
+        uint8_t* q = p.q + r[k] * 2 * p.F + c[k];
+        if (live && in_span(p.sp_q, q, 8) && in_span(p.sp_q, q + p.F, 8)) {
+          *reinterpret_cast<uint2*>(q) = qg;
+          *reinterpret_cast<uint2*>(q + p.F) = qu;
+        }
+        // One lane of a block's four writes its byte.  Rows past the matrix are
+        // zero and give 0, the padding of the blocked layout.
+        uint8_t* s = p.s + blocked_offset(r[k], 0, p.s_cols4);
+        if (c[k] < p.F && (lane & 3) == 0) {
+          const int cg = c[k] >> 5, cu = cg + (p.F >> 5);
+          uint8_t* a = s + (cg >> 2) * 512 + (cg & 3);
+          uint8_t* b = s + (cu >> 2) * 512 + (cu & 3);
+          if (in_span(p.sp_s, a, 1)) *a = static_cast<uint8_t>(sg);
+          if (in_span(p.sp_s, b, 1)) *b = static_cast<uint8_t>(su);
+        }
+        // Columns of scales past the row: zero.
+        if (c[k] == 0 && p.s_cols4 > p.F / 16)
+          for (int j = p.F / 16; j < p.s_cols4; ++j) {
+            uint8_t* a = s + (j >> 2) * 512 + (j & 3);
+            if (in_span(p.sp_s, a, 1)) *a = 0;
+          }
+      }
+      if (!live) continue;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) g[j] = mul2(mul2(g[j], sigmoid2(g[j])), u[j]);
+      uint16_t* h = p.out + r[k] * p.F + c[k];
+      if (in_span(p.sp_out, h, 16)) *reinterpret_cast<uint4*>(h) = pack_pairs(g);
+    }
+  }
+}
+
+template <bool SAVE, int U>
+__global__ void __launch_bounds__(kThreads) swiglu_back_rows8_kernel(const SwigluParams p) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x & 31;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
+  Place at(static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5), warps, p.runs);
+  const f32x2 one = pair(1.0f, 1.0f), minus = pair(-1.0f, -1.0f);
+  while (at.r < p.M) {
+    Piece<8> pd[U], pg[U], pu[U];            // saved bytes: in .w.x and .w.y
+    uint32_t sg[U], su[U];
+    int64_t r[U];
+    int c[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      r[k] = at.r;
+      c[k] = (at.run * 32 + lane) * 8;
+      at.next();
+      if (r[k] < p.M && c[k] < p.F) {
+        pd[k].load(p.dh + r[k] * p.F + c[k]);
+        if constexpr (SAVE) {
+          const uint8_t* q = p.q + r[k] * 2 * p.F + c[k];
+          const uint2 a = ld_q8(q), b = ld_q8(q + p.F);
+          pg[k].w = make_uint4(a.x, a.y, 0, 0);
+          pu[k].w = make_uint4(b.x, b.y, 0, 0);
+          const uint8_t* s = p.s + blocked_offset(r[k], 0, p.s_cols4);
+          const int cg = c[k] >> 5, cu = cg + (p.F >> 5);
+          sg[k] = __ldg(s + (cg >> 2) * 512 + (cg & 3));
+          su[k] = __ldg(s + (cu >> 2) * 512 + (cu & 3));
+        } else {
+          const uint16_t* x = p.gu + r[k] * 2 * p.F + c[k];
+          pg[k].load(x);
+          pu[k].load(x + p.F);
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      if (r[k] >= p.M || c[k] >= p.F) continue;
+      f32x2 d[4], g[4], u[4];
+      get_pairs(pd[k].w, d);
+      if constexpr (SAVE) {
+        mx_get_pairs(make_uint2(pg[k].w.x, pg[k].w.y), sg[k], g);
+        mx_get_pairs(make_uint2(pu[k].w.x, pu[k].w.y), su[k], u);
+      } else {
+        get_pairs(pg[k].w, g);
+        get_pairs(pu[k].w, u);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const f32x2 s = sigmoid2(g[j]);
+        const f32x2 a = mul2(g[j], s);
+        const f32x2 t = fma2(a, fma2(s, minus, one), s);    // s (1 + g (1 - s))
+        u[j] = mul2(mul2(d[j], u[j]), t);
+        g[j] = mul2(d[j], a);
+      }
+      uint16_t* o = p.out + r[k] * 2 * p.F + c[k];
+      if (in_span(p.sp_out, o, 16) && in_span(p.sp_out, o + p.F, 16)) {
+        *reinterpret_cast<uint4*>(o) = pack_pairs(u);
+        *reinterpret_cast<uint4*>(o + p.F) = pack_pairs(g);
+      }
+    }
+  }
+}
+
+// Other widths, in pieces of two values or one.
+template <int VEC>
 __global__ void __launch_bounds__(kThreads) swiglu_kernel(const SwigluParams p) {
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-       t < p.tasks; t += warps) {
-    const int64_t r = t / p.runs;
-    const int c = (static_cast<int>(t - r * p.runs) * 32 + lane) * VEC;
-    const bool live = r < p.M && c < p.F;
-    Piece<VEC> pg, pu;
-    pg.zero();
-    pu.zero();
-    if (live) {
-      pg.load(p.gu + r * 2 * p.F + c);
-      pu.load(p.gu + r * 2 * p.F + p.F + c);
-    }
-    if constexpr (SAVE) {
+  Place at(static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5), warps, p.runs);
+  for (; at.r < p.M; at.next()) {
+    const uint16_t* x = p.gu + at.r * 2 * p.F;
+    uint16_t* out = p.out + at.r * p.F;
+    Piece<VEC> pg[kOdd], pu[kOdd];
+    const int c0 = (at.run * 32 * kOdd + lane) * VEC;
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t sb;
-        const uint2 q = mx_cast_piece(half ? pu.w : pg.w, sb);
-        const int col = half * p.F + c;
-        uint8_t* qp = p.q + r * 2 * p.F + col;
-        if (live && in_span(p.sp_q, qp, 8)) *reinterpret_cast<uint2*>(qp) = q;
-        if (c < p.F && (lane & 3) == 0) {
-          uint8_t* sp = p.s + blocked_offset(r, col >> 5, p.s_cols4);
-          if (in_span(p.sp_s, sp, 1)) *sp = static_cast<uint8_t>(r < p.M ? sb : 0);
-        }
-      }
-      // Columns of scales past the row: zero.
-      const int pad = p.s_cols4 - p.F / 16;
-      if (c == 0 && pad > 0)
-        for (int k = 0; k < pad; ++k) {
-          uint8_t* sp = p.s + blocked_offset(r, p.F / 16 + k, p.s_cols4);
-          if (in_span(p.sp_s, sp, 1)) *sp = 0;
-        }
+    for (int i = 0; i < kOdd; ++i) {
+      const int c = c0 + i * 32 * VEC;
+      if (c >= p.F) continue;
+      pg[i].load(x + c);
+      pu[i].load(x + p.F + c);
     }
-    if (!live) continue;
-    float g[VEC], u[VEC], h[VEC];
-    pg.get(g);
-    pu.get(u);
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) h[j] = g[j] * sigmoid(g[j]) * u[j];
-    store_bf16<VEC>(p.out + r * p.F + c, h, p.sp_out);
+    for (int i = 0; i < kOdd; ++i) {
+      const int c = c0 + i * 32 * VEC;
+      if (c >= p.F) continue;
+      float g[VEC], u[VEC], h[VEC];
+      pg[i].get(g);
+      pu[i].get(u);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) h[j] = g[j] * sigmoid(g[j]) * u[j];
+      store_bf16<VEC>(out + c, h, p.sp_out);
+    }
   }
 }
 
-template <int VEC, bool SAVE>
+template <int VEC>
 __global__ void __launch_bounds__(kThreads) swiglu_back_kernel(const SwigluParams p) {
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-       t < p.tasks; t += warps) {
-    const int64_t r = t / p.runs;
-    const int c = (static_cast<int>(t - r * p.runs) * 32 + lane) * VEC;
-    if (c >= p.F) continue;
-    Piece<VEC> pd;
-    pd.load(p.dh + r * p.F + c);
-    float g[VEC], u[VEC], d[VEC], dg[VEC], du[VEC];
-    if constexpr (SAVE) {
-      const uint8_t* qp = p.q + r * 2 * p.F + c;
-      const uint2 qg = ld_q8(qp), qu = ld_q8(qp + p.F);
-      const uint32_t sg = __ldg(p.s + blocked_offset(r, c >> 5, p.s_cols4));
-      const uint32_t su = __ldg(p.s + blocked_offset(r, (p.F + c) >> 5, p.s_cols4));
-      mx_get8(qg, sg, g);
-      mx_get8(qu, su, u);
-    } else {
-      Piece<VEC> pg, pu;
-      pg.load(p.gu + r * 2 * p.F + c);
-      pu.load(p.gu + r * 2 * p.F + p.F + c);
-      pg.get(g);
-      pu.get(u);
-    }
-    pd.get(d);
+  Place at(static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5), warps, p.runs);
+  for (; at.r < p.M; at.next()) {
+    const uint16_t* x = p.gu + at.r * 2 * p.F;
+    const uint16_t* dh = p.dh + at.r * p.F;
+    uint16_t* out = p.out + at.r * 2 * p.F;
+    Piece<VEC> pd[kOdd], pg[kOdd], pu[kOdd];
+    const int c0 = (at.run * 32 * kOdd + lane) * VEC;
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      const float sg = sigmoid(g[j]);
-      const float a = g[j] * sg;
-      du[j] = d[j] * a;
-      dg[j] = d[j] * u[j] * (sg + a * (1.0f - sg));
+    for (int i = 0; i < kOdd; ++i) {
+      const int c = c0 + i * 32 * VEC;
+      if (c >= p.F) continue;
+      pd[i].load(dh + c);
+      pg[i].load(x + c);
+      pu[i].load(x + p.F + c);
     }
-    store_bf16<VEC>(p.out + r * 2 * p.F + c, dg, p.sp_out);
-    store_bf16<VEC>(p.out + r * 2 * p.F + p.F + c, du, p.sp_out);
+#pragma unroll
+    for (int i = 0; i < kOdd; ++i) {
+      const int c = c0 + i * 32 * VEC;
+      if (c >= p.F) continue;
+      float g[VEC], u[VEC], d[VEC], dg[VEC], du[VEC];
+      pd[i].get(d);
+      pg[i].get(g);
+      pu[i].get(u);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        const float s = sigmoid(g[j]);
+        const float a = g[j] * s;
+        du[j] = d[j] * a;
+        dg[j] = d[j] * u[j] * (s + a * (1.0f - s));
+      }
+      store_bf16<VEC>(out + c, dg, p.sp_out);
+      store_bf16<VEC>(out + p.F + c, du, p.sp_out);
+    }
   }
 }
 
@@ -129,7 +283,7 @@ int run(K kernel, const SwigluParams& p, int num_sms, cudaStream_t stream) {
   if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kThreads, 0) != cudaSuccess ||
       per < 1)
     per = 1;
-  const int64_t want = (p.tasks + kThreads / 32 - 1) / (kThreads / 32);
+  const int64_t want = (p.rows * p.runs + kThreads / 32 - 1) / (kThreads / 32);
   const int64_t most = static_cast<int64_t>(num_sms) * per;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(want < most ? want : most));
@@ -153,8 +307,8 @@ SwigluParams params(const SwigluArgs& a, int vec, bool padded) {
   p.M = a.M;
   p.rows = padded ? (a.M + 127) / 128 * 128 : a.M;
   p.F = static_cast<int>(a.F);
-  p.runs = static_cast<int>((a.F + 32 * vec - 1) / (32 * vec));
-  p.tasks = p.rows * p.runs;
+  const int64_t run = vec == 8 ? 256 : 32 * kOdd * vec;
+  p.runs = static_cast<int>((a.F + run - 1) / run);
   p.s_cols4 = static_cast<int>((a.F / 16 + 3) / 4 * 4);
   const uint64_t n = static_cast<uint64_t>(a.M) * static_cast<uint64_t>(a.F);
   p.sp_out = make_span(a.out, a.dh ? 4 * n : 2 * n);
@@ -170,19 +324,19 @@ int vec_of(int64_t F) { return F % 8 == 0 ? 8 : F % 2 == 0 ? 2 : 1; }
 int launch_swiglu(const SwigluArgs& a, int num_sms, cudaStream_t stream) {
   const int v = vec_of(a.F);
   const SwigluParams p = params(a, v, a.q != nullptr);
-  if (a.q) return run(swiglu_kernel<8, true>, p, num_sms, stream);
-  if (v == 8) return run(swiglu_kernel<8, false>, p, num_sms, stream);
-  if (v == 2) return run(swiglu_kernel<2, false>, p, num_sms, stream);
-  return run(swiglu_kernel<1, false>, p, num_sms, stream);
+  if (a.q) return run(swiglu_rows8_kernel<true, 2>, p, num_sms, stream);
+  if (v == 8) return run(swiglu_rows8_kernel<false, 2>, p, num_sms, stream);
+  if (v == 2) return run(swiglu_kernel<2>, p, num_sms, stream);
+  return run(swiglu_kernel<1>, p, num_sms, stream);
 }
 
 int launch_swiglu_backward(const SwigluArgs& a, int num_sms, cudaStream_t stream) {
   const int v = vec_of(a.F);
   const SwigluParams p = params(a, v, false);
-  if (a.q) return run(swiglu_back_kernel<8, true>, p, num_sms, stream);
-  if (v == 8) return run(swiglu_back_kernel<8, false>, p, num_sms, stream);
-  if (v == 2) return run(swiglu_back_kernel<2, false>, p, num_sms, stream);
-  return run(swiglu_back_kernel<1, false>, p, num_sms, stream);
+  if (a.q) return run(swiglu_back_rows8_kernel<true, 2>, p, num_sms, stream);
+  if (v == 8) return run(swiglu_back_rows8_kernel<false, 2>, p, num_sms, stream);
+  if (v == 2) return run(swiglu_back_kernel<2>, p, num_sms, stream);
+  return run(swiglu_back_kernel<1>, p, num_sms, stream);
 }
 
 int out_of_bounds_swiglu(bool clear) { return read_out_of_bounds(clear); }

@@ -203,7 +203,7 @@ __device__ __forceinline__ uint4 pack_pairs(const f32x2* v) {
   return make_uint4(pack_pair(v[0]), pack_pair(v[1]), pack_pair(v[2]), pack_pair(v[3]));
 }
 
-// Eight parameters (fp32 or bf16) as pairs; read by every row, so through L1.
+// Eight parameters (fp32 or bf16) as pairs, from global memory.
 __device__ __forceinline__ void load_param_pairs(const float* p, f32x2* v) {
   const ulonglong2 a = __ldg(reinterpret_cast<const ulonglong2*>(p));
   const ulonglong2 b = __ldg(reinterpret_cast<const ulonglong2*>(p) + 1);
@@ -215,6 +215,28 @@ __device__ __forceinline__ void load_param_pairs(const float* p, f32x2* v) {
 
 __device__ __forceinline__ void load_param_pairs(const uint16_t* p, f32x2* v) {
   get_pairs(__ldg(reinterpret_cast<const uint4*>(p)), v);
+}
+
+// D parameters in shared memory as fp32, zeros from D to `pitch`; the first and
+// the last four of every eight in halves of their own: a warp's 16-byte reads of
+// neighbouring pieces are then free of bank conflicts.
+template <typename W>
+__device__ __forceinline__ void stage_params(float* dst, const W* src, int D, int pitch) {
+  for (int c = threadIdx.x; c < pitch / 8; c += blockDim.x) {
+    f32x2 v[4] = {0, 0, 0, 0};
+    if (8 * c < D) load_param_pairs(src + 8 * c, v);
+    reinterpret_cast<ulonglong2*>(dst)[c] = make_ulonglong2(v[0], v[1]);
+    reinterpret_cast<ulonglong2*>(dst)[pitch / 8 + c] = make_ulonglong2(v[2], v[3]);
+  }
+}
+
+__device__ __forceinline__ void staged_pairs(const float* src, int pitch, int c, f32x2* v) {
+  const ulonglong2 a = reinterpret_cast<const ulonglong2*>(src)[c];
+  const ulonglong2 b = reinterpret_cast<const ulonglong2*>(src)[pitch / 8 + c];
+  v[0] = a.x;
+  v[1] = a.y;
+  v[2] = b.x;
+  v[3] = b.y;
 }
 
 __device__ __forceinline__ uint32_t e4m3_pair(f32x2 v) {
@@ -259,13 +281,15 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Sums over a group of `warps` <= 32 warps that meet at named barrier `id`.
-// `red` holds two slots of 32 pairs, zero at the start and used in turn, so that
+// Sums over a group of `warps` <= MAXW warps that meet at named barrier `id`.
+// `red` holds two slots of 64 floats, zero at the start and used in turn, so that
 // one barrier a sum is enough: a slot is written again only after the other
-// slot's barrier, which every thread reaches after its reads of this one.  Every
-// thread adds the warps' sums up itself, four at a time; the order is fixed.
+// slot's barrier, which every thread reaches after its reads of this one.  Two
+// sums travel together, one in either half of a warp after the first exchange.
+// The order of the additions is fixed.
+template <int MAXW>
 struct Group {
-  float2* red;
+  float* red;
   int id, warps, warp, lane;
   int phase;
   __device__ __forceinline__ void meet() const {
@@ -274,37 +298,38 @@ struct Group {
     else
       asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(32 * warps) : "memory");
   }
-  __device__ __forceinline__ float2 sum2(float a, float b) {
-    a = warp_sum(a);
-    b = warp_sum(b);
-    if (warps == 1) return make_float2(a, b);
-    float2* r = red + 32 * phase;
-    phase ^= 1;
-    if (lane == 0) r[warp] = make_float2(a, b);
-    meet();
-    a = b = 0.0f;
-    for (int w = 0; w < warps; w += 4) {
-      const float4 u = *reinterpret_cast<const float4*>(r + w);
-      const float4 v = *reinterpret_cast<const float4*>(r + w + 2);
-      a += (u.x + u.z) + (v.x + v.z);
-      b += (u.y + u.w) + (v.y + v.w);
-    }
-    return make_float2(a, b);
+  // The sum of v[0..MAXW), in every lane.
+  __device__ __forceinline__ float across(const float* v) const {
+    float a = v[lane & 15];
+    if (MAXW > 16) a += v[16 + (lane & 15)];
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+    return a;
   }
-  // One sum; the slots are used as 32 single values.
+  __device__ __forceinline__ float2 sum2(float a, float b) {
+    const bool low = lane < 16;
+    float v = low ? a : b;
+    v += __shfl_xor_sync(0xffffffffu, low ? b : a, 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (warps > 1) {
+      float* r = red + 64 * phase + (low ? 0 : 32);
+      phase ^= 1;
+      if ((lane & 15) == 0) r[warp] = v;
+      meet();
+      v = across(r);
+    }
+    const float w = __shfl_xor_sync(0xffffffffu, v, 16);
+    return low ? make_float2(v, w) : make_float2(w, v);
+  }
   __device__ __forceinline__ float sum(float a) {
     a = warp_sum(a);
     if (warps == 1) return a;
-    float* r = reinterpret_cast<float*>(red + 32 * phase);
+    float* r = red + 64 * phase;
     phase ^= 1;
     if (lane == 0) r[warp] = a;
     meet();
-    a = 0.0f;
-    for (int w = 0; w < warps; w += 4) {
-      const float4 u = *reinterpret_cast<const float4*>(r + w);
-      a += (u.x + u.y) + (u.z + u.w);
-    }
-    return a;
+    return across(r);
   }
 };
 

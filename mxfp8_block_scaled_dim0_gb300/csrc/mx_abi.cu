@@ -239,7 +239,7 @@ int64_t mx_3d_dim0_scale_bytes(int64_t E, int64_t N, int64_t K) {
 
 int64_t mx_layer_norm_backward_work_bytes(int64_t M, int64_t D) {
   if (M < 0 || D < 0) return -1;
-  return mx::norm_back_parts(M) * 8 * D;
+  return 4 * mx::norm_back_work_floats(M, D);
 }
 
 const char* mx_strerror(int code) {

@@ -136,8 +136,8 @@ struct LayerNormArgs {
   void* q;
   void* s;
 };
-// x null: the saved input q, s; db null: not wanted.  work: norm_back_parts(M)
-// partial sums of 2 D floats.
+// x null: the saved input q, s; db null: not wanted.  work:
+// norm_back_work_floats(M, D) floats.
 struct LayerNormBackArgs {
   const void* dy;
   const void* x;
@@ -155,7 +155,7 @@ struct LayerNormBackArgs {
 };
 constexpr int64_t kNormMaxParts = 304;
 constexpr int64_t kNormMaxWidth = 16384;
-int64_t norm_back_parts(int64_t M);
+int64_t norm_back_work_floats(int64_t M, int64_t D);
 int launch_layer_norm(const LayerNormArgs& a, int num_sms, cudaStream_t stream);
 int launch_layer_norm_backward(const LayerNormBackArgs& a, int num_sms, cudaStream_t stream);
 // Gated SiLU (mx_swiglu.cu).  Forward: gu -> out = h, saved into q, s unless

@@ -7,15 +7,21 @@
 //   dx   = rstd (g - (1/D) sum g - xh (1/D) sum g xh)
 //   dw   = sum over rows of dy xh, db = sum over rows of dy
 //
-// A group of warps works on a row.  Rows of a multiple of 8 values come into
-// shared memory by bulk copies, a ring of rows for every group, so that what is
-// in flight takes no registers and no instruction waits for memory; each SM runs
-// one CTA of several groups, which share w and b in shared memory.  A row's
-// place in shared memory is padded with zeros to the group's whole width, so
-// that the arithmetic needs no conditions.  (Rows loaded a row ahead into
-// registers, four CTAs an SM: 94 us forward and 159 us backward at 16640 x 5120
-// with the 8-bit save.)  Other rows go through registers in pieces of two values
-// or one.
+// A group of warps works on a row.  Rows come into shared memory by bulk copies,
+// a ring of rows for every group, so that what is in flight takes no registers
+// and no instruction waits for memory; each SM runs one CTA of several groups,
+// which share w and b in shared memory.  A row's place in shared memory is padded
+// with zeros to the group's whole width, so that the arithmetic needs no
+// conditions.  (Rows loaded a row ahead into registers, four CTAs an SM: 94 us
+// forward and 159 us backward at 16640 x 5120 with the 8-bit save.)
+//
+// Bulk copies and 16-byte accesses want 16-byte boundaries.  Where the row length
+// is no multiple of 8 values, rows r and r + 8 begin at the same distance from
+// one: the grid is a multiple of 8, so that all rows of a CTA have the same
+// distance, `lead` values, and the CTA works on rows that begin `lead` values
+// early, on the boundary, its w and b shifted by as much.  What a copy brings of
+// the neighbouring rows is cleared where it is read (first and last piece only),
+// and those two pieces are stored value by value.
 //
 // The backward kernel keeps dw and db of its threads' columns in registers over
 // all its rows, adds the groups of a CTA up at its end, and leaves one partial
@@ -28,9 +34,6 @@
 namespace mx {
 namespace {
 
-constexpr int kPer = 16;                     // values a thread holds of a row
-constexpr int kMaxThreads = 1024;
-
 // Every wait is bounded: one that runs out raises the abort flag, the threads go
 // on to the end without waiting, and the watchdog word is set.
 __device__ int g_norm_watchdog = 0;
@@ -41,19 +44,17 @@ constexpr int kMaxGroups = 20;
 constexpr int kMaxStages = 4;
 constexpr int kRingBytes = 212 * 1024;       // rings, w and b
 
-// How rows of a multiple of 8 values are shared out.
+// How rows are shared out.
 struct RowShape {
   int warps;           // of a group
   int groups;          // of a CTA
   int stages;          // rows of a group's ring
-  int pitch;           // values a group holds: 32 warps EPT >= D
+  int pitch;           // values a group holds: 32 warps EPT >= D (and the lead)
 };
 
-// Clears the rings' padding (all of it, once) and sets up the barriers.
-__device__ __forceinline__ void ring_setup(uint8_t* ring, int bytes, uint64_t* full, int n,
-                                           uint64_t* stall_bar, int* abort_flag, float* red) {
-  for (int i = threadIdx.x; i < bytes / 16; i += blockDim.x)
-    reinterpret_cast<uint4*>(ring)[i] = make_uint4(0, 0, 0, 0);
+// Sets up the barriers and the sums' slots.
+__device__ __forceinline__ void ring_setup(uint64_t* full, int n, uint64_t* stall_bar,
+                                           int* abort_flag, float* red) {
   for (int i = threadIdx.x; i < kMaxGroups * 128; i += blockDim.x) red[i] = 0.0f;
   if (threadIdx.x == 0) {
     for (int i = 0; i < n; ++i) mbar_init(&full[i], 1);
@@ -61,8 +62,67 @@ __device__ __forceinline__ void ring_setup(uint8_t* ring, int bytes, uint64_t* f
     *abort_flag = 0;
     fence_mbar_init();
   }
-  fence_proxy_async_smem();                  // the copies write what was cleared
 }
+
+// Zeros in bytes [from, to) of `n` places `stride` bytes apart: the padding that
+// no copy writes.  Multiples of 8.
+__device__ __forceinline__ void clear_padding(uint8_t* at, int n, int stride, int from, int to) {
+  const int words = (to - from) >> 3;
+  for (int i = threadIdx.x; i < n * words; i += blockDim.x) {
+    const int k = i / words;
+    *reinterpret_cast<uint2*>(at + k * stride + from + 8 * (i - k * words)) = make_uint2(0, 0);
+  }
+}
+
+// A CTA's rows: `lead` values early (ODD: the row length is no multiple of 8),
+// in `total` pieces of 8 values.
+template <bool ODD>
+struct RowSpan {
+  int lead, width, total;
+  __device__ __forceinline__ explicit RowSpan(int D) {
+    lead = ODD ? static_cast<int>((blockIdx.x * static_cast<unsigned>(D)) & 7u) : 0;
+    width = D + lead;
+    total = (width + 7) >> 3;
+  }
+  __device__ __forceinline__ bool edge(int c) const { return ODD && (c == 0 || c == total - 1); }
+  __device__ __forceinline__ bool holds(int e) const { return e >= lead && e < width; }
+  // Clears what a piece at the row's ends holds of its neighbours.
+  __device__ __forceinline__ void clear(uint4& v, int c) const {
+    if (!edge(c)) return;
+    uint32_t* w = &v.x;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      w[k] &= (holds(8 * c + 2 * k) ? 0xFFFFu : 0u) | (holds(8 * c + 2 * k + 1) ? 0xFFFF0000u : 0u);
+  }
+  // Stores piece c of the row that begins at `row` (lead included).
+  __device__ __forceinline__ void store(uint16_t* row, int c, const f32x2* v, const Span& sp) const {
+    if (c >= total) return;
+    const uint4 w = pack_pairs(v);
+    uint16_t* at = row + 8 * c;
+    if (!edge(c)) {
+      if (in_span(sp, at, 16)) *reinterpret_cast<uint4*>(at) = w;
+      return;
+    }
+    const uint32_t* h = &w.x;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (holds(8 * c + j) && in_span(sp, at + j, 2))
+        at[j] = static_cast<uint16_t>(h[j >> 1] >> (16 * (j & 1)));
+  }
+  // Bytes of a row's copy, and what of them lies before the end of the M rows.
+  __device__ __forceinline__ int copy_bytes(int64_t r, int64_t M, int D) const {
+    if (!ODD) return 2 * D;
+    const int64_t room = 2 * (M * D - (r * D - lead));
+    return room < 16 * total ? static_cast<int>(room & ~int64_t{15}) : 16 * total;
+  }
+  // The last values of the matrix, where no 16 bytes are left.
+  __device__ __forceinline__ void copy_tail(uint8_t* to, const uint16_t* row, int bytes) const {
+    if (!ODD || bytes == 16 * total) return;
+    uint16_t* d = reinterpret_cast<uint16_t*>(to);
+    for (int e = bytes / 2; e < width; ++e) d[e] = row[e];
+    fence_proxy_async_smem();
+  }
+};
 
 struct NormParams {
   const uint16_t* x;
@@ -74,7 +134,7 @@ struct NormParams {
   uint8_t* q;
   uint8_t* s;
   int64_t M;
-  int D, warps, groups;
+  int D;
   RowShape shape;
   int s_words;         // 128x4 scale tiles of a row
   int staged;          // w and b are read from shared memory
@@ -85,8 +145,8 @@ struct NormParams {
 };
 
 // EPT values a thread, as pairs.
-template <bool SAVE, typename W, int EPT>
-__global__ void __launch_bounds__(kRingThreads, 1) norm_rows8_kernel(const NormParams p) {
+template <bool SAVE, bool ODD, typename W, int EPT>
+__global__ void __launch_bounds__(kRingThreads, 1) norm_kernel(const NormParams p) {
   constexpr int V = EPT / 8;
   asm volatile("griddepcontrol.launch_dependents;");
   extern __shared__ __align__(128) uint8_t ring[];
@@ -95,18 +155,21 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_rows8_kernel(const NormP
   __shared__ __align__(8) uint64_t stall_bar;   // diagnostic: never completed
   __shared__ int abort_flag;
   const RowShape& sh = p.shape;
+  const RowSpan<ODD> span(p.D);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = warp / sh.warps;
   Group<16> grp{red + 128 * g, g + 1, sh.warps, warp - g * sh.warps, lane, 0};
   const int T = 32 * sh.warps, tid = grp.warp * 32 + lane;
   const int stage_bytes = 2 * sh.pitch;
-  const int ring_bytes = sh.groups * sh.stages * stage_bytes;
-  ring_setup(ring, ring_bytes, full, sh.groups * sh.stages, &stall_bar, &abort_flag, red);
+  const int places = sh.groups * sh.stages;
+  ring_setup(full, places, &stall_bar, &abort_flag, red);
+  clear_padding(ring, places, stage_bytes, 16 * span.total, 2 * sh.pitch);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  float* params = reinterpret_cast<float*>(ring + ring_bytes);   // w, then b
+  float* params = reinterpret_cast<float*>(ring + places * stage_bytes);   // w, then b
   if (p.staged) {
-    stage_params(params, static_cast<const W*>(p.w), p.D, sh.pitch);
-    stage_params(params + sh.pitch, static_cast<const W*>(p.b), p.b ? p.D : 0, sh.pitch);
+    stage_params<ODD>(params, static_cast<const W*>(p.w), span.lead, p.D, sh.pitch);
+    stage_params<ODD>(params + sh.pitch, static_cast<const W*>(p.b), span.lead, p.b ? p.D : 0,
+                      sh.pitch);
   }
   __syncthreads();
 
@@ -114,8 +177,12 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_rows8_kernel(const NormP
   uint64_t* bars = full + g * sh.stages;
   volatile int* aborted = &abort_flag;
   auto issue = [&](int st, int64_t r) {
-    mbar_arrive_expect_tx(&bars[st], 2 * p.D);
-    bulk_load(mine + st * stage_bytes, p.x + r * p.D, 2 * p.D, &bars[st]);
+    uint8_t* to = mine + st * stage_bytes;
+    const uint16_t* x = p.x + r * p.D - span.lead;
+    const int bytes = span.copy_bytes(r, p.M, p.D);
+    span.copy_tail(to, x, bytes);
+    mbar_arrive_expect_tx(&bars[st], bytes);
+    if (!ODD || bytes > 0) bulk_load(to, x, bytes, &bars[st]);
   };
   // Groups of a CTA are a grid apart, so that few rows spread over all CTAs.
   const int64_t r0 = static_cast<int64_t>(g) * gridDim.x + blockIdx.x;
@@ -136,7 +203,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_rows8_kernel(const NormP
   // four writes its scale; blocks past the row are zero and give 0, the padding
   // of the blocked layout.
   const int first = grp.warp * 32 * V + lane;
-  const int pieces = (p.D >> 3) - first;       // live: 32 i < pieces
+  const int pieces = span.total - first;       // live: 32 i < pieces
   const int scaled = SAVE && (lane & 3) == 0 ? 16 * p.s_words - first : 0;
   int st = 0;
   uint32_t parity = 0;
@@ -151,7 +218,8 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_rows8_kernel(const NormP
     f32x2 s2 = 0, s3 = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const uint4 v = *reinterpret_cast<const uint4*>(row + i * 512);
+      uint4 v = *reinterpret_cast<const uint4*>(row + i * 512);
+      span.clear(v, first + 32 * i);
       get_pairs(v, x + 4 * i);
       s2 = add2(s2, add2(x[4 * i], x[4 * i + 1]));
       s3 = add2(s3, add2(x[4 * i + 2], x[4 * i + 3]));
@@ -181,9 +249,18 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_rows8_kernel(const NormP
       const float m = 32 * i < pieces ? -mean : 0.0f;      // padding stays 0
       const f32x2 m2 = pair(m, m);
 #pragma unroll
+      for (int j = 4 * i; j < 4 * i + 4; ++j) x[j] = add2(x[j], m2);
+      if (span.edge(first + 32 * i)) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float lo, hi;
+          unpair(x[4 * i + j], lo, hi);
+          const int e = 8 * (first + 32 * i) + 2 * j;
+          x[4 * i + j] = pair(span.holds(e) ? lo : 0.0f, span.holds(e + 1) ? hi : 0.0f);
+        }
+      }
+#pragma unroll
       for (int j = 4 * i; j < 4 * i + 4; j += 2) {
-        x[j] = add2(x[j], m2);
-        x[j + 1] = add2(x[j + 1], m2);
         s2 = fma2(x[j], x[j], s2);
         s3 = fma2(x[j + 1], x[j + 1], s3);
       }
@@ -194,15 +271,14 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_rows8_kernel(const NormP
       if (in_span(p.sp_rstd, p.rstd + r, 4)) p.rstd[r] = rstd;
     }
     const f32x2 r2 = pair(rstd, rstd);
-    uint16_t* y = p.y + r * p.D + first * 8;
+    uint16_t* y = p.y + r * p.D - span.lead;
     auto put = [&](int i, const f32x2* wv, const f32x2* bv) {
       f32x2 o[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[j] = fma2(mul2(x[4 * i + j], r2), wv[j], bv[j]);
-      if (32 * i < pieces && in_span(p.sp_y, y + i * 256, 16))
-        *reinterpret_cast<uint4*>(y + i * 256) = pack_pairs(o);
+      span.store(y, first + 32 * i, o, p.sp_y);
     };
-    if (p.staged) {
+    if (ODD || p.staged) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         f32x2 wv[4], bv[4];
@@ -242,79 +318,6 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_rows8_kernel(const NormP
   }
 }
 
-// Other rows, in pieces of two values or one.
-template <int VEC, typename W>
-__global__ void __launch_bounds__(kMaxThreads, 1) norm_kernel(const NormParams p) {
-  constexpr int V = kPer / VEC;
-  asm volatile("griddepcontrol.launch_dependents;");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  __shared__ float red[8 * 128];
-  for (int i = threadIdx.x; i < 8 * 128; i += blockDim.x) red[i] = 0.0f;
-  __syncthreads();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = warp / p.warps;
-  Group<32> grp{red + 128 * g, g + 1, p.warps, warp - g * p.warps, lane, 0};
-  const int T = 32 * p.warps, tid = grp.warp * 32 + lane;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * p.groups;
-  const float inv = 1.0f / static_cast<float>(p.D);
-  const W* w = static_cast<const W*>(p.w);
-  const W* b = static_cast<const W*>(p.b);
-
-  Piece<VEC> cur[V], nxt[V];
-  auto fetch = [&](int64_t r, Piece<VEC>(&d)[V]) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      d[i].zero();
-      const int c = (i * T + tid) * VEC;
-      if (r < p.M && c < p.D) d[i].load(p.x + r * p.D + c);
-    }
-  };
-  int64_t r = static_cast<int64_t>(blockIdx.x) * p.groups + g;
-  fetch(r, nxt);
-  for (; r < p.M; r += step) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) cur[i] = nxt[i];
-    fetch(r + step, nxt);
-    float x[kPer];
-    float sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      cur[i].get(x + i * VEC);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) sum += x[i * VEC + j];
-    }
-    const float mean = grp.sum(sum) * inv;
-    float sq = 0.0f;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const bool live = (i * T + tid) * VEC < p.D;
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        x[i * VEC + j] = live ? x[i * VEC + j] - mean : 0.0f;
-        sq += x[i * VEC + j] * x[i * VEC + j];
-      }
-    }
-    const float rstd = rsqrtf(grp.sum(sq) * inv + p.eps);
-    if (tid == 0) {
-      if (in_span(p.sp_mean, p.mean + r, 4)) p.mean[r] = mean;
-      if (in_span(p.sp_rstd, p.rstd + r, 4)) p.rstd[r] = rstd;
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = (i * T + tid) * VEC;
-      if (c >= p.D) continue;
-      float wv[VEC], bv[VEC], y[VEC];
-      load_param<VEC>(w + c, wv);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) bv[j] = 0.0f;
-      if (b) load_param<VEC>(b + c, bv);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) y[j] = x[i * VEC + j] * rstd * wv[j] + bv[j];
-      store_bf16<VEC>(p.y + r * p.D + c, y, p.sp_y);
-    }
-  }
-}
-
 struct NormBackParams {
   const uint16_t* dy;
   const uint16_t* x;
@@ -324,9 +327,9 @@ struct NormBackParams {
   const float* mean;
   const float* rstd;
   uint16_t* dx;
-  float* parts;        // [grid][2][D]
+  float* parts;        // [grid][2][D padded to 4]
   int64_t M;
-  int D, warps, groups;
+  int D;
   RowShape shape;
   int s_words;
   Span sp_dx, sp_parts;
@@ -337,8 +340,8 @@ struct NormBackParams {
 // EPT values a thread.  The second pass reads the row from shared memory again:
 // with dw and db in 2 EPT registers there is no room for more of the row (16
 // values a thread, held from the first pass: 117 us where this takes 85).
-template <bool SAVE, typename W, int EPT>
-__global__ void __launch_bounds__(kBackThreads, 1) norm_back_rows8_kernel(const NormBackParams p) {
+template <bool SAVE, bool ODD, typename W, int EPT>
+__global__ void __launch_bounds__(kBackThreads, 1) norm_back_kernel(const NormBackParams p) {
   constexpr int V = EPT / 8;
   asm volatile("griddepcontrol.launch_dependents;");
   extern __shared__ __align__(128) uint8_t ring[];
@@ -347,16 +350,20 @@ __global__ void __launch_bounds__(kBackThreads, 1) norm_back_rows8_kernel(const 
   __shared__ __align__(8) uint64_t stall_bar;   // diagnostic: never completed
   __shared__ int abort_flag;
   const RowShape& sh = p.shape;
+  const RowSpan<ODD> span(p.D);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = warp / sh.warps;
   Group<16> grp{red + 128 * g, g + 1, sh.warps, warp - g * sh.warps, lane, 0};
   const int T = 32 * sh.warps, tid = grp.warp * 32 + lane;
   const int x_at = 2 * sh.pitch, stage_bytes = (SAVE ? 3 : 4) * sh.pitch;
-  const int ring_bytes = sh.groups * sh.stages * stage_bytes;
-  ring_setup(ring, ring_bytes, full, sh.groups * sh.stages, &stall_bar, &abort_flag, red);
+  const int places = sh.groups * sh.stages;
+  ring_setup(full, places, &stall_bar, &abort_flag, red);
+  clear_padding(ring, places, stage_bytes, 16 * span.total, 2 * sh.pitch);
+  clear_padding(ring + x_at, places, stage_bytes, SAVE ? p.D : 16 * span.total,
+                SAVE ? sh.pitch : 2 * sh.pitch);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  float* params = reinterpret_cast<float*>(ring + ring_bytes);   // w
-  stage_params(params, static_cast<const W*>(p.w), p.D, sh.pitch);
+  float* params = reinterpret_cast<float*>(ring + places * stage_bytes);   // w
+  stage_params<ODD>(params, static_cast<const W*>(p.w), span.lead, p.D, sh.pitch);
   __syncthreads();
 
   uint8_t* mine = ring + g * sh.stages * stage_bytes;
@@ -364,12 +371,20 @@ __global__ void __launch_bounds__(kBackThreads, 1) norm_back_rows8_kernel(const 
   volatile int* aborted = &abort_flag;
   auto issue = [&](int st, int64_t r) {
     uint8_t* to = mine + st * stage_bytes;
-    mbar_arrive_expect_tx(&bars[st], (SAVE ? 3 : 4) * p.D);
-    bulk_load(to, p.dy + r * p.D, 2 * p.D, &bars[st]);
-    if (SAVE)
+    if (SAVE) {
+      mbar_arrive_expect_tx(&bars[st], 3 * p.D);
+      bulk_load(to, p.dy + r * p.D, 2 * p.D, &bars[st]);
       bulk_load(to + x_at, p.q + r * p.D, p.D, &bars[st]);
-    else
-      bulk_load(to + x_at, p.x + r * p.D, 2 * p.D, &bars[st]);
+      return;
+    }
+    const int64_t at = r * p.D - span.lead;
+    const int bytes = span.copy_bytes(r, p.M, p.D);
+    span.copy_tail(to, p.dy + at, bytes);
+    span.copy_tail(to + x_at, p.x + at, bytes);
+    mbar_arrive_expect_tx(&bars[st], 2 * bytes);
+    if (ODD && bytes == 0) return;
+    bulk_load(to, p.dy + at, bytes, &bars[st]);
+    bulk_load(to + x_at, p.x + at, bytes, &bars[st]);
   };
   // Groups of a CTA are a grid apart, so that few rows spread over all CTAs.
   const int64_t r0 = static_cast<int64_t>(g) * gridDim.x + blockIdx.x;
@@ -389,7 +404,6 @@ __global__ void __launch_bounds__(kBackThreads, 1) norm_back_rows8_kernel(const 
   // Piece i of this thread is piece first + 32 i of the row (a warp's pieces lie
   // together, so that their distances are constants).
   const int first = grp.warp * 32 * V + lane;
-  const int pieces = (p.D >> 3) - first;       // live: 32 i < pieces
   // What the copies do not bring, a row ahead; without a condition, for loads
   // under one are waited for where it ends.  A warp's scales are 2 V words of
   // four, one to a lane (past the row its last word: the values there are 0).
@@ -437,17 +451,24 @@ __global__ void __launch_bounds__(kBackThreads, 1) norm_back_rows8_kernel(const 
           xv[j] = fma2(pair(lo, hi), m, ms);
         }
       } else {
-        get_pairs(*reinterpret_cast<const uint4*>(sx + i * 512), xv);
+        uint4 v = *reinterpret_cast<const uint4*>(sx + i * 512);
+        span.clear(v, first + 32 * i);
+        get_pairs(v, xv);
 #pragma unroll
         for (int j = 0; j < 4; ++j) xv[j] = add2(xv[j], ms);
       }
+    };
+    auto get_dy = [&](int i, f32x2* d) {
+      uint4 v = *reinterpret_cast<const uint4*>(sd + i * 512);
+      span.clear(v, first + 32 * i);
+      get_pairs(v, d);
     };
     f32x2 s1 = 0, s2 = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       f32x2 xv[4], d[4], wv[4];
       get_x(i, xv);
-      get_pairs(*reinterpret_cast<const uint4*>(sd + i * 512), d);
+      get_dy(i, d);
       staged_pairs(params, sh.pitch, first + 32 * i, wv);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -464,17 +485,16 @@ __global__ void __launch_bounds__(kBackThreads, 1) norm_back_rows8_kernel(const 
     // dx = rstd g - rstd c1 - (x - mean) rstd^2 c2
     const float c1 = -rstd * (t.x * inv), c2 = -rstd * (t.y * inv) * rstd;
     const f32x2 k1 = pair(c1, c1), k2 = pair(c2, c2);
-    uint16_t* dx = p.dx + r * p.D + first * 8;
+    uint16_t* dx = p.dx + r * p.D - span.lead;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       f32x2 xv[4], d[4], wv[4];
       get_x(i, xv);
-      get_pairs(*reinterpret_cast<const uint4*>(sd + i * 512), d);
+      get_dy(i, d);
       staged_pairs(params, sh.pitch, first + 32 * i, wv);
 #pragma unroll
       for (int j = 0; j < 4; ++j) d[j] = fma2(xv[j], k2, fma2(mul2(d[j], wv[j]), rs, k1));
-      if (32 * i < pieces && in_span(p.sp_dx, dx + i * 256, 16))
-        *reinterpret_cast<uint4*>(dx + i * 256) = pack_pairs(d);
+      span.store(dx, first + 32 * i, d, p.sp_dx);
     }
     grp.meet();
     // Every thread of the group has read the row: fill its place again.
@@ -498,177 +518,72 @@ __global__ void __launch_bounds__(kBackThreads, 1) norm_back_rows8_kernel(const 
     atomicOr(&g_norm_watchdog, 1);
   }
   // This CTA's partial sums: its groups' in order, through shared memory.
-  float* part = p.parts + static_cast<int64_t>(blockIdx.x) * 2 * p.D;
-  if (sh.groups > 1) {
-    float* sums = reinterpret_cast<float*>(ring);
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < EPT / 2; ++k) {
-      float lo, hi;
-      unpair(dw[k], lo, hi);
-      sums[(g * 2 * EPT + 2 * k) * T + tid] = lo;
-      sums[(g * 2 * EPT + 2 * k + 1) * T + tid] = hi;
-      unpair(db[k], lo, hi);
-      sums[(g * 2 * EPT + EPT + 2 * k) * T + tid] = lo;
-      sums[(g * 2 * EPT + EPT + 2 * k + 1) * T + tid] = hi;
-    }
-    __syncthreads();
-    for (int k = threadIdx.x; k < 2 * EPT * T; k += blockDim.x) {
-      const int v = k / T, id = k - v * T;                // value v of thread id
-      const int c = ((id >> 5) * 32 * V + ((v % EPT) >> 3) * 32 + (id & 31)) * 8 + (v & 7);
-      if (c >= p.D) continue;
-      float a = 0.0f;
-      for (int h = 0; h < sh.groups; ++h) a += sums[h * 2 * EPT * T + k];
-      float* at = part + (v < EPT ? 0 : p.D) + c;
-      if (in_span(p.sp_parts, at, 4)) *at = a;
-    }
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int c = (first + 32 * i) * 8;
-    if (c >= p.D || !in_span(p.sp_parts, part + p.D + c, 32)) continue;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      *reinterpret_cast<ulonglong2*>(part + c + 4 * j) = make_ulonglong2(dw[4 * i + 2 * j], dw[4 * i + 2 * j + 1]);
-      *reinterpret_cast<ulonglong2*>(part + p.D + c + 4 * j) = make_ulonglong2(db[4 * i + 2 * j], db[4 * i + 2 * j + 1]);
-    }
-  }
-}
-
-// Other rows, in pieces of two values or one.  MAXT: 512 threads with the
-// registers they need, or 1024 for rows of more than 8192 values.
-template <int VEC, typename W, int MAXT>
-__global__ void __launch_bounds__(MAXT, 1) norm_back_kernel(const NormBackParams p) {
-  constexpr int V = kPer / VEC;
-  asm volatile("griddepcontrol.launch_dependents;");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  extern __shared__ float sums[];            // groups > 1: 2 x padded row
-  __shared__ float red[8 * 128];
-  for (int i = threadIdx.x; i < 8 * 128; i += blockDim.x) red[i] = 0.0f;
+  const int pitch = (p.D + 3) & ~3;
+  float* part = p.parts + static_cast<int64_t>(blockIdx.x) * 2 * pitch;
+  // Value v of thread tid at (v T' + tid), T' = T + 4: the writes by v and the
+  // reads by column (eight values of a thread, then the next thread's) are both
+  // free of bank conflicts, and the partial sums leave in whole lines.
+  float* sums = reinterpret_cast<float*>(ring);
+  const int stride = T + 4, all = 2 * EPT * stride;
   __syncthreads();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = warp / p.warps;
-  Group<32> grp{red + 128 * g, g + 1, p.warps, warp - g * p.warps, lane, 0};
-  const int T = 32 * p.warps, tid = grp.warp * 32 + lane;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * p.groups;
-  const float inv = 1.0f / static_cast<float>(p.D);
-  const W* w = static_cast<const W*>(p.w);
-  float dw[kPer] = {}, db[kPer] = {};
-  for (int64_t r = static_cast<int64_t>(blockIdx.x) * p.groups + g; r < p.M; r += step) {
-    float xh[kPer], dy[kPer], gr[kPer];
-    const float mean = __ldg(p.mean + r), rstd = __ldg(p.rstd + r);
-    float s1 = 0.0f, s2 = 0.0f;
-    Piece<VEC> pd[V], px[V];
+  float* to = sums + g * all + tid;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = (i * T + tid) * VEC;
-      pd[i].zero();
-      px[i].zero();
-      if (c >= p.D) continue;
-      pd[i].load(p.dy + r * p.D + c);
-      px[i].load(p.x + r * p.D + c);
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = (i * T + tid) * VEC;
-      const bool live = c < p.D;
-      float wv[VEC];
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) wv[j] = 0.0f;
-      if (live) load_param<VEC>(w + c, wv);
-      pd[i].get(dy + i * VEC);
-      px[i].get(xh + i * VEC);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        const int k = i * VEC + j;
-        xh[k] = live ? (xh[k] - mean) * rstd : 0.0f;
-        gr[k] = dy[k] * wv[j];
-        s1 += gr[k];
-        s2 += gr[k] * xh[k];
-        dw[k] += dy[k] * xh[k];
-        db[k] += dy[k];
-      }
-    }
-    const float2 t = grp.sum2(s1, s2);
-    const float c1 = t.x * inv, c2 = t.y * inv;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = (i * T + tid) * VEC;
-      if (c >= p.D) continue;
-      float d[VEC];
-#pragma unroll
-      for (int j = 0; j < VEC; ++j)
-        d[j] = rstd * (gr[i * VEC + j] - c1 - xh[i * VEC + j] * c2);
-      store_bf16<VEC>(p.dx + r * p.D + c, d, p.sp_dx);
-    }
+  for (int k = 0; k < EPT / 2; ++k) {
+    unpair(dw[k], to[2 * k * stride], to[(2 * k + 1) * stride]);
+    unpair(db[k], to[(EPT + 2 * k) * stride], to[(EPT + 2 * k + 1) * stride]);
   }
-  // Groups of the CTA in order into group 0, then this CTA's partial sums.
-  for (int k = 1; k < p.groups; ++k) {
-    __syncthreads();
-    if (g == k)
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        sums[i * T + tid] = dw[i];
-        sums[(kPer + i) * T + tid] = db[i];
-      }
-    __syncthreads();
-    if (g == 0)
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        dw[i] += sums[i * T + tid];
-        db[i] += sums[(kPer + i) * T + tid];
-      }
-  }
-  if (g != 0) return;
-  float* part = p.parts + static_cast<int64_t>(blockIdx.x) * 2 * p.D;
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int c = (i * T + tid) * VEC;
-    if (c >= p.D || !in_span(p.sp_parts, part + p.D + c, 4 * VEC)) continue;
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      part[c + j] = dw[i * VEC + j];
-      part[p.D + c + j] = db[i * VEC + j];
+  __syncthreads();
+  for (int e = threadIdx.x; e < span.width; e += blockDim.x) {
+    if (!span.holds(e)) continue;
+    const int c = e >> 3;                                 // piece: warp, i, lane
+    const int v = (c >> 5) % V * 8 + (e & 7), id = (c >> 5) / V * 32 + (c & 31);
+    const float* s = sums + v * stride + id;
+    float a = 0.0f, b = 0.0f;
+    for (int h = 0; h < sh.groups; ++h, s += all) {
+      a += s[0];
+      b += s[EPT * stride];
     }
+    float* at = part + e - span.lead;
+    if (in_span(p.sp_parts, at, 4)) *at = a;
+    if (in_span(p.sp_parts, at + pitch, 4)) at[pitch] = b;
   }
 }
 
-// dw (blockIdx.y == 0) and db: 32 columns a CTA, in pieces of VEC; each of its
-// threads adds up a run of the partial sums, eight under way at a time, then the
-// runs are added up in order.
-template <int VEC, typename W>
+// dw (blockIdx.y == 0) and db: 32 columns a CTA, four to a thread; each thread
+// adds up a run of the partial sums, six under way at a time, then the runs are
+// added up in order.
+template <typename W>
 __global__ void __launch_bounds__(256) norm_grad_kernel(const float* parts, int n, int D, W* dw,
                                                         W* db, Span sp_dw, Span sp_db) {
   asm volatile("griddepcontrol.launch_dependents;");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  constexpr int kCols = 32 / VEC, kRuns = 256 / kCols;
+  constexpr int kRuns = 32, kAtOnce = 6;
   __shared__ float run[kRuns][33];
-  const int l = threadIdx.x % kCols, k = threadIdx.x / kCols;
-  const int c = blockIdx.x * 32 + l * VEC;
-  const float* src = parts + (blockIdx.y ? D : 0) + c;
-  float v[VEC] = {};
+  const int l = threadIdx.x & 7, k = threadIdx.x >> 3;
+  const int pitch = (D + 3) & ~3, c = blockIdx.x * 32 + l * 4;
+  const float* src = parts + (blockIdx.y ? pitch : 0) + c;
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (c < D)
-    for (int i = k; i < n; i += 8 * kRuns) {
-      float u[8][VEC];
+    for (int i = k; i < n; i += kAtOnce * kRuns) {
+      float4 u[kAtOnce];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < kAtOnce; ++j) {
         const int q = i + j * kRuns;
-        if constexpr (VEC == 4) {
-          const float4 f = q < n ? __ldcg(reinterpret_cast<const float4*>(src + static_cast<int64_t>(q) * 2 * D))
-                                 : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          u[j][0] = f.x; u[j][1] = f.y; u[j][2] = f.z; u[j][3] = f.w;
-        } else {
-          u[j][0] = q < n ? __ldcg(src + static_cast<int64_t>(q) * 2 * D) : 0.0f;
-        }
+        u[j] = q < n ? __ldcg(reinterpret_cast<const float4*>(src + static_cast<int64_t>(q) * 2 * pitch))
+                     : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) v[e] += u[j][e];
+      for (int j = 0; j < kAtOnce; ++j) {
+        v.x += u[j].x;
+        v.y += u[j].y;
+        v.z += u[j].z;
+        v.w += u[j].w;
+      }
     }
-#pragma unroll
-  for (int e = 0; e < VEC; ++e) run[k][l * VEC + e] = v[e];
+  run[k][4 * l] = v.x;
+  run[k][4 * l + 1] = v.y;
+  run[k][4 * l + 2] = v.z;
+  run[k][4 * l + 3] = v.w;
   __syncthreads();
   const int o = blockIdx.x * 32 + threadIdx.x;
   if (threadIdx.x >= 32 || o >= D) return;
@@ -696,40 +611,31 @@ int launch(void (*kernel)(A...), dim3 grid, int threads, int smem, cudaStream_t 
   return static_cast<int>(cudaLaunchKernelEx(&cfg, kernel, args...));
 }
 
-// Warps of a row's group of `per` values a thread, and groups of a CTA: `most`
-// warps' worth.
-void shape_of(int64_t D, int per, int most, int* warps, int* groups) {
-  *warps = static_cast<int>((D + 32 * per - 1) / (32 * per));
-  *groups = *warps < most ? most / *warps : 1;
-}
-
-template <typename K>
-int run_norm(K kernel, NormParams p, int num_sms, cudaStream_t stream) {
-  shape_of(p.D, kPer, 8, &p.warps, &p.groups);
-  const int threads = 32 * p.warps * p.groups;
-  int per = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, 0) != cudaSuccess ||
-      per < 1)
-    per = 1;
-  const int64_t want = (p.M + p.groups - 1) / p.groups;
-  const int64_t most = static_cast<int64_t>(num_sms) * per;
-  return launch(kernel, static_cast<int>(want < most ? want : most), threads, 0, stream, p);
-}
-
-// The shape for M rows of D values, `row` bytes a padded value of a stage and
-// `param` bytes a value of the parameters: as many groups as fit in `threads` and
-// have rows to work on, as many stages as fit.
-RowShape ring_shape(int64_t M, int64_t D, int ept, int threads, int row, int param, int num_sms) {
+// The shape for M rows of `width` values (the largest lead included), EPT values a
+// thread, `row` bytes a padded value of a stage and `param` bytes a value of the
+// parameters: as many groups as fit in `threads` and have rows to work on, as many
+// stages as fit.
+RowShape ring_shape(int64_t M, int64_t width, int ept, int threads, int row, int param,
+                    int num_sms) {
   RowShape s = {};
-  shape_of(D, ept, threads / 32, &s.warps, &s.groups);
+  s.warps = static_cast<int>((width + 32 * ept - 1) / (32 * ept));
+  s.groups = s.warps < threads / 32 ? threads / 32 / s.warps : 1;
   const int64_t rows = (M + num_sms - 1) / num_sms;
   if (s.groups > rows) s.groups = static_cast<int>(rows);
-  if (s.warps > 1 && s.groups > 15) s.groups = 15;   // named barriers
   s.pitch = 32 * s.warps * ept;
   const int64_t room = kRingBytes - static_cast<int64_t>(param) * s.pitch;
   s.stages = static_cast<int>(room / (static_cast<int64_t>(s.groups) * row * s.pitch));
   if (s.stages > kMaxStages) s.stages = kMaxStages;
   return s;
+}
+
+// CTAs: one an SM, no more than rows; with a lead, a multiple of 8.
+int grid_of(int64_t M, bool odd, int num_sms) {
+  int64_t most = num_sms < kNormMaxParts ? num_sms : kNormMaxParts;
+  if (!odd) return static_cast<int>(M < most ? M : most);
+  most = most < 8 ? 8 : most & ~int64_t{7};
+  const int64_t want = (M + 7) & ~int64_t{7};
+  return static_cast<int>(want < most ? want : most);
 }
 
 template <typename K>
@@ -738,101 +644,94 @@ int allow_ring(K kernel) {
       kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes));
 }
 
-template <bool SAVE, typename W, int EPT>
-int run_norm_rows8(NormParams p, int num_sms, cudaStream_t stream) {
+template <bool SAVE, bool ODD, typename W, int EPT>
+int run_norm(NormParams p, int num_sms, cudaStream_t stream) {
   // With a row or two a group, w and b are not worth a copy of their own.
-  p.staged = p.M > 8 * static_cast<int64_t>(num_sms);
+  p.staged = ODD || p.M > 8 * static_cast<int64_t>(num_sms);
   const int param = p.staged ? 8 : 0;
-  p.shape = ring_shape(p.M, p.D, EPT, kRingThreads, 2, param, num_sms);
+  p.shape = ring_shape(p.M, p.D + (ODD ? 7 : 0), EPT, kRingThreads, 2, param, num_sms);
   const int64_t smem = static_cast<int64_t>(p.shape.pitch) *
                        (p.shape.groups * p.shape.stages * 2 + param);
   static DeviceCache attr_cache;
-  const int attr = attr_cache.get([] { return allow_ring(norm_rows8_kernel<SAVE, W, EPT>); });
+  const int attr = attr_cache.get([] { return allow_ring(norm_kernel<SAVE, ODD, W, EPT>); });
   if (attr != 0) return attr;
   const Stall stall = take_stall();
   p.stall_at = stall.at;
   p.stall_ns = stall.ns;
-  return launch(norm_rows8_kernel<SAVE, W, EPT>, static_cast<int>(p.M < num_sms ? p.M : num_sms),
+  return launch(norm_kernel<SAVE, ODD, W, EPT>, dim3(grid_of(p.M, ODD, num_sms)),
                 32 * p.shape.warps * p.shape.groups, static_cast<int>(smem), stream, p);
 }
 
-template <int VEC, typename W>
+template <bool SAVE, bool ODD, typename W, int EPT>
 int run_norm_back(NormBackParams p, int num_sms, int* grid, cudaStream_t stream) {
-  shape_of(p.D, kPer, 8, &p.warps, &p.groups);
-  const int threads = 32 * p.warps * p.groups;
-  const int smem = p.groups > 1 ? 2 * kPer * 32 * p.warps * 4 : 0;
-  const int64_t want = (p.M + p.groups - 1) / p.groups;
-  int64_t most = 2 * static_cast<int64_t>(num_sms);
-  if (most > kNormMaxParts) most = kNormMaxParts;
-  *grid = static_cast<int>(want < most ? want : most);
-  return threads <= 512 ? launch(norm_back_kernel<VEC, W, 512>, *grid, threads, smem, stream, p)
-                        : launch(norm_back_kernel<VEC, W, 1024>, *grid, threads, smem, stream, p);
-}
-
-template <bool SAVE, typename W, int EPT>
-int run_norm_back_rows8(NormBackParams p, int num_sms, int* grid, cudaStream_t stream) {
-  p.shape = ring_shape(p.M, p.D, EPT, kBackThreads, SAVE ? 3 : 4, 4, num_sms);
+  constexpr int kRow = SAVE ? 3 : 4;
+  p.shape = ring_shape(p.M, p.D + (ODD ? 7 : 0), EPT, kBackThreads, kRow, 4, num_sms);
   const RowShape& s = p.shape;
-  int64_t smem = static_cast<int64_t>(s.pitch) * (s.groups * s.stages * (SAVE ? 3 : 4) + 4);
-  const int64_t sums = s.groups > 1 ? int64_t{8} * s.pitch * s.groups : 0;
+  int64_t smem = static_cast<int64_t>(s.pitch) * (s.groups * s.stages * kRow + 4);
+  const int64_t sums = int64_t{8} * EPT * (32 * s.warps + 4) * s.groups;
   if (smem < sums) smem = sums;
   static DeviceCache attr_cache;
-  const int attr =
-      attr_cache.get([] { return allow_ring(norm_back_rows8_kernel<SAVE, W, EPT>); });
+  const int attr = attr_cache.get([] { return allow_ring(norm_back_kernel<SAVE, ODD, W, EPT>); });
   if (attr != 0) return attr;
-  int64_t most = num_sms;
-  if (most > kNormMaxParts) most = kNormMaxParts;
-  *grid = static_cast<int>(p.M < most ? p.M : most);
+  *grid = grid_of(p.M, ODD, num_sms);
   const Stall stall = take_stall();
   p.stall_at = stall.at;
   p.stall_ns = stall.ns;
-  return launch(norm_back_rows8_kernel<SAVE, W, EPT>, *grid, 32 * s.warps * s.groups,
+  return launch(norm_back_kernel<SAVE, ODD, W, EPT>, dim3(*grid), 32 * s.warps * s.groups,
                 static_cast<int>(smem), stream, p);
 }
 
-// 32 values a thread; fewer where one warp then holds the row all the same.
-template <bool SAVE, typename W>
+// 32 values a thread (16 warps then hold a row of 16384); fewer where one warp
+// holds the row all the same, more for the few widths that need it for their lead.
+template <bool SAVE, bool ODD, typename W>
 int pick_norm(const NormParams& p, int num_sms, cudaStream_t stream) {
-  if (p.D <= 256) return run_norm_rows8<SAVE, W, 8>(p, num_sms, stream);
-  if (p.D <= 512) return run_norm_rows8<SAVE, W, 16>(p, num_sms, stream);
-  return run_norm_rows8<SAVE, W, 32>(p, num_sms, stream);
+  const int width = p.D + (ODD ? 7 : 0);
+  if (width <= 256) return run_norm<SAVE, ODD, W, 8>(p, num_sms, stream);
+  if (width <= 512) return run_norm<SAVE, ODD, W, 16>(p, num_sms, stream);
+  if constexpr (ODD)
+    if (width > kNormMaxWidth) return run_norm<SAVE, ODD, W, 40>(p, num_sms, stream);
+  return run_norm<SAVE, ODD, W, 32>(p, num_sms, stream);
 }
 
-template <bool SAVE, typename W>
+template <bool SAVE, bool ODD, typename W>
 int pick_norm_back(const NormBackParams& p, int num_sms, int* grid, cudaStream_t stream) {
-  if (p.D <= 256) return run_norm_back_rows8<SAVE, W, 8>(p, num_sms, grid, stream);
-  if (p.D <= 512) return run_norm_back_rows8<SAVE, W, 16>(p, num_sms, grid, stream);
-  return run_norm_back_rows8<SAVE, W, 32>(p, num_sms, grid, stream);
+  const int width = p.D + (ODD ? 7 : 0);
+  if (width <= 256) return run_norm_back<SAVE, ODD, W, 8>(p, num_sms, grid, stream);
+  if (width <= 512) return run_norm_back<SAVE, ODD, W, 16>(p, num_sms, grid, stream);
+  if constexpr (ODD)
+    if (width > kNormMaxWidth) return run_norm_back<SAVE, ODD, W, 40>(p, num_sms, grid, stream);
+  return run_norm_back<SAVE, ODD, W, 32>(p, num_sms, grid, stream);
 }
 
 template <typename W>
 int run_back(const NormBackParams& p, int num_sms, int* grid, cudaStream_t stream) {
-  if (p.q) return pick_norm_back<true, W>(p, num_sms, grid, stream);
-  if (p.D % 8 == 0) return pick_norm_back<false, W>(p, num_sms, grid, stream);
-  return p.D % 2 == 0 ? run_norm_back<2, W>(p, num_sms, grid, stream)
-                      : run_norm_back<1, W>(p, num_sms, grid, stream);
+  if (p.q) return pick_norm_back<true, false, W>(p, num_sms, grid, stream);
+  return p.D % 8 == 0 ? pick_norm_back<false, false, W>(p, num_sms, grid, stream)
+                      : pick_norm_back<false, true, W>(p, num_sms, grid, stream);
 }
 
 template <typename W>
 int run_forward(const NormParams& p, int num_sms, cudaStream_t stream) {
-  if (p.q) return pick_norm<true, W>(p, num_sms, stream);
-  if (p.D % 8 == 0) return pick_norm<false, W>(p, num_sms, stream);
-  return p.D % 2 == 0 ? run_norm(norm_kernel<2, W>, p, num_sms, stream)
-                      : run_norm(norm_kernel<1, W>, p, num_sms, stream);
+  if (p.q) return pick_norm<true, false, W>(p, num_sms, stream);
+  return p.D % 8 == 0 ? pick_norm<false, false, W>(p, num_sms, stream)
+                      : pick_norm<false, true, W>(p, num_sms, stream);
 }
 
 template <typename W>
 int run_grad(const LayerNormBackArgs& a, int D, int n, cudaStream_t stream) {
   const dim3 grid(static_cast<unsigned>((D + 31) / 32), a.db ? 2 : 1);
   const uint64_t bytes = static_cast<uint64_t>(D) * sizeof(W);
-  return launch(D % 4 == 0 ? norm_grad_kernel<4, W> : norm_grad_kernel<1, W>, grid, 256, 0, stream,
+  return launch(norm_grad_kernel<W>, grid, 256, 0, stream,
                 static_cast<const float*>(a.work), n, D, static_cast<W*>(a.dw),
                 static_cast<W*>(a.db), make_span(a.dw, bytes), make_span(a.db, bytes));
 }
 
 }  // namespace
 
-int64_t norm_back_parts(int64_t M) { return M < kNormMaxParts ? M : kNormMaxParts; }
+int64_t norm_back_work_floats(int64_t M, int64_t D) {
+  const int64_t ctas = D % 8 == 0 ? M : (M + 7) & ~int64_t{7};
+  return (ctas < kNormMaxParts ? ctas : kNormMaxParts) * 2 * ((D + 3) & ~int64_t{3});
+}
 
 int launch_layer_norm(const LayerNormArgs& a, int num_sms, cudaStream_t stream) {
   NormParams p = {};
@@ -872,7 +771,7 @@ int launch_layer_norm_backward(const LayerNormBackArgs& a, int num_sms, cudaStre
   p.D = static_cast<int>(a.D);
   p.s_words = static_cast<int>((a.D + 127) / 128);
   p.sp_dx = make_span(a.dx, 2 * static_cast<uint64_t>(a.M) * static_cast<uint64_t>(a.D));
-  p.sp_parts = make_span(a.work, static_cast<uint64_t>(norm_back_parts(a.M)) * 8 * a.D);
+  p.sp_parts = make_span(a.work, 4 * static_cast<uint64_t>(norm_back_work_floats(a.M, a.D)));
   int grid = 0;
   const int rc = a.w_f32 ? run_back<float>(p, num_sms, &grid, stream)
                          : run_back<uint16_t>(p, num_sms, &grid, stream);

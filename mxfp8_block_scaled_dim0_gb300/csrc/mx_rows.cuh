@@ -217,14 +217,27 @@ __device__ __forceinline__ void load_param_pairs(const uint16_t* p, f32x2* v) {
   get_pairs(__ldg(reinterpret_cast<const uint4*>(p)), v);
 }
 
-// D parameters in shared memory as fp32, zeros from D to `pitch`; the first and
-// the last four of every eight in halves of their own: a warp's 16-byte reads of
-// neighbouring pieces are then free of bank conflicts.
-template <typename W>
-__device__ __forceinline__ void stage_params(float* dst, const W* src, int D, int pitch) {
+// D parameters in shared memory as fp32, from place `lead` on (ODD; otherwise 0),
+// zeros before and up to `pitch`; the first and the last four of every eight in
+// halves of their own: a warp's 16-byte reads of neighbouring pieces are then
+// free of bank conflicts.
+template <bool ODD, typename W>
+__device__ __forceinline__ void stage_params(float* dst, const W* src, int lead, int D, int pitch) {
   for (int c = threadIdx.x; c < pitch / 8; c += blockDim.x) {
     f32x2 v[4] = {0, 0, 0, 0};
-    if (8 * c < D) load_param_pairs(src + 8 * c, v);
+    if constexpr (ODD) {
+      float f[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int e = 8 * c + j - lead;
+        f[j] = 0.0f;
+        if (e >= 0 && e < D) load_param<1>(src + e, f + j);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = pair(f[2 * j], f[2 * j + 1]);
+    } else if (8 * c < D) {
+      load_param_pairs(src + 8 * c, v);
+    }
     reinterpret_cast<ulonglong2*>(dst)[c] = make_ulonglong2(v[0], v[1]);
     reinterpret_cast<ulonglong2*>(dst)[pitch / 8 + c] = make_ulonglong2(v[2], v[3]);
   }

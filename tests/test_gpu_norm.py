@@ -69,7 +69,7 @@ def check_forward(x, w, b, got, eps=EPS):
     assert bool(((y.double() - y64).abs() <= tol * (1 + 2.0 ** -7)).all())
 
 
-ODD = [(1, 1), (2, 3), (1, 7), (5, 31), (3, 130), (33, 257), (7, 1021), (9, 1022), (4, 4099),
+ODD = [(1, 1), (2, 3), (9, 1), (1300, 5), (2500, 12), (1219, 250), (640, 514), (165, 1020), (1, 7), (5, 31), (3, 130), (33, 257), (7, 1021), (9, 1022), (4, 4099),
        (2, 16383), (3, 16382)]
 EVEN = [(1, 32), (1, 4096), (129, 96), (31, 160), (300, 512), (5, 544), (130, 1024), (65, 1056),
         (40, 5120), (17, 8192), (3, 16384), (700, 64), (9, 16360)]
@@ -130,6 +130,24 @@ def test_inf_and_nan_stay_in_their_rows():
     check_forward(x[good], w, b, (y[good], mean[good], rstd[good]))
     q0, s0 = mx.cast_dim0(x)
     assert torch.equal(q, q0) and torch.equal(s, s0)
+
+
+@pytest.mark.parametrize("D", [1, 13, 127, 254, 637, 1028, 4100])
+def test_neighbours_of_rows_off_the_boundary(D):
+    """Rows that do not begin on 16 bytes: what a copy brings of a row's
+    neighbours, NaN here, reaches neither its results nor theirs."""
+    M = 40
+    x, dy = rnd((M, D), 3, shift=1.0), rnd((M, D), 4)
+    w, b = rnd((D,), 1, F32), rnd((D,), 2, F32)
+    mean, rstd = stats(x)
+    xn, dyn, mn, rn = x.clone(), dy.clone(), mean.clone(), rstd.clone()
+    xn[1::2], dyn[1::2], mn[1::2], rn[1::2] = (float("nan"),) * 4
+    y = forward(xn, w, b, False)[0]
+    assert bool(torch.isnan(y[1::2]).all())
+    assert torch.equal(y[::2], forward(x, w, b, False)[0][::2])
+    dx = backward(dyn, xn, None, w, mn, rn)[0]
+    assert bool(torch.isnan(dx[1::2]).all())
+    assert torch.equal(dx[::2], backward(dy, x, None, w, mean, rstd)[0][::2])
 
 
 # ---- backward ------------------------------------------------------------------

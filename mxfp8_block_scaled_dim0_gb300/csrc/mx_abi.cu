@@ -450,7 +450,9 @@ int mx_matmul(const void* qa, const void* sa_blk, const void* qb, const void* sb
   const int64_t tiles_k = cdiv(K, 128);
   auto operand = [&](CUtensorMap* m, const void* q, int64_t rows, bool mn) {
     return encode_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, q, mn ? rows : K, mn ? K : rows,
-                     mn ? rows : K, 128, 128, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+                     mn ? rows : K, 128,
+                     static_cast<uint32_t>(pairs ? 128 : mx::matmul_box_rows(rows, mn)),
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
   };
   auto scales = [&](CUtensorMap* m, const void* s, int64_t rows, uint32_t box) {
     return encode_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, s, tiles_k * 128, cdiv(rows, 128),
@@ -461,7 +463,7 @@ int mx_matmul(const void* qa, const void* sa_blk, const void* qb, const void* sb
   if (int rc = operand(&maps.b, qb, N, b_mn)) return rc;
   if (int rc = scales(&maps.sa, sa_blk, M, 1)) return rc;
   if (int rc = scales(&maps.sb, sb_blk, N, pairs ? 2 : 1)) return rc;
-  if (!pairs) {
+  if (!mx::matmul_mapped(N, f32)) {
     maps.out = maps.a;
   } else if (int rc = encode_2d(&maps.out,
                                 f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32

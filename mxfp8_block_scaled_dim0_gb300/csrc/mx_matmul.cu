@@ -46,10 +46,25 @@ namespace {
 
 __device__ int g_matmul_watchdog = 0;
 
+}  // namespace
+
+// Rows of an operand's load box in the tile kernel: no more than there are (a box
+// past the operand's end is filled with zeros at the price of a load).  What a
+// narrower box leaves in shared memory only reaches results that are not stored.
+int matmul_box_rows(int64_t rows, bool mn) {
+  return mn || rows >= 128 ? 128 : static_cast<int>((rows + 7) & ~int64_t{7});
+}
+
+// Whether a tensor map can describe rows of N results.
+bool matmul_mapped(int64_t N, bool out_f32) { return (N * (out_f32 ? 4 : 2)) % 16 == 0; }
+
+namespace {
+
 constexpr int kBK = 128;                    // contraction bytes of one stage
 constexpr int kTile = 128;                  // rows of one operand box
 constexpr int kBoxBytes = kTile * kBK;      // 16 KB
 constexpr int kSfBytes = 512;               // one 128x4 blocked scale tile
+constexpr int kStageOut = 4096;             // 32 rows x 128 bytes on their way out
 
 struct MatmulParams {
   void* out;
@@ -58,10 +73,13 @@ struct MatmulParams {
   int last_steps;      // 32-step MMAs of the last block, 1..4
   int m_tiles, n_tiles;
   int split;           // CTAs of a cluster along the contraction (tile kernel)
+  int stages;          // of the load ring (tile kernel)
   int out_f32;
   int a_mn, b_mn;      // operand stored with its rows contiguous
   int run;             // blocks summed in tensor memory at a time (pair kernel)
   int band;            // M-tiles of a band (pair kernel)
+  int mapped;          // maps.out describes the output
+  int load_bytes;      // of a stage (tile kernel)
   Span sp_out;
   int64_t stall_at;
   uint64_t stall_ns;
@@ -69,14 +87,16 @@ struct MatmulParams {
 
 // ---- one tile per cluster ------------------------------------------------------
 
-constexpr int kTileStages = 4;
+// Six stages where a CTA has an SM to itself (1024^3: 5.3 us, 6.2 with three;
+// 64 x 8192 x 5120: 11.5 and 14.4).  With three, and 256 columns of tensor memory,
+// two CTAs fit an SM, so that one starts while the other stores.
+constexpr int kTileStages = 6, kFewStages = 3;
 constexpr int kTileStageBytes = 2 * kBoxBytes + 2 * kSfBytes;
 constexpr int kTileThreads = 192;           // loads, MMA, four epilogue warps
 constexpr int kPitch = 132;                 // floats a row of the partial tile
-constexpr int kTileSmem = kTileStages * kTileStageBytes + 1024;
-static_assert(kTile * kPitch * 4 <= kTileStages * kTileStageBytes, "partial tile fits the ring");
+static_assert(kTile * kPitch * 4 <= kFewStages * kTileStageBytes, "partial tile fits the ring");
 
-__global__ void __launch_bounds__(kTileThreads, 1)
+__global__ void __launch_bounds__(kTileThreads, 2)
     tile_matmul_kernel(const __grid_constant__ MatmulMaps maps, const MatmulParams p) {
   asm volatile("griddepcontrol.launch_dependents;");
   extern __shared__ uint8_t smem_raw[];
@@ -94,7 +114,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int nkb = per + (rank < more ? 1 : 0);
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kTileStages; ++s) {
+    for (int s = 0; s < p.stages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
@@ -117,38 +137,41 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
   if (warp == 0) {
     if (elect_one()) {
-      int i = 0;
+      int i = 0, s = 0;
+      uint32_t turn = 0;                     // of the ring, mod 2
       for (; i < nkb; ++i) {
-        const int s = i % kTileStages;
         if (kDiagStall && blockIdx.x == 0 && i == p.stall_at) {
           mbar_wait(&stall_bar, 0u, &abort_flag, p.stall_ns);
           break;
         }
-        if (i >= kTileStages &&
-            !mbar_wait(&empty[s], static_cast<uint32_t>((i / kTileStages - 1) & 1), &abort_flag))
-          break;
+        if (i >= p.stages && !mbar_wait(&empty[s], turn ^ 1u, &abort_flag)) break;
         uint8_t* st = ring + s * kTileStageBytes;
         const int kb = kb0 + i;
-        mbar_arrive_expect_tx(&full[s], kTileStageBytes);
+        mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(p.load_bytes));
         tma_load_2d(st, &maps.a, p.a_mn ? mt * kTile : kb * kBK, p.a_mn ? kb * kBK : mt * kTile,
                     &full[s]);
         tma_load_2d(st + kBoxBytes, &maps.b, p.b_mn ? nt * kTile : kb * kBK,
                     p.b_mn ? kb * kBK : nt * kTile, &full[s]);
         tma_load_2d(st + 2 * kBoxBytes, &maps.sa, kb * 128, mt, &full[s]);
         tma_load_2d(st + 2 * kBoxBytes + kSfBytes, &maps.sb, kb * 128, nt, &full[s]);
+        if (++s == p.stages) {
+          s = 0;
+          turn ^= 1u;
+        }
       }
       // Gave up: the copies already issued land before the CTA moves on.
       if (i < nkb)
-        for (int j = i > kTileStages ? i - kTileStages : 0; j < i; ++j)
-          mbar_drain(&full[j % kTileStages], static_cast<uint32_t>((j / kTileStages) & 1));
+        for (int j = i > p.stages ? i - p.stages : 0; j < i; ++j)
+          mbar_drain(&full[j % p.stages], static_cast<uint32_t>((j / p.stages) & 1));
     }
   } else if (warp == 1) {
     if (elect_one()) {
       const uint32_t idesc = mxf8_idesc(128, 128, p.a_mn, p.b_mn);
       const uint32_t step_a = p.a_mn ? kStepMN : kStepK, step_b = p.b_mn ? kStepMN : kStepK;
+      int s = 0;
+      uint32_t turn = 0;
       for (int i = 0; i < nkb; ++i) {
-        const int s = i % kTileStages;
-        if (!mbar_wait(&full[s], static_cast<uint32_t>((i / kTileStages) & 1), &abort_flag)) break;
+        if (!mbar_wait(&full[s], turn, &abort_flag)) break;
         tcgen05_fence_after();
         const uint32_t st = smem_u32(ring + s * kTileStageBytes);
         tcgen05_cp_scales<1>(t_sfa, scale_desc(st + 2 * kBoxBytes));
@@ -161,6 +184,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             mma_mxf8<1>(tmem, da + step_a * k, db + step_b * k, mxf8_idesc_step(idesc, k), t_sfa,
                         t_sfb, i + k > 0);
         tcgen05_commit<1>(&empty[s]);
+        if (++s == p.stages) {
+          s = 0;
+          turn ^= 1u;
+        }
       }
       tcgen05_commit<1>(&done);
       mbar_drain(&done, 0u, kWaitLimitNs);   // every MMA issued has finished
@@ -171,20 +198,69 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   __syncthreads();
   tcgen05_fence_after();
   const bool ok = abort_flag == 0;
+  const int64_t n0 = static_cast<int64_t>(nt) * kTile;
+  const int quarter = warp & 3;
+  const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+  if (p.split == 1 && p.mapped) {
+    // 32 rows at a time and warp through shared memory and a tensor map, 128
+    // bytes of a row a box.
+    const int64_t m = static_cast<int64_t>(mt) * kTile + quarter * 32;
+    if (warp >= 2 && ok && m < p.M) {
+      uint8_t* so = ring + quarter * 4 * kStageOut;
+      const int per = p.out_f32 ? 32 : 64;              // columns of a box
+#pragma unroll 1
+      for (int c = 0; c < 128; c += 32) {
+        if (n0 + c >= p.N) break;
+        uint32_t v[32];
+        tmem_ld_32(tmem + lanes + c, v);
+        tmem_ld_wait();
+        uint8_t* row = so + c / per * kStageOut + lane * 128;
+        if (p.out_f32) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<uint4*>(row + ((j ^ (lane & 7)) << 4)) =
+                make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        } else {
+          const int j0 = (c >> 3) & 4;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            auto f = [&](int k) { return __uint_as_float(v[8 * j + k]); };
+            *reinterpret_cast<uint4*>(row + (((j0 + j) ^ (lane & 7)) << 4)) =
+                make_uint4(bf16x2(f(0), f(1)), bf16x2(f(2), f(3)), bf16x2(f(4), f(5)),
+                           bf16x2(f(6), f(7)));
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        for (int c = 0; c < 128 && n0 + c < p.N; c += per)
+          tma_store_2d(&maps.out, static_cast<int>(n0) + c, static_cast<int>(m), so + c / per * kStageOut);
+        bulk_commit();
+        bulk_wait<0>();
+      }
+      tcgen05_fence_before();
+    }
+    __syncthreads();
+    if (warp == 1) {
+      tcgen05_fence_after();
+      tmem_dealloc<1>(tmem, 256);
+    }
+    if (threadIdx.x == 0 && !ok) atomicOr(&g_matmul_watchdog, 1);
+    return;
+  }
   float* part = reinterpret_cast<float*>(ring);
   if (warp >= 2) {
-    const int row = (warp & 3) * 32 + lane;
+    const int row = quarter * 32 + lane;
 #pragma unroll 1
     for (int c = 0; c < 128; c += 32) {
       uint32_t v[32];
-      tmem_ld_32(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + c, v);
+      tmem_ld_32(tmem + lanes + c, v);
       tmem_ld_wait();
-      float4* dst = reinterpret_cast<float4*>(part + row * kPitch + c);
+      uint4* dst = reinterpret_cast<uint4*>(part + row * kPitch + c);
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        dst[j] = nkb > 0 ? make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
-                                       __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]))
-                         : make_float4(0.f, 0.f, 0.f, 0.f);
+        dst[j] = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
     }
     tcgen05_fence_before();
   }
@@ -192,26 +268,34 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     cluster_sync();
   else
     __syncthreads();
-  // Rows of the tile that this CTA writes, summed over the cluster.
+  // Rows of the tile that this CTA writes, summed over the cluster: the loads of
+  // all CTAs' values are under way before the first is added.
   const int rows = kTile / p.split;
   const int64_t m0 = static_cast<int64_t>(mt) * kTile + rank * rows;
-  const int64_t n0 = static_cast<int64_t>(nt) * kTile;
   const bool vec = (p.N & 7) == 0;
   if (ok) {
     for (int i = threadIdx.x; i < rows * 16; i += kTileThreads) {
       const int r = i >> 4, c = (i & 15) * 8;
       const int64_t m = m0 + r, n = n0 + c;
       if (m >= p.M || n >= p.N) continue;
-      float v[8] = {};
       const uint32_t at = smem_u32(part + (rank * rows + r) * kPitch + c);
-      for (int q = 0; q < p.split; ++q) {
-        const uint32_t a = p.split > 1 ? map_to_rank(at, static_cast<uint32_t>(q)) : at;
-        const float4 lo = p.split > 1 ? ld_cluster_f4(a) : *reinterpret_cast<const float4*>(part + (rank * rows + r) * kPitch + c);
-        const float4 hi = p.split > 1 ? ld_cluster_f4(a + 16) : *reinterpret_cast<const float4*>(part + (rank * rows + r) * kPitch + c + 4);
-        v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
-        v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
-      }
-      store_out8(p.out, p.out_f32, m * p.N + n, v, vec ? 8 : static_cast<int>(p.N - n < 8 ? p.N - n : 8), vec, p.sp_out);
+      float4 lo[8], hi[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (q < p.split) {
+          const uint32_t a = map_to_rank(at, static_cast<uint32_t>(q));
+          lo[q] = ld_cluster_f4(a);
+          hi[q] = ld_cluster_f4(a + 16);
+        }
+      float v[8] = {};
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (q < p.split) {
+          v[0] += lo[q].x; v[1] += lo[q].y; v[2] += lo[q].z; v[3] += lo[q].w;
+          v[4] += hi[q].x; v[5] += hi[q].y; v[6] += hi[q].z; v[7] += hi[q].w;
+        }
+      store_out8(p.out, p.out_f32, m * p.N + n, v,
+                 vec ? 8 : static_cast<int>(p.N - n < 8 ? p.N - n : 8), vec, p.sp_out);
     }
   }
   if (p.split > 1) cluster_sync();            // peers have read this CTA's partial tile
@@ -227,7 +311,6 @@ constexpr int kPairStageBytes = 2 * kBoxBytes + 3 * kSfBytes;
 constexpr int kPairStrideBytes = 34 * 1024;   // 1024-byte aligned boxes
 constexpr int kPairThreads = 320;             // loads, MMA, eight epilogue warps
 constexpr int kBufCols = 240;                 // second result's first column
-constexpr int kStageOut = 4096;               // bytes an epilogue warp stages
 constexpr int kPairSmem = kPairStages * kPairStrideBytes + 8 * kStageOut + 1024;
 constexpr uint32_t kSfaCol = 496, kSfbCol = 500;
 
@@ -472,7 +555,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 // The pair kernel takes outputs that a tensor map can describe, of enough
 // 256 x 256 tiles to keep the GPU's pairs busy.
 bool use_pairs(int64_t M, int64_t N, bool out_f32, int num_sms) {
-  if ((N * (out_f32 ? 4 : 2)) % 16 != 0) return false;
+  if (!matmul_mapped(N, out_f32)) return false;
   const int64_t tiles = ((M + 255) / 256) * ((N + 255) / 256);
   return tiles * 4 >= num_sms;
 }
@@ -533,19 +616,38 @@ int launch_matmul(const MatmulMaps& maps, int64_t M, int64_t N, int64_t K, bool 
   p.m_tiles = static_cast<int>((M + kTile - 1) / kTile);
   p.n_tiles = static_cast<int>((N + kTile - 1) / kTile);
   const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
+  // The contraction is cut in 2, 4 or 8 where that is estimated to be quicker: a
+  // block of 128 steps takes about 0.2 us of a CTA that waits for its loads,
+  // joining up to 0.4 us + 2.4 us for 128 rows (64 KB of partial sums a CTA, two
+  // cluster barriers).  160 x 1024 x 1024: 5.4 us whole, 7.1 in two; 160 x 1024 x
+  // 4096: 11.3 us whole, 9.1 in four; 32 x 32 x 16640: 34 us whole, 8.5 in eight.
+  // Clusters of eight only up to 96 CTAs: 128 of them do not all find room at
+  // once (512 x 512 x 16640: 15.8 us in four, 24.5 in eight).
   p.split = 1;
-  while (p.split < 8 && tiles * p.split * 2 <= num_sms && p.split * 2 <= p.k_blocks) p.split *= 2;
+  const int64_t join = 2 + 12 * (M < 128 ? M : 128) / 128;        // in blocks
+  int64_t best = p.k_blocks;
+  for (int s = 2; s <= 8 && s <= p.k_blocks; s *= 2) {
+    const int64_t cost = (p.k_blocks + s - 1) / s + join;
+    if (cost < best && tiles * s <= (s == 8 ? 96 : num_sms)) {
+      best = cost;
+      p.split = s;
+    }
+  }
+  p.mapped = matmul_mapped(N, out_f32);
+  p.stages = tiles * p.split <= num_sms ? kTileStages : kFewStages;
+  p.load_bytes = matmul_box_rows(M, a_mn) * kBK + matmul_box_rows(N, b_mn) * kBK + 2 * kSfBytes;
   if (tiles * p.split > 0x7fffffff) return static_cast<int>(cudaErrorInvalidConfiguration);
   static DeviceCache attr_cache;
   const int attr = attr_cache.get([] {
     return static_cast<int>(cudaFuncSetAttribute(
-        tile_matmul_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTileSmem));
+        tile_matmul_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        kTileStages * kTileStageBytes + 1024));
   });
   if (attr != 0) return attr;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles * p.split));
   cfg.blockDim = dim3(kTileThreads);
-  cfg.dynamicSmemBytes = kTileSmem;
+  cfg.dynamicSmemBytes = static_cast<size_t>(p.stages * kTileStageBytes + 1024);
   cfg.stream = stream;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -126,6 +126,9 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _stream(stream, dev=None):
     """The call's cudaStream_t: `stream` (a torch.cuda.Stream or a raw
     handle), else the current stream of device index `dev` (default: the
@@ -157,7 +160,7 @@ def _call(name, dev, stream, *args):
     launches on the current device) and the stream appended: by default the
     current stream of that device."""
     fn = getattr(_LIB or _lib(), name)
-    if torch.cuda.current_device() == dev:
+    if _current_device() == dev:
         rc = fn(*args, _raw_stream(dev) if stream is None else _stream(stream, dev))
     else:
         with torch.cuda.device(dev):
@@ -645,8 +648,11 @@ def _width_param(t, name, D):
 
 def _one_device(t, *others):
     dev = t.get_device()
-    if dev < 0 or any(o is not None and o.get_device() != dev for o in others):
+    if dev < 0:
         return _device(t, *others)
+    for o in others:
+        if o is not None and o.get_device() != dev:
+            return _device(t, *others)
     return dev
 
 

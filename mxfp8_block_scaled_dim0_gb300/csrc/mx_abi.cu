@@ -65,7 +65,7 @@ struct MapKey {
 };
 
 struct MapCache {
-  static constexpr int kEntries = 16;
+  static constexpr int kEntries = 64;   // a product takes five, a fused cast three
   MapKey key[kEntries];
   CUtensorMap map[kEntries];
   bool used[kEntries] = {};

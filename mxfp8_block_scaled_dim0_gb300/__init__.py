@@ -15,12 +15,14 @@ Convenience wrappers (``cast_dim0_dim1``, ``cast_dim0``, ``cast_dim1``,
 """
 import ctypes
 import functools
+import importlib.util
 import os
 
 import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmxfp8_cast.so")
+CALL_PATH = os.path.join(_PKG, "_torch_call.so")
 
 MX_OK = 0
 MX_ERR_NULL = -1
@@ -103,8 +105,28 @@ def _lib():
             fn = getattr(lib, name)
             fn.argtypes = args
             fn.restype = res
+        # Addresses that the compiled wrappers call.
+        lib.addresses = {name: ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
+                         for name in sig}
         _LIB = lib
+        _load_call()
     return _LIB
+
+
+# The compiled wrappers of the training operators (csrc/torch_call.cpp).
+_CALL = None
+
+
+def _load_call():
+    global _CALL
+    if _CALL is None:
+        if not os.path.exists(CALL_PATH):
+            raise ImportError("_torch_call.so is not built (expected at %s); build it with "
+                              "`python -m mxfp8_block_scaled_dim0_gb300.build`" % CALL_PATH)
+        spec = importlib.util.spec_from_file_location("_torch_call", CALL_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _CALL = module
 
 
 def library():
@@ -619,41 +641,17 @@ def cast_rowwise(x, stream=None):
 
 
 # The training operators below are called per layer, on tensors that may take the
-# GPU a few microseconds, so the wrappers check their inputs once, by the cheapest
-# tests that tell a good one (a bad one goes to the checks above, which raise),
-# and hand the outputs that they allocate straight to the library.
+# GPU a few microseconds: their usual calls go through the compiled wrappers,
+# which answer None where an argument is not what they know; the checked path
+# then works, or raises the error that says what is wrong.
 
-_BF16, _F32, _U8 = torch.bfloat16, torch.float32, torch.uint8
-
-
-def _rows(t, name):
-    """(rows, columns) of a contiguous 2D bf16 tensor."""
-    if isinstance(t, torch.Tensor) and t.dtype is _BF16 and t.dim() == 2 and t.is_contiguous():
-        return t.shape
-    return _dev_tensor(t, name, dtypes=BF16, ndim=2).shape
-
-
-def _like(t, name, shape, dtype):
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
-            and t.is_contiguous()):
-        _shaped(t, name, tuple(shape), (dtype,))
-
-
-def _width_param(t, name, D):
-    if not (isinstance(t, torch.Tensor) and t.dtype in TYPES and t.shape == (D,)
-            and t.is_contiguous()):
-        _shaped(t, name, (D,), tuple(TYPES))
-    return t.dtype
-
-
-def _one_device(t, *others):
-    dev = t.get_device()
-    if dev < 0:
-        return _device(t, *others)
-    for o in others:
-        if o is not None and o.get_device() != dev:
-            return _device(t, *others)
-    return dev
+def _compiled(name, *args):
+    """The outputs of compiled wrapper `name`, or None."""
+    lib = _LIB or _lib()
+    r = getattr(_CALL, name)(lib.addresses["mx_" + name], *args)
+    if type(r) is int:
+        raise MXError(r, "mx_" + name)
+    return r
 
 
 def _on_stream(stream, t):
@@ -676,20 +674,13 @@ def matmul(qa, sa_blk, qb, sb_blk, out_dtype=torch.bfloat16, stream=None):
     if stream is not None:
         with _on_stream(stream, qa):
             return matmul(qa, sa_blk, qb, sb_blk, out_dtype)
-    orders = _operand(qa, "qa") | _operand(qb, "qb") << 1
-    M, K = qa.shape
-    N = qb.shape[0]
-    if qb.shape[1] != K:
-        raise ValueError("qa and qb must have equal rows, got %d and %d values" % (K, qb.shape[1]))
-    _dev_tensor(sa_blk, "sa_blk", mx_blocked_bytes(M, K // 32), BYTES)
-    _dev_tensor(sb_blk, "sb_blk", mx_blocked_bytes(N, K // 32), BYTES)
     if out_dtype not in TYPES:
         raise TypeError("out_dtype must be one of %s, got %s"
                         % (", ".join(str(d) for d in TYPES), out_dtype))
-    dev = _one_device(qa, sa_blk, qb, sb_blk)
-    out = torch.empty((M, N), dtype=out_dtype, device=qa.device)
-    _call("mx_matmul", dev, None, qa.data_ptr(), sa_blk.data_ptr(), qb.data_ptr(),
-          sb_blk.data_ptr(), M, N, K, orders, out.data_ptr(), TYPES[out_dtype])
+    out = _compiled("matmul", qa, sa_blk, qb, sb_blk, TYPES[out_dtype])
+    if out is None:
+        out = torch.empty((qa.shape[0], qb.shape[0]), dtype=out_dtype, device=qa.device)
+        mx_matmul(qa, sa_blk, qb, sb_blk, out)
     return out
 
 
@@ -699,23 +690,19 @@ def layer_norm(x, w, b=None, eps=1e-5, save=False, stream=None):
     if stream is not None:
         with _on_stream(stream, x):
             return layer_norm(x, w, b, eps, save)
-    M, D = _rows(x, "x")
-    wt = _width_param(w, "w", D)
-    if b is not None:
-        _like(b, "b", (D,), wt)
-    dev = _one_device(x, w, b)
-    y = torch.empty_like(x)
-    mean = torch.empty(M, dtype=_F32, device=x.device)
-    rstd = torch.empty_like(mean)
-    bp = None if b is None else b.data_ptr()
+    r = _compiled("layer_norm", x, w, b, eps, save)
+    if r is not None:
+        return r
+    M, D = x.shape
+    y = torch.empty((M, D), dtype=torch.bfloat16, device=x.device)
+    mean = torch.empty(M, dtype=torch.float32, device=x.device)
+    rstd = torch.empty(M, dtype=torch.float32, device=x.device)
     if not save:
-        _call("mx_layer_norm", dev, None, x.data_ptr(), w.data_ptr(), bp, TYPES[wt], M, D, eps,
-              y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), None, None)
+        mx_layer_norm(x, w, b, eps, y, mean, rstd)
         return y, mean, rstd
-    q0 = torch.empty((M, D), dtype=_U8, device=x.device)
-    s0 = torch.empty(mx_blocked_bytes(M, D // 32), dtype=_U8, device=x.device)
-    _call("mx_layer_norm", dev, None, x.data_ptr(), w.data_ptr(), bp, TYPES[wt], M, D, eps,
-          y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), q0.data_ptr(), s0.data_ptr())
+    q0 = torch.empty((M, D), dtype=torch.uint8, device=x.device)
+    s0 = _u8(mx_blocked_bytes(M, D // 32), x.device)
+    mx_layer_norm(x, w, b, eps, y, mean, rstd, q0, s0)
     return y, mean, rstd, q0, s0
 
 
@@ -725,22 +712,18 @@ def layer_norm_backward(dy, saved, w, mean, rstd, bias=True, stream=None):
     if stream is not None:
         with _on_stream(stream, dy):
             return layer_norm_backward(dy, saved, w, mean, rstd, bias)
+    r = _compiled("layer_norm_backward",
+                  (_LIB or _lib()).addresses["mx_layer_norm_backward_work_bytes"], dy, saved, w,
+                  mean, rstd, bias)
+    if r is not None:
+        return r
     x, q0, s0 = _split_saved(saved)
-    M, D = _rows(dy, "dy")
-    if x is not None:
-        _like(x, "x", (M, D), _BF16)
-    else:
-        _saved(q0, s0, M, D)
-    wt = _width_param(w, "w", D)
-    _like(mean, "mean", (M,), _F32)
-    _like(rstd, "rstd", (M,), _F32)
-    dev = _one_device(dy, x, q0, s0, w, mean, rstd)
-    dx, dw = torch.empty_like(dy), torch.empty_like(w)
-    db = torch.empty_like(w) if bias else None
-    work = torch.empty(mx_layer_norm_backward_work_bytes(M, D), dtype=_U8, device=dy.device)
-    _call("mx_layer_norm_backward", dev, None, dy.data_ptr(), _ptr(x), _ptr(q0), _ptr(s0),
-          w.data_ptr(), TYPES[wt], mean.data_ptr(), rstd.data_ptr(), M, D, dx.data_ptr(),
-          dw.data_ptr(), _ptr(db), work.data_ptr())
+    M, D = dy.shape
+    dx = torch.empty((M, D), dtype=torch.bfloat16, device=dy.device)
+    dw = torch.empty(D, dtype=w.dtype, device=dy.device)
+    db = torch.empty(D, dtype=w.dtype, device=dy.device) if bias else None
+    work = _u8(mx_layer_norm_backward_work_bytes(M, D), dy.device)
+    mx_layer_norm_backward(dy, x, q0, s0, w, mean, rstd, dx, dw, db, work)
     return dx, dw, db
 
 
@@ -750,18 +733,17 @@ def swiglu(gu, save=False, stream=None):
     if stream is not None:
         with _on_stream(stream, gu):
             return swiglu(gu, save)
-    M, F2 = _rows(gu, "gu")
-    if F2 % 2:
-        raise ValueError("gu must have an even number of columns, got %d" % F2)
-    dev = _one_device(gu)
-    h = torch.empty((M, F2 // 2), dtype=_BF16, device=gu.device)
+    r = _compiled("swiglu", gu, save)
+    if r is not None:
+        return r
+    M, F2 = gu.shape
+    h = torch.empty((M, F2 // 2), dtype=torch.bfloat16, device=gu.device)
     if not save:
-        _call("mx_swiglu", dev, None, gu.data_ptr(), M, F2 // 2, h.data_ptr(), None, None)
+        mx_swiglu(gu, h)
         return h
-    q0 = torch.empty((M, F2), dtype=_U8, device=gu.device)
-    s0 = torch.empty(mx_blocked_bytes(M, F2 // 32), dtype=_U8, device=gu.device)
-    _call("mx_swiglu", dev, None, gu.data_ptr(), M, F2 // 2, h.data_ptr(), q0.data_ptr(),
-          s0.data_ptr())
+    q0 = torch.empty((M, F2), dtype=torch.uint8, device=gu.device)
+    s0 = _u8(mx_blocked_bytes(M, F2 // 32), gu.device)
+    mx_swiglu(gu, h, q0, s0)
     return h, q0, s0
 
 
@@ -771,14 +753,11 @@ def swiglu_backward(dh, saved, stream=None):
     if stream is not None:
         with _on_stream(stream, dh):
             return swiglu_backward(dh, saved)
+    r = _compiled("swiglu_backward", dh, saved)
+    if r is not None:
+        return r
     gu, q0, s0 = _split_saved(saved)
-    M, F = _rows(dh, "dh")
-    if gu is not None:
-        _like(gu, "gu", (M, 2 * F), _BF16)
-    else:
-        _saved(q0, s0, M, 2 * F)
-    dev = _one_device(dh, gu, q0, s0)
-    dgu = torch.empty((M, 2 * F), dtype=_BF16, device=dh.device)
-    _call("mx_swiglu_backward", dev, None, dh.data_ptr(), _ptr(gu), _ptr(q0), _ptr(s0), M, F,
-          dgu.data_ptr())
+    M, F = dh.shape
+    dgu = torch.empty((M, 2 * F), dtype=torch.bfloat16, device=dh.device)
+    mx_swiglu_backward(dh, gu, q0, s0, dgu)
     return dgu

@@ -22,6 +22,9 @@ LIB = os.path.join(PKG, "libmxfp8_cast.so")
 # the tests run parity cases through it.
 OBJ_DIR_BOUNDS = os.path.join(PKG, "_build_bounds")
 LIB_BOUNDS = os.path.join(PKG, "libmxfp8_cast_bounds.so")
+# The allocating wrappers of the training operators (CPython functions on torch's
+# C++ API, host code only).
+CALL = os.path.join(PKG, "_torch_call.so")
 SOURCES = ["mx_cast.cu", "mx_blocked.cu", "mx_dequant.cu", "mx_scaled.cu", "mx_matmul.cu",
            "mx_norm.cu", "mx_swiglu.cu", "mx_abi.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -63,9 +66,44 @@ def _compile(src, verbose_ptxas=False, bounds=False):
     return obj, r.stderr
 
 
+def build_call(force: bool = False) -> str:
+    """Compile _torch_call.so against the torch that runs this."""
+    src = os.path.join(CSRC, "torch_call.cpp")
+    if not force and not _stale(CALL, [src, os.path.abspath(__file__)]):
+        return CALL
+    import sysconfig
+    import torch
+    root = os.path.dirname(torch.__file__)
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api",
+                                                       "include"),
+           os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+    tmp = CALL + ".tmp.%d" % os.getpid()
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+           "-I", sysconfig.get_paths()["include"], *sum((["-isystem", i] for i in inc), []), src,
+           "-o", tmp, "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cuda",
+           "-ltorch_cpu", "-ltorch", "-lc10_cuda", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("compiling %s failed:\n%s\n%s" % (src, r.stdout, r.stderr))
+    os.replace(tmp, CALL)
+    return CALL
+
+
 def build(force: bool = False, verbose_ptxas: bool = False, bounds: bool = False) -> str:
-    """Compile and link if any source is newer than the library.  bounds=True
-    builds the bounds-checked variant (libmxfp8_cast_bounds.so) instead."""
+    """Compile and link if any source is newer than the library, the torch
+    wrappers beside it.  bounds=True builds the bounds-checked variant
+    (libmxfp8_cast_bounds.so) instead."""
+    if bounds:
+        return _build_library(force, verbose_ptxas, True)
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        call = ex.submit(build_call, force)
+        lib_path = _build_library(force, verbose_ptxas, False)
+        call.result()
+    return lib_path
+
+
+def _build_library(force, verbose_ptxas, bounds) -> str:
     lib_path = LIB_BOUNDS if bounds else LIB
     deps = _deps()
     if not force and not verbose_ptxas and not _stale(lib_path, deps):

@@ -339,7 +339,8 @@ struct NormBackParams {
 
 // EPT values a thread.  The second pass reads the row from shared memory again:
 // with dw and db in 2 EPT registers there is no room for more of the row (16
-// values a thread, held from the first pass: 117 us where this takes 85).
+// values a thread, held from the first pass, are no quicker: 70 us against 71 at
+// 16640 x 4096, 111 us against 94 at 16640 x 5120, with the 8-bit save).
 template <bool SAVE, bool ODD, typename W, int EPT>
 __global__ void __launch_bounds__(kBackThreads, 1) norm_back_kernel(const NormBackParams p) {
   constexpr int V = EPT / 8;
@@ -681,25 +682,37 @@ int run_norm_back(NormBackParams p, int num_sms, int* grid, cudaStream_t stream)
                 static_cast<int>(smem), stream, p);
 }
 
-// 32 values a thread (16 warps then hold a row of 16384); fewer where one warp
-// holds the row all the same, more for the few widths that need it for their lead.
+// Values a thread holds of a row.  32 carry the most rows at a time (a group of 16
+// warps holds 16384); few values for an SM are spread over more threads (values:
+// an SM's rows times the width); 40 for the few widths that need them for their
+// lead.  Backward, 32 / 16 / 8 values: 1031 x 1021 11.0 / 9.0 / 8.1 us, 600 x 4096
+// 10.2 / 9.5 / 10.1, 2400 x 4096 17.0 / 17.7 / 21.4; forward: 1 x 4096 2.9 / 2.5 /
+// 2.4 us, 1200 x 1024 3.3 / 3.1 / 3.6, 2400 x 1024 3.9 / 4.3 / 5.6.
+int values_of(int width, int64_t M, int num_sms, int64_t few) {
+  if (width > kNormMaxWidth) return 40;
+  const int64_t values = (M + num_sms - 1) / num_sms * width;
+  if (width <= 256 || (width <= 4096 && values < 8192)) return 8;
+  if (width <= 512 || (width <= 8192 && values < few)) return 16;
+  return 32;
+}
+
 template <bool SAVE, bool ODD, typename W>
 int pick_norm(const NormParams& p, int num_sms, cudaStream_t stream) {
-  const int width = p.D + (ODD ? 7 : 0);
-  if (width <= 256) return run_norm<SAVE, ODD, W, 8>(p, num_sms, stream);
-  if (width <= 512) return run_norm<SAVE, ODD, W, 16>(p, num_sms, stream);
+  const int n = values_of(p.D + (ODD ? 7 : 0), p.M, num_sms, 16384);
+  if (n == 8) return run_norm<SAVE, ODD, W, 8>(p, num_sms, stream);
+  if (n == 16) return run_norm<SAVE, ODD, W, 16>(p, num_sms, stream);
   if constexpr (ODD)
-    if (width > kNormMaxWidth) return run_norm<SAVE, ODD, W, 40>(p, num_sms, stream);
+    if (n == 40) return run_norm<SAVE, ODD, W, 40>(p, num_sms, stream);
   return run_norm<SAVE, ODD, W, 32>(p, num_sms, stream);
 }
 
 template <bool SAVE, bool ODD, typename W>
 int pick_norm_back(const NormBackParams& p, int num_sms, int* grid, cudaStream_t stream) {
-  const int width = p.D + (ODD ? 7 : 0);
-  if (width <= 256) return run_norm_back<SAVE, ODD, W, 8>(p, num_sms, grid, stream);
-  if (width <= 512) return run_norm_back<SAVE, ODD, W, 16>(p, num_sms, grid, stream);
+  const int n = values_of(p.D + (ODD ? 7 : 0), p.M, num_sms, 40000);
+  if (n == 8) return run_norm_back<SAVE, ODD, W, 8>(p, num_sms, grid, stream);
+  if (n == 16) return run_norm_back<SAVE, ODD, W, 16>(p, num_sms, grid, stream);
   if constexpr (ODD)
-    if (width > kNormMaxWidth) return run_norm_back<SAVE, ODD, W, 40>(p, num_sms, grid, stream);
+    if (n == 40) return run_norm_back<SAVE, ODD, W, 40>(p, num_sms, grid, stream);
   return run_norm_back<SAVE, ODD, W, 32>(p, num_sms, grid, stream);
 }
 

@@ -114,9 +114,10 @@ __device__ __forceinline__ uint2 mx_cast_piece(const uint4& w, uint32_t& sbyte) 
                     e4m3x4(bf_lo(w.z), bf_hi(w.z), bf_lo(w.w), bf_hi(w.w), mult));
 }
 
-// 2^(s - 127) of a scale byte; 0xFF is NaN.
+// 2^(s - 127) of a scale byte; 0xFF is NaN.  The exponent field, but for s = 0 a
+// subnormal's bit, and for 0xFF the quiet bit too.
 __device__ __forceinline__ float scale_mult(uint32_t s) {
-  return __uint_as_float(s == 0 ? 0x00400000u : s == 255 ? 0x7FC00000u : s << 23);
+  return __uint_as_float(max(s << 23, 0x00400000u) | ((s + 1) >> 8) << 22);
 }
 
 // Two e4m3 bytes -> two floats (exact: through f16, whose range holds e4m3's).

@@ -90,6 +90,12 @@ int encode_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t
   }
   EncodeFn fn = encode_fn();
   if (!fn) return cuda_fail(static_cast<int>(cudaErrorNotSupported));
+  // A driver call: the device's context must be the thread's, which a thread that
+  // has made no runtime call that needs one (autograd's) does not have yet.
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaSetDevice(dev);
+  if (e != cudaSuccess) return cuda_fail(static_cast<int>(e));
   const cuuint64_t dims[2] = {inner, outer};
   const cuuint64_t strides[1] = {stride};
   const cuuint32_t box[2] = {bin, bout};

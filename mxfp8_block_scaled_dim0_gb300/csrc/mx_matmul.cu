@@ -23,8 +23,8 @@
 // so a byte of shared memory feeds twice the products that one CTA's tile
 // would.  Loads run five stages ahead of the MMAs.  Tensor memory (512 columns)
 // holds two results of 256 columns that overlap in 16, and the scales in the
-// last 16; the eight epilogue warps of a CTA read the overlap first, and the
-// next tile's MMAs begin while they store the rest.  For an fp32 result longer
+// last 16; the eight epilogue warps of a CTA take a result into registers at
+// once, and the next tile's MMAs run while they store it.  For an fp32 result longer
 // sums are cut into runs of 4096 steps that the epilogue adds up in registers:
 // the tensor core's accumulator cuts bits off at every addition, an error
 // that grows with the run (3.7e-7 in the 2-norm at 4096 steps, 1.5e-6 at
@@ -326,6 +326,7 @@ struct Tiles {
   }
 };
 
+template <bool F32>
 __global__ void __launch_bounds__(kPairThreads, 1)
     pair_matmul_kernel(const __grid_constant__ MatmulMaps maps, const MatmulParams p) {
   asm volatile("griddepcontrol.launch_dependents;");
@@ -450,12 +451,21 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     uint8_t* so = stage_out + (warp - 2) * kStageOut;
     const uint32_t drained_bar = map_to_rank(smem_u32(&drained), 0);
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-    float v[128];
+    // This lane's row of 128 results, in boxes of 128 bytes: four of fp32, two of
+    // bf16 (packed as they are read).
+    constexpr int kBoxes = F32 ? 4 : 2;
+    uint32_t v[kBoxes][32];
     int item = 0;
     bool ok = true;
     for (int t = first; ok && t < n_tiles; t += stride) {
       int mt, nt;
       tiles.at(t, mt, nt);
+      if constexpr (F32) {
+#pragma unroll
+        for (int x = 0; x < kBoxes; ++x)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[x][j] = 0;
+      }
       for (int k0 = 0; k0 < p.k_blocks; k0 += p.run, ++item) {
         if (!mbar_wait(&ready[item & 1], static_cast<uint32_t>((item >> 1) & 1), &abort_flag)) {
           ok = false;
@@ -463,57 +473,55 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
         tcgen05_fence_after();
         const uint32_t at = tmem + lanes + ((item & 1) ? kBufCols : 0) + half * 128;
+        if constexpr (!F32) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          // Chunks 0 and 7 hold the overlap: first.
-          const int c = j == 0 ? 0 : j == 1 ? 7 : j - 1;
-          uint32_t w[16];
-          tmem_ld_16(at + 16 * c, w);
-          tmem_ld_wait();
-          if (j == 1) {
-            tcgen05_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_remote(drained_bar);
+          for (int x = 0; x < 2; ++x) {
+            uint32_t a[32], b[32];
+            tmem_ld_32(at + 64 * x, a);
+            tmem_ld_32(at + 64 * x + 32, b);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              v[x][j] = bf16x2(__uint_as_float(a[2 * j]), __uint_as_float(a[2 * j + 1]));
+              v[x][16 + j] = bf16x2(__uint_as_float(b[2 * j]), __uint_as_float(b[2 * j + 1]));
+            }
           }
-          if (k0 == 0) {
+        } else {
 #pragma unroll
-            for (int x = 0; x < 16; ++x) v[16 * c + x] = __uint_as_float(w[x]);
-          } else {
+          for (int c = 0; c < 8; ++c) {
+            uint32_t w[16];
+            tmem_ld_16(at + 16 * c, w);
+            tmem_ld_wait();
 #pragma unroll
-            for (int x = 0; x < 16; ++x) v[16 * c + x] += __uint_as_float(w[x]);
+            for (int j = 0; j < 16; ++j) {
+              uint32_t& s = v[(c >> 1) % kBoxes][(c & 1) * 16 + j];
+              s = __float_as_uint(__uint_as_float(s) + __uint_as_float(w[j]));
+            }
           }
         }
+        tcgen05_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(drained_bar);
       }
       if (!ok) break;
-      // 32 rows x 128 columns through shared memory, 128 bytes of a row at a
-      // time, in the swizzled order the tensor map expects.
+      // 32 rows x 128 columns through shared memory, a box at a time, in the
+      // swizzled order the tensor map expects.
       const int m = (2 * mt + rank) * kTile + quarter * 32;
       const int n = 2 * nt * kTile + half * 128;
       if (m >= p.M || n >= p.N) continue;
       uint8_t* row = so + lane * 128;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        if (!p.out_f32 && x >= 2) break;
+      for (int x = 0; x < kBoxes; ++x) {
         if (lane == 0) bulk_wait_read<0>();
         __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          uint4 o;
-          if (p.out_f32) {
-            o = make_uint4(__float_as_uint(v[32 * x + 4 * j]), __float_as_uint(v[32 * x + 4 * j + 1]),
-                           __float_as_uint(v[32 * x + 4 * j + 2]),
-                           __float_as_uint(v[32 * x + 4 * j + 3]));
-          } else {
-            const int b = 64 * (x & 1) + 8 * j;
-            o = make_uint4(bf16x2(v[b], v[b + 1]), bf16x2(v[b + 2], v[b + 3]),
-                           bf16x2(v[b + 4], v[b + 5]), bf16x2(v[b + 6], v[b + 7]));
-          }
-          *reinterpret_cast<uint4*>(row + ((j ^ (lane & 7)) << 4)) = o;
-        }
+        for (int j = 0; j < 8; ++j)
+          *reinterpret_cast<uint4*>(row + ((j ^ (lane & 7)) << 4)) =
+              make_uint4(v[x][4 * j], v[x][4 * j + 1], v[x][4 * j + 2], v[x][4 * j + 3]);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          const int c = n + x * (p.out_f32 ? 32 : 64);
+          const int c = n + x * (128 / kBoxes);
           if (c < p.N) tma_store_2d(&maps.out, c, m, so);
           bulk_commit();
         }
@@ -566,15 +574,18 @@ bool matmul_pairs(int64_t M, int64_t N, bool out_f32, int num_sms) {
   return use_pairs(M, N, out_f32, num_sms);
 }
 
+template <bool F32>
 static int launch_pairs(const MatmulMaps& maps, MatmulParams p, int num_sms, cudaStream_t stream) {
   p.m_tiles = static_cast<int>((p.M + 255) / 256);
   p.n_tiles = static_cast<int>((p.N + 255) / 256);
-  p.run = p.out_f32 ? 32 : p.k_blocks;
+  // Equal runs: a short last one would leave no time to read the one before.
+  const int runs = F32 ? (p.k_blocks + 31) / 32 : 1;
+  p.run = (p.k_blocks + runs - 1) / runs;
   p.band = 8;
   static DeviceCache attr_cache;
   const int attr = attr_cache.get([] {
     return static_cast<int>(cudaFuncSetAttribute(
-        pair_matmul_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem));
+        pair_matmul_kernel<F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem));
   });
   if (attr != 0) return attr;
   const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
@@ -594,7 +605,7 @@ static int launch_pairs(const MatmulMaps& maps, MatmulParams p, int num_sms, cud
   at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 2;
-  return static_cast<int>(cudaLaunchKernelEx(&cfg, pair_matmul_kernel, maps, p));
+  return static_cast<int>(cudaLaunchKernelEx(&cfg, pair_matmul_kernel<F32>, maps, p));
 }
 
 int launch_matmul(const MatmulMaps& maps, int64_t M, int64_t N, int64_t K, bool a_mn,
@@ -612,7 +623,9 @@ int launch_matmul(const MatmulMaps& maps, int64_t M, int64_t N, int64_t K, bool 
   const Stall stall = take_stall();
   p.stall_at = stall.at;
   p.stall_ns = stall.ns;
-  if (use_pairs(M, N, out_f32, num_sms)) return launch_pairs(maps, p, num_sms, stream);
+  if (use_pairs(M, N, out_f32, num_sms))
+    return out_f32 ? launch_pairs<true>(maps, p, num_sms, stream)
+                   : launch_pairs<false>(maps, p, num_sms, stream);
   p.m_tiles = static_cast<int>((M + kTile - 1) / kTile);
   p.n_tiles = static_cast<int>((N + kTile - 1) / kTile);
   const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles;

@@ -47,9 +47,11 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   return v;
 }
 
-// Arrivals on a barrier of another CTA of the cluster (`bar` from map_to_rank).
+// Arrival on a barrier of another CTA of the cluster (`bar` from map_to_rank).  It
+// orders tensor memory, with the tcgen05 fences around it, not shared memory of
+// the cluster: no release at cluster scope, which waits for the thread's stores.
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // Counts `bytes` that no copy will bring as if they had arrived.

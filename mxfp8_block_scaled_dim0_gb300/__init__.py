@@ -537,6 +537,9 @@ def _u8(n, device):
 
 def cast_dim0_dim1(x, stream=None):
     """Returns (q0 (M,K), s0_blk, q1 (K,M), s1_blk) as uint8 tensors."""
+    r = _compiled("cast_dim0_dim1", x) if stream is None else None
+    if r is not None:
+        return r
     M, K = x.shape
     q0 = torch.empty((M, K), dtype=torch.uint8, device=x.device)
     q1 = torch.empty((K, M), dtype=torch.uint8, device=x.device)
@@ -547,6 +550,9 @@ def cast_dim0_dim1(x, stream=None):
 
 
 def cast_dim0(x, stream=None):
+    r = _compiled("cast_dim0", x) if stream is None else None
+    if r is not None:
+        return r
     M, K = x.shape
     q0 = torch.empty((M, K), dtype=torch.uint8, device=x.device)
     s0 = _u8(mx_blocked_bytes(M, K // 32), x.device)
@@ -555,6 +561,9 @@ def cast_dim0(x, stream=None):
 
 
 def cast_dim1(x, stream=None):
+    r = _compiled("cast_dim1", x) if stream is None else None
+    if r is not None:
+        return r
     M, K = x.shape
     q1 = torch.empty((K, M), dtype=torch.uint8, device=x.device)
     s1 = _u8(mx_blocked_bytes(K, M // 32), x.device)

@@ -48,11 +48,12 @@ __device__ __forceinline__ f32x2 sigmoid2(f32x2 g) {
 }
 
 // A warp's place: row r, piece `run` of the row, walked in steps of the whole
-// grid without a division.
+// grid without a division.  Rows in 32 bits (M < 2^31), so that an address is one
+// wide multiplication.
 struct Place {
-  int64_t r, dr;
+  uint32_t r, dr;
   int run, drun, runs;
-  __device__ __forceinline__ Place(int64_t warp, int64_t warps, int runs_) : runs(runs_) {
+  __device__ __forceinline__ Place(uint32_t warp, uint32_t warps, int runs_) : runs(runs_) {
     r = warp / runs;
     run = static_cast<int>(warp - r * runs);
     dr = warps / runs;
@@ -68,6 +69,17 @@ struct Place {
   }
 };
 
+__device__ __forceinline__ int64_t wide(uint32_t r, int n) {
+  return static_cast<int64_t>(static_cast<uint64_t>(r) * static_cast<uint32_t>(n));
+}
+
+// Bytes of a row of scales: where row r of the blocked layout begins, and block
+// `b` of a row.
+__device__ __forceinline__ int64_t scale_row(uint32_t r, int cols4) {
+  return wide(r >> 7, cols4 * 128) + (r & 31) * 16 + (r >> 5 & 3) * 4;
+}
+__device__ __forceinline__ int scale_block(int b) { return (b >> 2) * 512 + (b & 3); }
+
 // Rows whose halves are a multiple of 8 values: pieces of eight, as pairs.  The
 // next piece's loads are issued before this one is worked on, without a condition
 // (past the matrix its last row, past the row its first piece: not used), for
@@ -79,23 +91,25 @@ __global__ void __launch_bounds__(kThreads) swiglu_rows8_kernel(const SwigluPara
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
-  Place at(static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5), warps, p.runs);
+  Place at(blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), gridDim.x * (kThreads / 32), p.runs);
+  const uint32_t M = static_cast<uint32_t>(p.M);
   Piece<8> next_g, next_u;
   auto fetch = [&]() {
     const int c = (at.run * 32 + lane) * 8;
-    const uint16_t* x = p.gu + (at.r < p.M ? at.r : p.M - 1) * 2 * p.F + (c < p.F ? c : 0);
+    const uint16_t* x = p.gu + wide(min(at.r, M - 1), 2 * p.F) + (c < p.F ? c : 0);
     next_g.load(x);
     next_u.load(x + p.F);
   };
   fetch();
-  while (at.r < p.rows) {
-    const int64_t r = at.r;
+  const uint32_t rows = static_cast<uint32_t>(p.rows);
+  const bool whole = p.F % 128 == 0;           // the up half's scales begin a tile
+  while (at.r < rows) {
+    const uint32_t r = at.r;
     const int c = (at.run * 32 + lane) * 8;
     Piece<8> pg = next_g, pu = next_u;
     at.next();
     fetch();
-    const bool live = r < p.M && c < p.F;
+    const bool live = r < M && c < p.F;
     f32x2 g[4], u[4];
     if constexpr (SAVE) {
       if (!live) {
@@ -109,32 +123,29 @@ __global__ void __launch_bounds__(kThreads) swiglu_rows8_kernel(const SwigluPara
       uint32_t sg, su;
       const uint2 qg = mx_cast_pairs(pg.w, g, sg);
       const uint2 qu = mx_cast_pairs(pu.w, u, su);
-      uint8_t* q = p.q + r * 2 * p.F + c;
+      uint8_t* q = p.q + wide(r, 2 * p.F) + c;
       if (live && in_span(p.sp_q, q, 8) && in_span(p.sp_q, q + p.F, 8)) {
         *reinterpret_cast<uint2*>(q) = qg;
         *reinterpret_cast<uint2*>(q + p.F) = qu;
       }
       // One lane of a block's four writes its byte.  Rows past the matrix are zero
       // and give 0, the padding of the blocked layout.
-      uint8_t* s = p.s + blocked_offset(r, 0, p.s_cols4);
+      uint8_t* s = p.s + scale_row(r, p.s_cols4);
       if (c < p.F && (lane & 3) == 0) {
-        const int cg = c >> 5, cu = cg + (p.F >> 5);
-        uint8_t* a = s + (cg >> 2) * 512 + (cg & 3);
-        uint8_t* b = s + (cu >> 2) * 512 + (cu & 3);
+        uint8_t* a = s + scale_block(c >> 5);
+        uint8_t* b = whole ? a + (p.F >> 7) * 512 : s + scale_block((c + p.F) >> 5);
         if (in_span(p.sp_s, a, 1)) *a = static_cast<uint8_t>(sg);
         if (in_span(p.sp_s, b, 1)) *b = static_cast<uint8_t>(su);
       }
       // Columns of scales past the row: zero.
-      if (c == 0 && p.s_cols4 > p.F / 16)
-        for (int j = p.F / 16; j < p.s_cols4; ++j) {
-          uint8_t* a = s + (j >> 2) * 512 + (j & 3);
-          if (in_span(p.sp_s, a, 1)) *a = 0;
-        }
+      if (!whole && c == 0)
+        for (int j = p.F / 16; j < p.s_cols4; ++j)
+          if (in_span(p.sp_s, s + scale_block(j), 1)) s[scale_block(j)] = 0;
     }
     if (!live) continue;
 #pragma unroll
     for (int j = 0; j < 4; ++j) g[j] = mul2(mul2(g[j], sigmoid2(g[j])), u[j]);
-    uint16_t* h = p.out + r * p.F + c;
+    uint16_t* h = p.out + wide(r, p.F) + c;
     if (in_span(p.sp_out, h, 16)) *reinterpret_cast<uint4*>(h) = pack_pairs(g);
   }
 }
@@ -145,34 +156,33 @@ __global__ void __launch_bounds__(kThreads) swiglu_back_rows8_kernel(const Swigl
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
-  Place at(static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5), warps, p.runs);
+  Place at(blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), gridDim.x * (kThreads / 32), p.runs);
+  const uint32_t M = static_cast<uint32_t>(p.M);
   const f32x2 one = pair(1.0f, 1.0f), minus = pair(-1.0f, -1.0f);
   Piece<8> next_d, next_g, next_u;
   uint2 next_qg, next_qu;
   uint32_t next_sg, next_su;
   auto fetch = [&]() {
-    const int64_t r = at.r < p.M ? at.r : p.M - 1;
+    const uint32_t r = min(at.r, M - 1);
     int c = (at.run * 32 + lane) * 8;
     c = c < p.F ? c : 0;
-    next_d.load(p.dh + r * p.F + c);
+    next_d.load(p.dh + wide(r, p.F) + c);
     if constexpr (SAVE) {
-      const uint8_t* q = p.q + r * 2 * p.F + c;
+      const uint8_t* q = p.q + wide(r, 2 * p.F) + c;
       next_qg = ld_q8(q);
       next_qu = ld_q8(q + p.F);
-      const uint8_t* s = p.s + blocked_offset(r, 0, p.s_cols4);
-      const int cg = c >> 5, cu = cg + (p.F >> 5);
-      asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(next_sg) : "l"(s + (cg >> 2) * 512 + (cg & 3)));
-      asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(next_su) : "l"(s + (cu >> 2) * 512 + (cu & 3)));
+      const uint8_t* s = p.s + scale_row(r, p.s_cols4);
+      asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(next_sg) : "l"(s + scale_block(c >> 5)));
+      asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(next_su) : "l"(s + scale_block((c + p.F) >> 5)));
     } else {
-      const uint16_t* x = p.gu + r * 2 * p.F + c;
+      const uint16_t* x = p.gu + wide(r, 2 * p.F) + c;
       next_g.load(x);
       next_u.load(x + p.F);
     }
   };
   fetch();
-  while (at.r < p.M) {
-    const int64_t r = at.r;
+  while (at.r < M) {
+    const uint32_t r = at.r;
     const int c = (at.run * 32 + lane) * 8;
     f32x2 d[4], g[4], u[4];
     get_pairs(next_d.w, d);
@@ -194,7 +204,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_back_rows8_kernel(const Swigl
       g[j] = mul2(d[j], a);
     }
     if (c >= p.F) continue;
-    uint16_t* o = p.out + r * 2 * p.F + c;
+    uint16_t* o = p.out + wide(r, 2 * p.F) + c;
     if (in_span(p.sp_out, o, 16) && in_span(p.sp_out, o + p.F, 16)) {
       *reinterpret_cast<uint4*>(o) = pack_pairs(u);
       *reinterpret_cast<uint4*>(o + p.F) = pack_pairs(g);
@@ -208,11 +218,11 @@ __global__ void __launch_bounds__(kThreads) swiglu_kernel(const SwigluParams p) 
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
-  Place at(static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5), warps, p.runs);
-  for (; at.r < p.M; at.next()) {
-    const uint16_t* x = p.gu + at.r * 2 * p.F;
-    uint16_t* out = p.out + at.r * p.F;
+  Place at(blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), gridDim.x * (kThreads / 32), p.runs);
+  const uint32_t M = static_cast<uint32_t>(p.M);
+  for (; at.r < M; at.next()) {
+    const uint16_t* x = p.gu + wide(at.r, 2 * p.F);
+    uint16_t* out = p.out + wide(at.r, p.F);
     Piece<VEC> pg[kOdd], pu[kOdd];
     const int c0 = (at.run * 32 * kOdd + lane) * VEC;
 #pragma unroll
@@ -241,12 +251,12 @@ __global__ void __launch_bounds__(kThreads) swiglu_back_kernel(const SwigluParam
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
-  Place at(static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5), warps, p.runs);
-  for (; at.r < p.M; at.next()) {
-    const uint16_t* x = p.gu + at.r * 2 * p.F;
-    const uint16_t* dh = p.dh + at.r * p.F;
-    uint16_t* out = p.out + at.r * 2 * p.F;
+  Place at(blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), gridDim.x * (kThreads / 32), p.runs);
+  const uint32_t M = static_cast<uint32_t>(p.M);
+  for (; at.r < M; at.next()) {
+    const uint16_t* x = p.gu + wide(at.r, 2 * p.F);
+    const uint16_t* dh = p.dh + wide(at.r, p.F);
+    uint16_t* out = p.out + wide(at.r, 2 * p.F);
     Piece<VEC> pd[kOdd], pg[kOdd], pu[kOdd];
     const int c0 = (at.run * 32 * kOdd + lane) * VEC;
 #pragma unroll

@@ -64,7 +64,8 @@ def test_layer_norm(M, D):
         same(lambda: mx.layer_norm_backward(dy, saved, w, mean, rstd))
 
 
-@pytest.mark.parametrize("M,F", [(1, 1), (5, 33), (9, 62), (130, 32), (129, 96), (64, 128), (3, 4096)])
+@pytest.mark.parametrize("M,F", [(1, 1), (5, 33), (9, 62), (130, 32), (129, 96), (64, 128), (3, 4096),
+                                 (12501, 4096)])
 def test_swiglu(M, F):
     gu, dh = rnd((M, 2 * F), 1), rnd((M, F), 2)
     same(lambda: mx.swiglu(gu))

@@ -144,9 +144,11 @@ struct NormParams {
   uint64_t stall_ns;
 };
 
-// EPT values a thread, as pairs.
-template <bool SAVE, bool ODD, typename W, int EPT>
-__global__ void __launch_bounds__(kRingThreads, 1) norm_kernel(const NormParams p) {
+// EPT values a thread, as pairs, and R rows a turn, which share a reading of w and b
+// and the reductions' barriers.
+template <bool SAVE, bool ODD, typename W, int EPT, int R>
+__global__ void __launch_bounds__(R == 1 ? kRingThreads : kBackThreads, 1)
+    norm_kernel(const NormParams p) {
   constexpr int V = EPT / 8;
   asm volatile("griddepcontrol.launch_dependents;");
   extern __shared__ __align__(128) uint8_t ring[];
@@ -205,78 +207,118 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_kernel(const NormParams 
   const int first = grp.warp * 32 * V + lane;
   const int pieces = span.total - first;       // live: 32 i < pieces
   const int scaled = SAVE && (lane & 3) == 0 ? 16 * p.s_words - first : 0;
+  auto group_sums = [&](float (&v)[R]) {
+    if constexpr (R == 1) {
+      v[0] = grp.sum(v[0]);
+    } else {
+      const float2 s = grp.sum2(v[0], v[1]);
+      v[0] = s.x;
+      v[1] = s.y;
+    }
+  };
   int st = 0;
   uint32_t parity = 0;
-  for (int64_t r = r0; r < p.M; r += step) {
-    mbar_wait(&bars[st], parity, aborted);
-    const uint8_t* row = mine + st * stage_bytes + first * 16;
-    uint8_t* q = SAVE ? p.q + r * p.D + first * 8 : nullptr;
-    uint8_t* s = SAVE ? p.s + blocked_offset(r, 0, 4 * p.s_words) + (first >> 4) * 512 +
-                            (first >> 2 & 3)
-                      : nullptr;
-    f32x2 x[EPT / 2];
-    f32x2 s2 = 0, s3 = 0;
+  for (int64_t r = r0; r < p.M; r += R * step) {
+    f32x2 x[R][EPT / 2];
+    float mean[R], rstd[R];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      uint4 v = *reinterpret_cast<const uint4*>(row + i * 512);
-      span.clear(v, first + 32 * i);
-      get_pairs(v, x + 4 * i);
-      s2 = add2(s2, add2(x[4 * i], x[4 * i + 1]));
-      s3 = add2(s3, add2(x[4 * i + 2], x[4 * i + 3]));
-      if constexpr (SAVE) {
-        uint32_t sb;
-        const uint2 o = mx_cast_pairs(v, x + 4 * i, sb);
-        if (32 * i < pieces && in_span(p.sp_q, q + i * 256, 8))
-          *reinterpret_cast<uint2*>(q + i * 256) = o;
-        if (32 * i < scaled && in_span(p.sp_s, s + i * 1024, 1))
-          s[i * 1024] = static_cast<uint8_t>(sb);
+    for (int k = 0; k < R; ++k) {
+      mean[k] = 0.0f;
+      if (k > 0 && r + k * step >= p.M) continue;
+      const int64_t rk = r + k * step;
+      mbar_wait(&bars[st], parity, aborted);
+      const uint8_t* row = mine + st * stage_bytes + first * 16;
+      if (++st == sh.stages) {
+        st = 0;
+        parity ^= 1;
       }
-    }
-    const float mean = grp.sum(sum_pair(add2(s2, s3))) * inv;
-    if (sh.warps == 1) __syncwarp();
-    // Every thread of the group has read the row: fill its place again.
-    if (tid == 0 && r + sh.stages * step < p.M && !*aborted) {
-      if (kDiagStall && blockIdx.x == 0 && g == 0 && issued == p.stall_at) {
-        mbar_wait(&stall_bar, 0u, &abort_flag, p.stall_ns);
-      } else {
-        issue(st, r + sh.stages * step);
-        ++issued;
-      }
-    }
-    s2 = s3 = 0;
+      uint8_t* q = SAVE ? p.q + rk * p.D + first * 8 : nullptr;
+      uint8_t* s = SAVE ? p.s + blocked_offset(rk, 0, 4 * p.s_words) + (first >> 4) * 512 +
+                              (first >> 2 & 3)
+                        : nullptr;
+      f32x2 s2 = 0, s3 = 0;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const float m = 32 * i < pieces ? -mean : 0.0f;      // padding stays 0
-      const f32x2 m2 = pair(m, m);
-#pragma unroll
-      for (int j = 4 * i; j < 4 * i + 4; ++j) x[j] = add2(x[j], m2);
-      if (span.edge(first + 32 * i)) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float lo, hi;
-          unpair(x[4 * i + j], lo, hi);
-          const int e = 8 * (first + 32 * i) + 2 * j;
-          x[4 * i + j] = pair(span.holds(e) ? lo : 0.0f, span.holds(e + 1) ? hi : 0.0f);
+      for (int i = 0; i < V; ++i) {
+        f32x2* xi = x[k] + 4 * i;
+        uint4 v = *reinterpret_cast<const uint4*>(row + i * 512);
+        span.clear(v, first + 32 * i);
+        get_pairs(v, xi);
+        s2 = add2(s2, add2(xi[0], xi[1]));
+        s3 = add2(s3, add2(xi[2], xi[3]));
+        if constexpr (SAVE) {
+          uint32_t sb;
+          const uint2 o = mx_cast_pairs(v, xi, sb);
+          if (32 * i < pieces && in_span(p.sp_q, q + i * 256, 8))
+            *reinterpret_cast<uint2*>(q + i * 256) = o;
+          if (32 * i < scaled && in_span(p.sp_s, s + i * 1024, 1))
+            s[i * 1024] = static_cast<uint8_t>(sb);
         }
       }
-#pragma unroll
-      for (int j = 4 * i; j < 4 * i + 4; j += 2) {
-        s2 = fma2(x[j], x[j], s2);
-        s3 = fma2(x[j + 1], x[j + 1], s3);
+      mean[k] = sum_pair(add2(s2, s3));
+    }
+    group_sums(mean);
+    if (sh.warps == 1) __syncwarp();
+    // Every thread of the group has read the rows: fill their places again.
+    if (tid == 0) {
+      for (int64_t k = r + sh.stages * step; k < r + (sh.stages + R) * step && k < p.M && !*aborted;
+           k += step) {
+        if (kDiagStall && blockIdx.x == 0 && g == 0 && issued == p.stall_at) {
+          mbar_wait(&stall_bar, 0u, &abort_flag, p.stall_ns);
+        } else {
+          issue(issued % sh.stages, k);
+          ++issued;
+        }
       }
     }
-    const float rstd = rsqrtf(grp.sum(sum_pair(add2(s2, s3))) * inv + p.eps);
-    if (tid == 0) {
-      if (in_span(p.sp_mean, p.mean + r, 4)) p.mean[r] = mean;
-      if (in_span(p.sp_rstd, p.rstd + r, 4)) p.rstd[r] = rstd;
-    }
-    const f32x2 r2 = pair(rstd, rstd);
-    uint16_t* y = p.y + r * p.D - span.lead;
-    auto put = [&](int i, const f32x2* wv, const f32x2* bv) {
-      f32x2 o[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) o[j] = fma2(mul2(x[4 * i + j], r2), wv[j], bv[j]);
-      span.store(y, first + 32 * i, o, p.sp_y);
+    for (int k = 0; k < R; ++k) {
+      rstd[k] = 0.0f;
+      if (k > 0 && r + k * step >= p.M) continue;
+      mean[k] *= inv;
+      f32x2 s2 = 0, s3 = 0;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        f32x2* xi = x[k] + 4 * i;
+        const float m = 32 * i < pieces ? -mean[k] : 0.0f;      // padding stays 0
+        const f32x2 m2 = pair(m, m);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) xi[j] = add2(xi[j], m2);
+        if (span.edge(first + 32 * i)) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float lo, hi;
+            unpair(xi[j], lo, hi);
+            const int e = 8 * (first + 32 * i) + 2 * j;
+            xi[j] = pair(span.holds(e) ? lo : 0.0f, span.holds(e + 1) ? hi : 0.0f);
+          }
+        }
+        s2 = fma2(xi[0], xi[0], s2);
+        s3 = fma2(xi[1], xi[1], s3);
+        s2 = fma2(xi[2], xi[2], s2);
+        s3 = fma2(xi[3], xi[3], s3);
+      }
+      rstd[k] = sum_pair(add2(s2, s3));
+    }
+    group_sums(rstd);
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      rstd[k] = rsqrtf(rstd[k] * inv + p.eps);
+      const int64_t rk = r + k * step;
+      if (tid == 0 && (k == 0 || rk < p.M)) {
+        if (in_span(p.sp_mean, p.mean + rk, 4)) p.mean[rk] = mean[k];
+        if (in_span(p.sp_rstd, p.rstd + rk, 4)) p.rstd[rk] = rstd[k];
+      }
+    }
+    auto put = [&](int i, const f32x2* wv, const f32x2* bv) {
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        if (k > 0 && r + k * step >= p.M) continue;
+        const f32x2 r2 = pair(rstd[k], rstd[k]);
+        f32x2 o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] = fma2(mul2(x[k][4 * i + j], r2), wv[j], bv[j]);
+        span.store(p.y + (r + k * step) * p.D - span.lead, first + 32 * i, o, p.sp_y);
+      }
     };
     if (ODD || p.staged) {
 #pragma unroll
@@ -296,10 +338,6 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_kernel(const NormParams 
         }
         put(i, wv, bv);
       }
-    }
-    if (++st == sh.stages) {
-      st = 0;
-      parity ^= 1;
     }
   }
   if (SAVE && blockIdx.x == 0) {
@@ -645,21 +683,23 @@ int allow_ring(K kernel) {
       kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes));
 }
 
-template <bool SAVE, bool ODD, typename W, int EPT>
+template <bool SAVE, bool ODD, typename W, int EPT, int R = 1>
 int run_norm(NormParams p, int num_sms, cudaStream_t stream) {
   // With a row or two a group, w and b are not worth a copy of their own.
   p.staged = ODD || p.M > 8 * static_cast<int64_t>(num_sms);
   const int param = p.staged ? 8 : 0;
-  p.shape = ring_shape(p.M, p.D + (ODD ? 7 : 0), EPT, kRingThreads, 2, param, num_sms);
+  p.shape = ring_shape(p.M, p.D + (ODD ? 7 : 0), EPT, R == 1 ? kRingThreads : kBackThreads, 2,
+                       param, num_sms);
+  if (p.shape.stages < R) return static_cast<int>(cudaErrorInvalidConfiguration);   // no width is
   const int64_t smem = static_cast<int64_t>(p.shape.pitch) *
                        (p.shape.groups * p.shape.stages * 2 + param);
   static DeviceCache attr_cache;
-  const int attr = attr_cache.get([] { return allow_ring(norm_kernel<SAVE, ODD, W, EPT>); });
+  const int attr = attr_cache.get([] { return allow_ring(norm_kernel<SAVE, ODD, W, EPT, R>); });
   if (attr != 0) return attr;
   const Stall stall = take_stall();
   p.stall_at = stall.at;
   p.stall_ns = stall.ns;
-  return launch(norm_kernel<SAVE, ODD, W, EPT>, dim3(grid_of(p.M, ODD, num_sms)),
+  return launch(norm_kernel<SAVE, ODD, W, EPT, R>, dim3(grid_of(p.M, ODD, num_sms)),
                 32 * p.shape.warps * p.shape.groups, static_cast<int>(smem), stream, p);
 }
 
@@ -703,7 +743,7 @@ int pick_norm(const NormParams& p, int num_sms, cudaStream_t stream) {
   if (n == 16) return run_norm<SAVE, ODD, W, 16>(p, num_sms, stream);
   if constexpr (ODD)
     if (n == 40) return run_norm<SAVE, ODD, W, 40>(p, num_sms, stream);
-  return run_norm<SAVE, ODD, W, 32>(p, num_sms, stream);
+  return run_norm<SAVE, ODD, W, 32, 2>(p, num_sms, stream);
 }
 
 template <bool SAVE, bool ODD, typename W>

@@ -274,8 +274,10 @@ int mx_cast_rowwise(const void* x, int64_t M, int64_t K, void* q, void* scale, v
  *           its scales as always by row and 32 contraction steps
  *   out     M x N values of out_type (MX_BF16 or MX_F32)    [out]
  * A NaN scale (0xFF) or element makes the results that use it NaN; sums
- * beyond the output type's range give infinity.  A call gives the same bits
- * every time. */
+ * beyond the output type's range give infinity, sums below 2^-126 may come out as
+ * zero.  For an fp32 output longer sums are formed 4096 steps at a time, each run
+ * in the tensor core's accumulator, which cuts bits off where fp32 would round.
+ * A call gives the same bits every time. */
 int mx_matmul(const void* qa, const void* sa_blk, const void* qb, const void* sb_blk, int64_t M,
               int64_t N, int64_t K, int32_t orders, void* out, int32_t out_type, void* stream);
 
@@ -321,7 +323,7 @@ int mx_layer_norm_backward(const void* dy, const void* x, const void* q0, const 
  * have no counterpart (see mx_layer_norm).
  *   h = g u / (1 + exp(-g)), rounded once to bf16
  *   gu      bf16 (M x 2F): g in columns [0, F), u in [F, 2F)    [in]
- *   M, F    >= 1; with a saved input F % 32 == 0
+ *   M, F    M >= 1, 1 <= F <= 2^24; with a saved input F % 32 == 0
  *   h       bf16 (M x F)                                        [out]
  *   q0, s0_blk  both NULL, or gu saved: mx_cast_dim0's outputs for gu, byte
  *           for byte                                            [out] */

@@ -524,7 +524,7 @@ int mx_layer_norm_backward(const void* dy, const void* x, const void* q0, const 
 int mx_swiglu(const void* gu, int64_t M, int64_t F, void* h, void* q0, void* s0_blk,
               void* stream) {
   if (!gu || !h || !q0 != !s0_blk) return MX_ERR_NULL;
-  if (M < 1 || F < 1 || M > kMaxDim || F > kMaxDim / 2 || (q0 && F % 32 != 0)) return MX_ERR_SHAPE;
+  if (M < 1 || F < 1 || M > kMaxDim || F > mx::kSwigluMaxWidth || (q0 && F % 32 != 0)) return MX_ERR_SHAPE;
   if (!aligned(gu, 16) || !aligned(h, 16) || !aligned(q0, 16) || !aligned(s0_blk, 16))
     return MX_ERR_ALIGN;
   if (int rc = check_device({gu, h, q0, s0_blk})) return rc;
@@ -537,7 +537,7 @@ int mx_swiglu(const void* gu, int64_t M, int64_t F, void* h, void* q0, void* s0_
 int mx_swiglu_backward(const void* dh, const void* gu, const void* q0, const void* s0_blk,
                        int64_t M, int64_t F, void* dgu, void* stream) {
   if (!dh || !dgu || !q0 != !s0_blk || !gu == !q0) return MX_ERR_NULL;
-  if (M < 1 || F < 1 || M > kMaxDim || F > kMaxDim / 2 || (q0 && F % 32 != 0)) return MX_ERR_SHAPE;
+  if (M < 1 || F < 1 || M > kMaxDim || F > mx::kSwigluMaxWidth || (q0 && F % 32 != 0)) return MX_ERR_SHAPE;
   if (!aligned(dh, 16) || !aligned(gu, 16) || !aligned(q0, 16) || !aligned(s0_blk, 16) ||
       !aligned(dgu, 16))
     return MX_ERR_ALIGN;

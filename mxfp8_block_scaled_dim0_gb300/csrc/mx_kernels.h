@@ -161,6 +161,8 @@ constexpr int64_t kNormMaxWidth = 16384;
 int64_t norm_back_work_floats(int64_t M, int64_t D);
 int launch_layer_norm(const LayerNormArgs& a, int num_sms, cudaStream_t stream);
 int launch_layer_norm_backward(const LayerNormBackArgs& a, int num_sms, cudaStream_t stream);
+// Widest half of a row: a row's scale bytes are counted in 32 bits.
+constexpr int64_t kSwigluMaxWidth = int64_t{1} << 24;
 // Gated SiLU (mx_swiglu.cu).  Forward: gu -> out = h, saved into q, s unless
 // null.  Backward: dh and gu, or q, s -> out = the gradient of gu.
 struct SwigluArgs {

@@ -43,6 +43,8 @@ bool is_bytes(ScalarType t) {
   return t == at::kByte || t == at::kFloat8_e4m3fn || t == at::kFloat8_e8m0fnu;
 }
 
+bool is_bool(PyObject* o) { return o == Py_True || o == Py_False; }
+
 bool plain(const Tensor& t) { return t.layout() == at::kStrided && t.is_contiguous(); }
 
 bool is_2d(const Tensor* t, ScalarType type) {
@@ -65,9 +67,11 @@ int64_t blocked_bytes(int64_t R, int64_t C) { return (R + 127) / 128 * 128 * ((C
 
 // Index of the current device if all tensors live there, or -1.
 int common_device(std::initializer_list<const Tensor*> ts) {
+  for (const Tensor* t : ts)
+    if (t && !t->is_cuda()) return -1;
   const int dev = c10::cuda::current_device();
   for (const Tensor* t : ts)
-    if (t && (!t->is_cuda() || t->get_device() != dev)) return -1;
+    if (t && t->get_device() != dev) return -1;
   return dev;
 }
 
@@ -177,7 +181,8 @@ PyObject* layer_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor *x = tensor(a[1]), *w = tensor(a[2]), *b = tensor(a[3]);
   const double eps = PyFloat_CheckExact(a[4]) ? PyFloat_AS_DOUBLE(a[4]) : -1.0;
   const bool save = a[5] == Py_True;
-  if (!is_2d(x, at::kBFloat16) || !w || (!b && a[3] != Py_None) || eps < 0) Py_RETURN_NONE;
+  if (!is_2d(x, at::kBFloat16) || !w || (!b && a[3] != Py_None) || eps < 0 || !is_bool(a[5]))
+    Py_RETURN_NONE;
   const int64_t M = x->size(0), D = x->size(1);
   const ScalarType wt = w->scalar_type();
   if ((wt != at::kFloat && wt != at::kBFloat16) || !is_1d(w, wt, D) || (b && !is_1d(b, wt, D)))
@@ -217,7 +222,7 @@ PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor *dy = tensor(a[2]), *x = tensor(a[3]), *w = tensor(a[4]), *mean = tensor(a[5]),
                *rstd = tensor(a[6]), *q = nullptr, *s = nullptr;
   const bool bias = a[7] == Py_True;
-  if (!is_2d(dy, at::kBFloat16) || !w) Py_RETURN_NONE;
+  if (!is_2d(dy, at::kBFloat16) || !w || !is_bool(a[7])) Py_RETURN_NONE;
   const int64_t M = dy->size(0), D = dy->size(1);
   const ScalarType wt = w->scalar_type();
   if ((wt != at::kFloat && wt != at::kBFloat16) || !is_1d(w, wt, D) ||
@@ -255,7 +260,7 @@ PyObject* swiglu(PyObject*, PyObject* const* a, Py_ssize_t n) {
   using Fn = int (*)(const void*, int64_t, int64_t, void*, void*, void*, void*);
   const Tensor* gu = tensor(a[1]);
   const bool save = a[2] == Py_True;
-  if (!is_2d(gu, at::kBFloat16) || gu->size(1) % 2 != 0) Py_RETURN_NONE;
+  if (!is_2d(gu, at::kBFloat16) || gu->size(1) % 2 != 0 || !is_bool(a[2])) Py_RETURN_NONE;
   const int64_t M = gu->size(0), F = gu->size(1) / 2;
   const int dev = common_device({gu});
   if (dev < 0) Py_RETURN_NONE;

@@ -1,4 +1,7 @@
-"""Refusals of the training operators' C entry points, before any CUDA call."""
+"""Refusals of the training operators, before any CUDA call: their C entry points
+and their allocating wrappers."""
+import torch
+
 import mxfp8_block_scaled_dim0_gb300 as mx
 from mxfp8_block_scaled_dim0_gb300 import build as mxbuild
 import pytest
@@ -70,5 +73,34 @@ def test_swiglu_refuses(lib):
     for name in ("dh", "q", "s", "out"):
         assert back(**{name: None}) == mx.MX_ERR_NULL and back(**{name: B}) == mx.MX_ERR_ALIGN
     assert back(gu=A) == mx.MX_ERR_NULL and back(q=None, s=None) == mx.MX_ERR_NULL
-    for bad in (dict(M=0), dict(F=0), dict(F=48), dict(M=1 << 31), dict(F=1 << 30)):
+    for bad in (dict(M=0), dict(F=0), dict(F=48), dict(M=1 << 31), dict(F=(1 << 24) + 32)):
         assert fwd(**bad) == mx.MX_ERR_SHAPE and back(**bad) == mx.MX_ERR_SHAPE
+
+
+def test_wrappers_refuse_cpu_tensors_and_wrong_types(lib):
+    x, w = torch.zeros(64, 96, dtype=torch.bfloat16), torch.zeros(96)
+    q, s = torch.zeros(64, 96, dtype=torch.uint8), torch.zeros(128 * 4, dtype=torch.uint8)
+    stats = torch.zeros(64)
+    for call in (lambda: mx.layer_norm(x, w), lambda: mx.layer_norm(x, w, save=True),
+                 lambda: mx.layer_norm_backward(x, x, w, stats, stats),
+                 lambda: mx.layer_norm_backward(x, (q, s), w, stats, stats),
+                 lambda: mx.swiglu(x), lambda: mx.swiglu(x, save=False),
+                 lambda: mx.swiglu_backward(x[:, :48].contiguous(), x),
+                 lambda: mx.matmul(q, s, q, s), lambda: mx.cast_dim0(x), lambda: mx.cast_dim1(x),
+                 lambda: mx.cast_dim0_dim1(x)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
+    for call in (lambda: mx.layer_norm(x.float(), w), lambda: mx.layer_norm(x, w.double()),
+                 lambda: mx.layer_norm(x, w, w.to(torch.bfloat16)),
+                 lambda: mx.swiglu(x.half()), lambda: mx.swiglu_backward(x.float(), x),
+                 lambda: mx.matmul(x, s, q, s), lambda: mx.matmul(q, s, q, s, torch.float16)):
+        with pytest.raises(TypeError):
+            call()
+    for call in (lambda: mx.layer_norm(x.t(), w), lambda: mx.layer_norm(x, w[:5]),
+                 lambda: mx.layer_norm_backward(x, x, w, stats[:3], stats),
+                 lambda: mx.layer_norm_backward(x, (q[:5], s), w, stats, stats),
+                 lambda: mx.swiglu(x[:, :33].contiguous()), lambda: mx.swiglu_backward(x, x),
+                 lambda: mx.matmul(q, s, q[:, :64].contiguous(), s),
+                 lambda: mx.matmul(q, s[:9], q, s)):
+        with pytest.raises(ValueError):
+            call()

@@ -1,6 +1,8 @@
 /*
  * mxfp8_cast.h -- C ABI of libmxfp8_cast.so: MX-FP8 (e4m3 elements, e8m0
- * block scales, blocks of 32) quantisation of bf16 matrices on sm_103a.
+ * block scales, blocks of 32) quantisation of bf16 matrices on sm_103a, and the
+ * operators that train on such values: products of two MX operands, layer norm
+ * and gated SiLU whose inputs are saved for the backward pass in MX-FP8.
  *
  * Conventions for every entry point below
  *   - All data pointers are DEVICE pointers of the calling thread's current
@@ -390,9 +392,11 @@ int mx_selftest_watchdog(int64_t wait_ns, void* stream);
  * of a kernel whose waits are bounded (the cast kernels of mx_cast_dim0_dim1,
  * mx_cast_dim0, mx_cast_dim1, mx_cast_grouped_m and the 3D casts; the
  * bulk-staged kernel of mx_cast_rowwise, used for K <= 24576; the tiled
- * kernel of mx_dequant_blocked, used for C >= 1024).  In that launch the
+ * kernel of mx_dequant_blocked, used for C >= 1024; the kernels of mx_matmul,
+ * mx_layer_norm and the first of mx_layer_norm_backward).  In that launch the
  * thread of CTA 0 that issues its loads waits, at its `at`-th tile (rowwise:
- * step), on a barrier that nothing completes, for at most `wait_ns` nanoseconds
+ * step; mx_matmul: block of 128 contraction steps; layer norm: row of its first
+ * group), on a barrier that nothing completes, for at most `wait_ns` nanoseconds
  * (1e3 .. 1e10).  The wait gives up, the CTA stops every role, lets the
  * copies it has in flight land, sets the word read by mx_watchdog(), and the
  * kernel returns normally: the abort path of a real cast, exercised without

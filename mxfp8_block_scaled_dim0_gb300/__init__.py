@@ -1,4 +1,5 @@
-"""MX-FP8 casts of bf16 matrices on sm_103a (GB300): Python binding.
+"""MX-FP8 casts of bf16 matrices, and operators that train on their outputs, on
+sm_103a (GB300): Python binding.
 
 Thin ctypes layer over the C ABI of ``libmxfp8_cast.so`` (declared in
 ``include/mxfp8_cast.h``).  Functions named like the C entry points take torch
@@ -11,7 +12,12 @@ raises.
 Convenience wrappers (``cast_dim0_dim1``, ``cast_dim0``, ``cast_dim1``,
 ``cast_grouped_m``, ``cast_3d_dim1``, ``cast_3d_dim0``, ``cast_3d_dim0_dim1``,
 ``scales_to_blocked``, ``dequant_blocked``, ``cast_tensorwise``,
-``cast_rowwise``) allocate outputs with torch and call the same entry points.
+``cast_rowwise``, ``matmul``, ``layer_norm``, ``layer_norm_backward``,
+``swiglu``, ``swiglu_backward``) allocate outputs with torch and call the same
+entry points; the 2D casts and the last five in compiled code
+(``_torch_call.so``), which hands every call it does not take as it stands to
+the checked functions here.  ``feed_forward`` is a block of a network trained
+with them.
 """
 import ctypes
 import functools

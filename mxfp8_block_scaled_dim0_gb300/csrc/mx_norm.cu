@@ -15,6 +15,13 @@
 // conditions.  (Rows loaded a row ahead into registers, four CTAs an SM: 94 us
 // forward and 159 us backward at 16640 x 5120 with the 8-bit save.)
 //
+// Every tensor crosses the memory bus once: 5 bytes a value forward with the save
+// and backward from it, 6 backward from bf16.  16640 x 5120: forward with the save
+// 74 us (5.8 TB/s), backward from 8 bits 94 us (4.5 TB/s, the gradient kernel's
+// 5 us in it), from bf16 87 us (5.9 TB/s); 1 x 4096 forward 2.4 us.  Forward is
+// bound by the way through shared memory (waits for its loads, 52% of the issue
+// slots taken), backward by issue and by the few warps that dw and db leave room for.
+//
 // Bulk copies and 16-byte accesses want 16-byte boundaries.  Where the row length
 // is no multiple of 8 values, rows r and r + 8 begin at the same distance from
 // one: the grid is a multiple of 8, so that all rows of a CTA have the same
@@ -160,7 +167,7 @@ __global__ void __launch_bounds__(R == 1 ? kRingThreads : kBackThreads, 1)
   const RowSpan<ODD> span(p.D);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = warp / sh.warps;
-  Group<16> grp{red + 128 * g, g + 1, sh.warps, warp - g * sh.warps, lane, 0};
+  Group grp{red + 128 * g, g + 1, sh.warps, warp - g * sh.warps, lane, 0};
   const int T = 32 * sh.warps, tid = grp.warp * 32 + lane;
   const int stage_bytes = 2 * sh.pitch;
   const int places = sh.groups * sh.stages;
@@ -392,7 +399,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) norm_back_kernel(const NormBa
   const RowSpan<ODD> span(p.D);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = warp / sh.warps;
-  Group<16> grp{red + 128 * g, g + 1, sh.warps, warp - g * sh.warps, lane, 0};
+  Group grp{red + 128 * g, g + 1, sh.warps, warp - g * sh.warps, lane, 0};
   const int T = 32 * sh.warps, tid = grp.warp * 32 + lane;
   const int x_at = 2 * sh.pitch, stage_bytes = (SAVE ? 3 : 4) * sh.pitch;
   const int places = sh.groups * sh.stages;

@@ -1,6 +1,7 @@
 // mx_rows.cuh -- what the layer norm and gated SiLU kernels share: row pieces
-// of 8, 2 or 1 bf16 values in registers, the MX cast of a row held by a warp
-// group, MX values back from their bytes, and sums over a warp group.
+// of 8, 2 or 1 bf16 values in registers, fp32 arithmetic on pairs, the MX cast of
+// blocks held by four lanes, MX values back from their bytes, and sums over a
+// group of warps.
 #pragma once
 
 #include "mx_common.cuh"
@@ -26,10 +27,6 @@ struct Piece<8> {
     asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
                  : "l"(p));
-  }
-  __device__ __forceinline__ void get(float* v) const {
-    v[0] = bf_lo(w.x); v[1] = bf_hi(w.x); v[2] = bf_lo(w.y); v[3] = bf_hi(w.y);
-    v[4] = bf_lo(w.z); v[5] = bf_hi(w.z); v[6] = bf_lo(w.w); v[7] = bf_hi(w.w);
   }
 };
 
@@ -61,57 +58,16 @@ struct Piece<1> {
 template <int VEC>
 __device__ __forceinline__ void store_bf16(uint16_t* p, const float* v, const Span& sp) {
   if (!in_span(sp, p, 2 * VEC)) return;
-  if constexpr (VEC == 8)
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
-                                              pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-  else if constexpr (VEC == 2)
+  if constexpr (VEC == 2)
     *reinterpret_cast<uint32_t*>(p) = pack_bf16(v[0], v[1]);
   else
     *p = static_cast<uint16_t>(pack_bf16(v[0], 0.0f));
 }
 
-// VEC parameters (fp32 or bf16) as floats; read by every row, so through L1.
-template <int VEC>
-__device__ __forceinline__ void load_param(const float* p, float* v) {
-  if constexpr (VEC == 8) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-    const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  } else if constexpr (VEC == 2) {
-    const float2 a = __ldg(reinterpret_cast<const float2*>(p));
-    v[0] = a.x; v[1] = a.y;
-  } else {
-    v[0] = __ldg(p);
-  }
-}
-
-template <int VEC>
-__device__ __forceinline__ void load_param(const uint16_t* p, float* v) {
-  if constexpr (VEC == 8) {
-    Piece<8> w;
-    w.w = __ldg(reinterpret_cast<const uint4*>(p));
-    w.get(v);
-  } else if constexpr (VEC == 2) {
-    const uint32_t a = __ldg(reinterpret_cast<const uint32_t*>(p));
-    v[0] = bf_lo(a); v[1] = bf_hi(a);
-  } else {
-    v[0] = __uint_as_float(static_cast<uint32_t>(__ldg(p)) << 16);
-  }
-}
-
-// MX cast of one 32-block held as eight values by each of four neighbouring
-// lanes: this lane's eight e4m3 bytes and the block's scale byte (the same in
-// the four lanes).  Every lane of the warp takes part.
-__device__ __forceinline__ uint2 mx_cast_piece(const uint4& w, uint32_t& sbyte) {
-  uint32_t m = absmax2(absmax2(w.x, w.y), absmax2(w.z, w.w));
-  m = max(mag_lo(m), mag_hi(m));
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  float mult;
-  mx_scale(m, sbyte, mult);
-  return make_uint2(e4m3x4(bf_lo(w.x), bf_hi(w.x), bf_lo(w.y), bf_hi(w.y), mult),
-                    e4m3x4(bf_lo(w.z), bf_hi(w.z), bf_lo(w.w), bf_hi(w.w), mult));
+// One parameter (fp32 or bf16).
+__device__ __forceinline__ float load_param(const float* p) { return __ldg(p); }
+__device__ __forceinline__ float load_param(const uint16_t* p) {
+  return __uint_as_float(static_cast<uint32_t>(__ldg(p)) << 16);
 }
 
 // 2^(s - 127) of a scale byte; 0xFF is NaN.  The exponent field, but for s = 0 a
@@ -127,17 +83,6 @@ __device__ __forceinline__ void e4m3x2_get(uint32_t pair, float& lo, float& hi) 
   asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
       : "=f"(lo), "=f"(hi)
       : "r"(h));
-}
-
-// Eight saved values: e4m3 bytes times their block's scale.
-__device__ __forceinline__ void mx_get8(const uint2& q, uint32_t sbyte, float* v) {
-  const float m = scale_mult(sbyte);
-  e4m3x2_get(q.x & 0xFFFFu, v[0], v[1]);
-  e4m3x2_get(q.x >> 16, v[2], v[3]);
-  e4m3x2_get(q.y & 0xFFFFu, v[4], v[5]);
-  e4m3x2_get(q.y >> 16, v[6], v[7]);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = mul_rn(v[j], m);
 }
 
 __device__ __forceinline__ uint2 ld_q8(const uint8_t* p) {
@@ -231,8 +176,7 @@ __device__ __forceinline__ void stage_params(float* dst, const W* src, int lead,
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int e = 8 * c + j - lead;
-        f[j] = 0.0f;
-        if (e >= 0 && e < D) load_param<1>(src + e, f + j);
+        f[j] = e >= 0 && e < D ? load_param(src + e) : 0.0f;
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[j] = pair(f[2 * j], f[2 * j + 1]);
@@ -261,7 +205,10 @@ __device__ __forceinline__ uint32_t e4m3_pair(f32x2 v) {
   return r;
 }
 
-// mx_cast_piece for values that are at hand as pairs too (v: those of w).
+// MX cast of one 32-block held as eight values by each of four neighbouring
+// lanes (w, and v, the same as pairs): this lane's eight e4m3 bytes and the
+// block's scale byte (the same in the four lanes).  Every lane of the warp takes
+// part.
 __device__ __forceinline__ uint2 mx_cast_pairs(const uint4& w, const f32x2* v, uint32_t& sbyte) {
   uint32_t m = absmax2(absmax2(w.x, w.y), absmax2(w.z, w.w));
   m = max(mag_lo(m), mag_hi(m));
@@ -295,13 +242,12 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Sums over a group of `warps` <= MAXW warps that meet at named barrier `id`.
+// Sums over a group of `warps` <= 16 warps that meet at named barrier `id`.
 // `red` holds two slots of 64 floats, zero at the start and used in turn, so that
 // one barrier a sum is enough: a slot is written again only after the other
 // slot's barrier, which every thread reaches after its reads of this one.  Two
 // sums travel together, one in either half of a warp after the first exchange.
 // The order of the additions is fixed.
-template <int MAXW>
 struct Group {
   float* red;
   int id, warps, warp, lane;
@@ -312,10 +258,9 @@ struct Group {
     else
       asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(32 * warps) : "memory");
   }
-  // The sum of v[0..MAXW), in every lane.
+  // The sum of v[0..16), in every lane.
   __device__ __forceinline__ float across(const float* v) const {
     float a = v[lane & 15];
-    if (MAXW > 16) a += v[16 + (lane & 15)];
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
     return a;

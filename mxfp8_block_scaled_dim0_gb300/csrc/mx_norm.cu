@@ -468,6 +468,23 @@ __global__ void __launch_bounds__(kBackThreads, 1) norm_back_kernel(const NormBa
     }
   };
   fetch(r0);
+  // Fills the place of row r, which every thread of the group has read.  From 8
+  // bits, where three rows at least fit, this waits for the barrier of the next
+  // row's sums, and a row needs no second one (16640 x 5120 95.1 -> 88.7 us, 4096 x
+  // 16384 79.6 -> 73.7); with the two bf16 rows that fit at wide rows that is too
+  // late (8192 x 8192 68.4 us, 82.2 so; 16640 x 5120, three rows, 85.6 and 84.1),
+  // and a choice at run time costs what it gains.
+  constexpr bool late = SAVE;
+  auto refill = [&](int64_t r) {
+    r += sh.stages * step;
+    if (r >= p.M || *aborted) return;
+    if (kDiagStall && blockIdx.x == 0 && g == 0 && issued == p.stall_at) {
+      mbar_wait(&stall_bar, 0u, &abort_flag, p.stall_ns);
+      return;
+    }
+    issue(issued % sh.stages, r);
+    ++issued;
+  };
   int st = 0;
   uint32_t parity = 0;
   for (int64_t r = r0; r < p.M; r += step) {
@@ -527,7 +544,10 @@ __global__ void __launch_bounds__(kBackThreads, 1) norm_back_kernel(const NormBa
       }
     }
     const float2 t = grp.sum2(sum_pair(s1), sum_pair(s2));
+    if (sh.warps == 1) __syncwarp();
     asm volatile("" ::: "memory");           // the second pass reads anew
+    // Every thread of the group is past the row before this one.
+    if (late && tid == 0 && r > r0) refill(r - step);
     // dx = rstd g - rstd c1 - (x - mean) rstd^2 c2
     const float c1 = -rstd * (t.x * inv), c2 = -rstd * (t.y * inv) * rstd;
     const f32x2 k1 = pair(c1, c1), k2 = pair(c2, c2);
@@ -542,15 +562,9 @@ __global__ void __launch_bounds__(kBackThreads, 1) norm_back_kernel(const NormBa
       for (int j = 0; j < 4; ++j) d[j] = fma2(xv[j], k2, fma2(mul2(d[j], wv[j]), rs, k1));
       span.store(dx, first + 32 * i, d, p.sp_dx);
     }
-    grp.meet();
-    // Every thread of the group has read the row: fill its place again.
-    if (tid == 0 && r + sh.stages * step < p.M && !*aborted) {
-      if (kDiagStall && blockIdx.x == 0 && g == 0 && issued == p.stall_at) {
-        mbar_wait(&stall_bar, 0u, &abort_flag, p.stall_ns);
-      } else {
-        issue(st, r + sh.stages * step);
-        ++issued;
-      }
+    if (!late) {
+      grp.meet();
+      if (tid == 0) refill(r);
     }
     if (++st == sh.stages) {
       st = 0;
@@ -715,6 +729,8 @@ int run_norm_back(NormBackParams p, int num_sms, int* grid, cudaStream_t stream)
   constexpr int kRow = SAVE ? 3 : 4;
   p.shape = ring_shape(p.M, p.D + (ODD ? 7 : 0), EPT, kBackThreads, kRow, 4, num_sms);
   const RowShape& s = p.shape;
+  // No width is: 3 x 16384 bytes and 4 x 16384 of parameters fit three times, 4 x twice.
+  if (s.stages < (SAVE ? 3 : 2)) return static_cast<int>(cudaErrorInvalidConfiguration);
   int64_t smem = static_cast<int64_t>(s.pitch) * (s.groups * s.stages * kRow + 4);
   const int64_t sums = int64_t{8} * EPT * (32 * s.warps + 4) * s.groups;
   if (smem < sums) smem = sums;

@@ -17,8 +17,8 @@
 //
 // Every tensor crosses the memory bus once: 5 bytes a value forward with the save
 // and backward from it, 6 backward from bf16.  16640 x 5120: forward with the save
-// 74 us (5.8 TB/s), backward from 8 bits 94 us (4.5 TB/s, the gradient kernel's
-// 5 us in it), from bf16 87 us (5.9 TB/s); 1 x 4096 forward 2.4 us.  Forward is
+// 74 us (5.8 TB/s), backward from 8 bits 89 us (4.8 TB/s, the gradient kernel's
+// 5 us in it), from bf16 85 us (6.0 TB/s); 1 x 4096 forward 2.4 us.  Forward is
 // bound by the way through shared memory (waits for its loads, 52% of the issue
 // slots taken), backward by issue and by the few warps that dw and db leave room for.
 //
@@ -27,8 +27,9 @@
 // one: the grid is a multiple of 8, so that all rows of a CTA have the same
 // distance, `lead` values, and the CTA works on rows that begin `lead` values
 // early, on the boundary, its w and b shifted by as much.  What a copy brings of
-// the neighbouring rows is cleared where it is read (first and last piece only),
-// and those two pieces are stored value by value.
+// the neighbouring rows (in the first and the last piece) is cleared by the
+// thread that reads it (backward, which reads twice, in shared memory: 16640 x 4099
+// 125 -> 94 us, 16640 x 500 17.2 -> 18.3), and those two pieces are stored value by value.
 //
 // The backward kernel keeps dw and db of its threads' columns in registers over
 // all its rows, adds the groups of a CTA up at its end, and leaves one partial
@@ -93,13 +94,32 @@ struct RowSpan {
   }
   __device__ __forceinline__ bool edge(int c) const { return ODD && (c == 0 || c == total - 1); }
   __device__ __forceinline__ bool holds(int e) const { return e >= lead && e < width; }
-  // Clears what a piece at the row's ends holds of its neighbours.
+  // Bit i: piece first + 32 i, of `n` that a thread works on, is the row's first or
+  // last.
+  __device__ __forceinline__ uint32_t edges(int first, int n) const {
+    uint32_t m = 0;
+    if (ODD)
+      for (int i = 0; i < n; ++i)
+        if (edge(first + 32 * i)) m |= 1u << i;
+    return m;
+  }
+  // Clears what piece c, an edge, holds of the neighbouring rows.
   __device__ __forceinline__ void clear(uint4& v, int c) const {
-    if (!edge(c)) return;
     uint32_t* w = &v.x;
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       w[k] &= (holds(8 * c + 2 * k) ? 0xFFFFu : 0u) | (holds(8 * c + 2 * k + 1) ? 0xFFFF0000u : 0u);
+  }
+  // The same in the row's place (at: piece `first`) for its later reads, all by
+  // this thread.
+  __device__ __forceinline__ void clear_place(uint8_t* at, int first, uint32_t edges) const {
+    for (; edges; edges &= edges - 1) {
+      const int i = __ffs(edges) - 1;
+      uint4* place = reinterpret_cast<uint4*>(at + i * 512);
+      uint4 v = *place;
+      clear(v, first + 32 * i);
+      *place = v;
+    }
   }
   // Stores piece c of the row that begins at `row` (lead included).
   __device__ __forceinline__ void store(uint16_t* row, int c, const f32x2* v, const Span& sp) const {
@@ -248,7 +268,7 @@ __global__ void __launch_bounds__(R == 1 ? kRingThreads : kBackThreads, 1)
       for (int i = 0; i < V; ++i) {
         f32x2* xi = x[k] + 4 * i;
         uint4 v = *reinterpret_cast<const uint4*>(row + i * 512);
-        span.clear(v, first + 32 * i);
+        if (span.edge(first + 32 * i)) span.clear(v, first + 32 * i);
         get_pairs(v, xi);
         s2 = add2(s2, add2(xi[0], xi[1]));
         s3 = add2(s3, add2(xi[2], xi[3]));
@@ -450,6 +470,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) norm_back_kernel(const NormBa
   // Piece i of this thread is piece first + 32 i of the row (a warp's pieces lie
   // together, so that their distances are constants).
   const int first = grp.warp * 32 * V + lane;
+  const uint32_t edges = span.edges(first, V);
   // What the copies do not bring, a row ahead; without a condition, for loads
   // under one are waited for where it ends.  A warp's scales are 2 V words of
   // four, one to a lane (past the row its last word: the values there are 0).
@@ -471,10 +492,11 @@ __global__ void __launch_bounds__(kBackThreads, 1) norm_back_kernel(const NormBa
   // Fills the place of row r, which every thread of the group has read.  From 8
   // bits, where three rows at least fit, this waits for the barrier of the next
   // row's sums, and a row needs no second one (16640 x 5120 95.1 -> 88.7 us, 4096 x
-  // 16384 79.6 -> 73.7); with the two bf16 rows that fit at wide rows that is too
-  // late (8192 x 8192 68.4 us, 82.2 so; 16640 x 5120, three rows, 85.6 and 84.1),
-  // and a choice at run time costs what it gains.
-  constexpr bool late = SAVE;
+  // 16384 79.6 -> 73.7), and for odd lengths (16640 x 4099 94.0 -> 91.8 us, 4096 x
+  // 16383 140 -> 121.5).  For bf16 rows it is too late where only two fit (8192 x
+  // 8192 68.4 us, 82.2 so; 16640 x 5120, three rows, 85.6 and 84.1), and a choice at
+  // run time costs what it gains.
+  constexpr bool late = SAVE || ODD;
   auto refill = [&](int64_t r) {
     r += sh.stages * step;
     if (r >= p.M || *aborted) return;
@@ -499,8 +521,12 @@ __global__ void __launch_bounds__(kBackThreads, 1) norm_back_kernel(const NormBa
     }
     fetch(r + step);
     mbar_wait(&bars[st], parity, aborted);
-    const uint8_t* sd = mine + st * stage_bytes + first * 16;
-    const uint8_t* sx = mine + st * stage_bytes + x_at + first * (SAVE ? 8 : 16);
+    uint8_t* sd = mine + st * stage_bytes + first * 16;
+    uint8_t* sx = mine + st * stage_bytes + x_at + first * (SAVE ? 8 : 16);
+    if (ODD && edges) {
+      span.clear_place(sd, first, edges);
+      span.clear_place(sx, first, edges);
+    }
     // x - mean of piece i.
     auto get_x = [&](int i, f32x2* xv) {
       if constexpr (SAVE) {
@@ -514,17 +540,13 @@ __global__ void __launch_bounds__(kBackThreads, 1) norm_back_kernel(const NormBa
           xv[j] = fma2(pair(lo, hi), m, ms);
         }
       } else {
-        uint4 v = *reinterpret_cast<const uint4*>(sx + i * 512);
-        span.clear(v, first + 32 * i);
-        get_pairs(v, xv);
+        get_pairs(*reinterpret_cast<const uint4*>(sx + i * 512), xv);
 #pragma unroll
         for (int j = 0; j < 4; ++j) xv[j] = add2(xv[j], ms);
       }
     };
     auto get_dy = [&](int i, f32x2* d) {
-      uint4 v = *reinterpret_cast<const uint4*>(sd + i * 512);
-      span.clear(v, first + 32 * i);
-      get_pairs(v, d);
+      get_pairs(*reinterpret_cast<const uint4*>(sd + i * 512), d);
     };
     f32x2 s1 = 0, s2 = 0;
 #pragma unroll
@@ -562,6 +584,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) norm_back_kernel(const NormBa
       for (int j = 0; j < 4; ++j) d[j] = fma2(xv[j], k2, fma2(mul2(d[j], wv[j]), rs, k1));
       span.store(dx, first + 32 * i, d, p.sp_dx);
     }
+    if (ODD && edges) fence_proxy_async_smem();   // what was cleared, before the next copies
     if (!late) {
       grp.meet();
       if (tid == 0) refill(r);

@@ -770,31 +770,40 @@ int run_norm_back(NormBackParams p, int num_sms, int* grid, cudaStream_t stream)
 
 // Values a thread holds of a row.  32 carry the most rows at a time (a group of 16
 // warps holds 16384); few values for an SM are spread over more threads (values:
-// an SM's rows times the width); 40 for the few widths that need them for their
-// lead.  Backward, 32 / 16 / 8 values: 1031 x 1021 11.0 / 9.0 / 8.1 us, 600 x 4096
-// 10.2 / 9.5 / 10.1, 2400 x 4096 17.0 / 17.7 / 21.4; forward: 1 x 4096 2.9 / 2.5 /
-// 2.4 us, 1200 x 1024 3.3 / 3.1 / 3.6, 2400 x 1024 3.9 / 4.3 / 5.6.
-int values_of(int width, int64_t M, int num_sms, int64_t few) {
+// an SM's rows times the width).  Backward, 32 / 16 / 8 values: 1031 x 1021 11.0 /
+// 9.0 / 8.1 us, 600 x 4096 10.2 / 9.5 / 10.1, 2400 x 4096 17.0 / 17.7 / 21.4;
+// forward: 1 x 4096 2.9 / 2.5 / 2.4 us, 1200 x 1024 3.3 / 3.1 / 3.6, 2400 x 1024
+// 3.9 / 4.3 / 5.6.  With a lead, 40 for the few widths that need them and where they
+// carry many more rows, as past 1024 and 8192: backward, 32 / 40 values, 16640 x
+// 1021 44.5 / 34.0 us, 8000 x 8190 108 / 95.8, 16640 x 2050 60.4 / 54.4 (1.6 times
+// the rows), but 4000 x 6001 38.2 / 42.5 (1.5 times); forward 30.0 / 19.6, 80.4 /
+// 63.1, 40.1 / 33.4, 25.0 / 23.3.
+int values_of(int width, int64_t M, int num_sms, int64_t few, bool odd) {
   if (width > kNormMaxWidth) return 40;
   const int64_t values = (M + num_sms - 1) / num_sms * width;
   if (width <= 256 || (width <= 4096 && values < 8192)) return 8;
   if (width <= 512 || (width <= 8192 && values < few)) return 16;
-  return 32;
+  const int rows32 = 16 / ((width + 1023) / 1024), rows40 = 16 / ((width + 1279) / 1280);
+  return odd && 5 * rows40 >= 8 * rows32 ? 40 : 32;
 }
 
 template <bool SAVE, bool ODD, typename W>
 int pick_norm(const NormParams& p, int num_sms, cudaStream_t stream) {
-  const int n = values_of(p.D + (ODD ? 7 : 0), p.M, num_sms, 16384);
+  const int n = values_of(p.D + (ODD ? 7 : 0), p.M, num_sms, 16384, ODD);
   if (n == 8) return run_norm<SAVE, ODD, W, 8>(p, num_sms, stream);
   if (n == 16) return run_norm<SAVE, ODD, W, 16>(p, num_sms, stream);
   if constexpr (ODD)
-    if (n == 40) return run_norm<SAVE, ODD, W, 40>(p, num_sms, stream);
+    if (n == 40)
+      // Two rows a turn where a row has a group of many warps: 8000 x 8190 63.1 ->
+      // 59.7 us, 4096 x 16383 70.8 -> 63.0, but 16640 x 1021 19.6 -> 20.2.
+      return p.D > 8000 ? run_norm<SAVE, ODD, W, 40, 2>(p, num_sms, stream)
+                        : run_norm<SAVE, ODD, W, 40>(p, num_sms, stream);
   return run_norm<SAVE, ODD, W, 32, 2>(p, num_sms, stream);
 }
 
 template <bool SAVE, bool ODD, typename W>
 int pick_norm_back(const NormBackParams& p, int num_sms, int* grid, cudaStream_t stream) {
-  const int n = values_of(p.D + (ODD ? 7 : 0), p.M, num_sms, 40000);
+  const int n = values_of(p.D + (ODD ? 7 : 0), p.M, num_sms, 40000, ODD);
   if (n == 8) return run_norm_back<SAVE, ODD, W, 8>(p, num_sms, grid, stream);
   if (n == 16) return run_norm_back<SAVE, ODD, W, 16>(p, num_sms, grid, stream);
   if constexpr (ODD)

@@ -323,3 +323,37 @@ def test_refusals():
         mx.layer_norm(rnd((2, 48), 1), rnd((48,), 1, F32), save=True)
     with pytest.raises(mx.MXError):
         mx.layer_norm(rnd((2, 16392), 1), rnd((16392,), 1, F32))
+
+
+# Enough rows that each SM works through many, with every share of a row to a
+# thread; lengths just past a multiple of 1024, and off the 16-byte boundary.
+MANY = [(6100, 1021), (3100, 2050), (330, 8190), (2500, 4104), (6100, 1504), (1300, 5127)]
+
+
+@pytest.mark.parametrize("M,D", MANY)
+def test_many_rows(M, D):
+    x, dy = rnd((M, D), 3, scale=2.0, shift=0.5), rnd((M, D), 4, scale=1e-2)
+    w, b = rnd((D,), 1, F32, 0.2, 1.0), rnd((D,), 2, F32, 0.3)
+    check_forward(x, w, b, forward(x, w, b, False))
+    mean, rstd = stats(x)
+    check_backward(dy, x, w, mean, rstd, backward(dy, x, None, w, mean, rstd))
+
+
+@pytest.mark.parametrize("M,D", [(2600, 5120), (330, 16384), (1300, 8224)])
+def test_many_saved_rows(M, D):
+    x, dy = rnd((M, D), 3, scale=2.0, shift=0.5), rnd((M, D), 4, scale=1e-2)
+    w = rnd((D,), 1, BF, 0.2, 1.0)
+    y, mean, rstd, q, s = mx.layer_norm(x, w, None, EPS, save=True)
+    got = backward(dy, None, (q, s), w, mean, rstd)
+    check_backward(dy, plain64.mx_values(q, s), w, mean, rstd, got)
+
+
+@pytest.mark.parametrize("M,D", [(6100, 1021), (330, 8190)])
+def test_neighbours_among_many_rows(M, D):
+    x, dy = rnd((M, D), 3, shift=1.0), rnd((M, D), 4)
+    w, b = rnd((D,), 1, F32), rnd((D,), 2, F32)
+    mean, rstd = stats(x)
+    y, dx = forward(x, w, b, False)[0], backward(dy, x, None, w, mean, rstd)[0]
+    x[1::2], dy[1::2], mean[1::2], rstd[1::2] = (float("nan"),) * 4
+    assert torch.equal(forward(x, w, b, False)[0][::2], y[::2])
+    assert torch.equal(backward(dy, x, None, w, mean, rstd)[0][::2], dx[::2])

@@ -115,3 +115,8 @@ def test_layer_norm_gives_up(D, at):
             assert torch.equal(call(), want)
             assert mx.mx_watchdog(clear=True) == 0
         assert mx.mx_bounds_check(clear=True) == 0
+
+
+@pytest.mark.parametrize("M,D", [(6100, 1021), (330, 8190)])
+def test_layer_norm_of_many_rows(M, D):
+    test_layer_norm(M, D)

@@ -118,3 +118,29 @@ def test_errors_carry_the_code():
     with pytest.raises(mx.MXError) as e:
         mx.layer_norm(rnd((8, 64), 1)[:, :].view(64, 8)[1:].reshape(63, 8), rnd((8,), 2, torch.float32), eps=float("nan"))
     assert e.value.code == mx.MX_ERR_SHAPE
+
+
+def test_captured_in_a_graph():
+    """Every call, in one graph: the same results from new contents of its inputs."""
+    x, dy = rnd((160, 96), 1), rnd((160, 96), 2)
+    w, gu, dh = rnd((96,), 3, torch.float32), rnd((160, 256), 5), rnd((160, 128), 6)
+
+    def step():
+        y, mean, rstd, q, s = mx.layer_norm(x, w, save=True)
+        dx, dw, db = mx.layer_norm_backward(dy, (q, s), w, mean, rstd)
+        h, gq, gs = mx.swiglu(gu, save=True)
+        out = [y, mean, rstd, q, s, dx, dw, db, h, gq, gs, mx.swiglu_backward(dh, (gq, gs))]
+        a, b = mx.cast_dim0(x), mx.cast_dim0(dy)
+        return out + [mx.matmul(*a, *b), mx.matmul(*a, *b, torch.float32)]
+
+    step()
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        got = step()
+    for t, seed in ((x, 11), (dy, 12), (gu, 13), (dh, 14)):
+        t.copy_(rnd(tuple(t.shape), seed))
+    g.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(got, step()):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))

@@ -451,7 +451,7 @@ int mx_matmul(const void* qa, const void* sa_blk, const void* qb, const void* sb
   int sms = 0;
   if (int rc = current_sm_count(&sms)) return rc;
   const bool f32 = out_type == MX_F32;
-  const bool pairs = mx::matmul_pairs(M, N, f32, sms);
+  const bool pairs = mx::matmul_pairs(M, N, sms);
   mx::MatmulMaps maps;
   const int64_t tiles_k = cdiv(K, 128);
   auto operand = [&](CUtensorMap* m, const void* q, int64_t rows, bool mn) {

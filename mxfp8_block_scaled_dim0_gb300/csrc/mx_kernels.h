@@ -121,7 +121,7 @@ struct MatmulMaps {
 };
 bool matmul_mapped(int64_t N, bool out_f32);
 int matmul_box_rows(int64_t rows, bool mn);
-bool matmul_pairs(int64_t M, int64_t N, bool out_f32, int num_sms);
+bool matmul_pairs(int64_t M, int64_t N, int num_sms);
 int launch_matmul(const MatmulMaps& maps, int64_t M, int64_t N, int64_t K, bool a_mn, bool b_mn,
                   void* out, bool out_f32, int num_sms, cudaStream_t stream);
 int read_matmul_watchdog(int* out, bool clear);

@@ -34,6 +34,11 @@
 // 8192 x 8192 x 4096); the rest goes to a launch's first loads, to the last tiles'
 // stores, and to pairs that have no tile left.
 //
+// Rows of results that no tensor map can describe (no multiple of 16 bytes) leave
+// the same shared memory a row at a time, by the warp: 16640 x 8191 x 5120 415 us
+// (839 in single tiles, eight values a thread), 2000 x 3001 x 1024 14.0 (30.0; 11.5 at
+// 3008).
+//
 // tile_matmul_kernel: one 128 x 128 tile of C per cluster of S CTAs, the
 // contraction cut into S equal runs of 128-step blocks; each CTA leaves its
 // partial tile in its shared memory, and each then sums 128 / S of the tile's
@@ -84,7 +89,7 @@ struct MatmulParams {
   int a_mn, b_mn;      // operand stored with its rows contiguous
   int run;             // blocks summed in tensor memory at a time (pair kernel)
   int band;            // M-tiles of a band (pair kernel)
-  int mapped;          // maps.out describes the output
+  int mapped;          // maps.out describes the result's rows
   int load_bytes;      // of a stage (tile kernel)
   Span sp_out;
   int64_t stall_at;
@@ -207,9 +212,9 @@ __global__ void __launch_bounds__(kTileThreads, 2)
   const int64_t n0 = static_cast<int64_t>(nt) * kTile;
   const int quarter = warp & 3;
   const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-  if (p.split == 1 && p.mapped) {
-    // 32 rows at a time and warp through shared memory and a tensor map, 128
-    // bytes of a row a box.
+  if (p.split == 1) {
+    // 32 rows at a time and warp through shared memory, and a tensor map where one
+    // can describe the result, 128 bytes of a row a box.
     const int64_t m = static_cast<int64_t>(mt) * kTile + quarter * 32;
     if (warp >= 2 && ok && m < p.M) {
       uint8_t* so = ring + quarter * 4 * kStageOut;
@@ -239,7 +244,13 @@ __global__ void __launch_bounds__(kTileThreads, 2)
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) {
+      if (!p.mapped) {
+        for (int c = 0; c < 128 && n0 + c < p.N; c += per) {
+          const uint8_t* box = so + c / per * kStageOut;
+          if (p.out_f32) store_box<4>(box, p.out, m, n0 + c, p.M, p.N, lane, p.sp_out);
+          else store_box<2>(box, p.out, m, n0 + c, p.M, p.N, lane, p.sp_out);
+        }
+      } else if (lane == 0) {
         for (int c = 0; c < 128 && n0 + c < p.N; c += per)
           tma_store_2d(&maps.out, static_cast<int>(n0) + c, static_cast<int>(m), so + c / per * kStageOut);
         bulk_commit();
@@ -270,10 +281,7 @@ __global__ void __launch_bounds__(kTileThreads, 2)
     }
     tcgen05_fence_before();
   }
-  if (p.split > 1)
-    cluster_sync();
-  else
-    __syncthreads();
+  cluster_sync();
   // Rows of the tile that this CTA writes, summed over the cluster: the loads of
   // all CTAs' values are under way before the first is added.
   const int rows = kTile / p.split;
@@ -304,8 +312,7 @@ __global__ void __launch_bounds__(kTileThreads, 2)
                  vec ? 8 : static_cast<int>(p.N - n < 8 ? p.N - n : 8), vec, p.sp_out);
     }
   }
-  if (p.split > 1) cluster_sync();            // peers have read this CTA's partial tile
-  else __syncthreads();
+  cluster_sync();                             // peers have read this CTA's partial tile
   if (warp == 1) tmem_dealloc<1>(tmem, 256);
   if (threadIdx.x == 0 && !ok) atomicOr(&g_matmul_watchdog, 1);
 }
@@ -526,8 +533,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
               make_uint4(v[x][4 * j], v[x][4 * j + 1], v[x][4 * j + 2], v[x][4 * j + 3]);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          const int c = n + x * (128 / kBoxes);
+        const int c = n + x * (128 / kBoxes);
+        if (!p.mapped) {
+          if (c < p.N) store_box<F32 ? 4 : 2>(so, p.out, m, c, p.M, p.N, lane, p.sp_out);
+        } else if (lane == 0) {
           if (c < p.N) tma_store_2d(&maps.out, c, m, so);
           bulk_commit();
         }
@@ -566,19 +575,15 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   if (threadIdx.x == 0 && failed) atomicOr(&g_matmul_watchdog, 1);
 }
 
-// The pair kernel takes outputs that a tensor map can describe, of enough
-// 256 x 256 tiles to keep the GPU's pairs busy.
-bool use_pairs(int64_t M, int64_t N, bool out_f32, int num_sms) {
-  if (!matmul_mapped(N, out_f32)) return false;
+// The pair kernel takes what has enough 256 x 256 tiles to keep the GPU's pairs busy.
+bool use_pairs(int64_t M, int64_t N, int num_sms) {
   const int64_t tiles = ((M + 255) / 256) * ((N + 255) / 256);
   return tiles * 4 >= num_sms;
 }
 
 }  // namespace
 
-bool matmul_pairs(int64_t M, int64_t N, bool out_f32, int num_sms) {
-  return use_pairs(M, N, out_f32, num_sms);
-}
+bool matmul_pairs(int64_t M, int64_t N, int num_sms) { return use_pairs(M, N, num_sms); }
 
 template <bool F32>
 static int launch_pairs(const MatmulMaps& maps, MatmulParams p, int num_sms, cudaStream_t stream) {
@@ -625,11 +630,12 @@ int launch_matmul(const MatmulMaps& maps, int64_t M, int64_t N, int64_t K, bool 
   p.k_blocks = static_cast<int>((K + kBK - 1) / kBK);
   p.last_steps = static_cast<int>((K - static_cast<int64_t>(p.k_blocks - 1) * kBK) / 32);
   p.out_f32 = out_f32;
+  p.mapped = matmul_mapped(N, out_f32);
   p.sp_out = make_span(out, static_cast<uint64_t>(M) * static_cast<uint64_t>(N) * (out_f32 ? 4 : 2));
   const Stall stall = take_stall();
   p.stall_at = stall.at;
   p.stall_ns = stall.ns;
-  if (use_pairs(M, N, out_f32, num_sms))
+  if (use_pairs(M, N, num_sms))
     return out_f32 ? launch_pairs<true>(maps, p, num_sms, stream)
                    : launch_pairs<false>(maps, p, num_sms, stream);
   p.m_tiles = static_cast<int>((M + kTile - 1) / kTile);
@@ -652,7 +658,6 @@ int launch_matmul(const MatmulMaps& maps, int64_t M, int64_t N, int64_t K, bool 
       p.split = s;
     }
   }
-  p.mapped = matmul_mapped(N, out_f32);
   p.stages = tiles * p.split <= num_sms ? kTileStages : kFewStages;
   p.load_bytes = matmul_box_rows(M, a_mn) * kBK + matmul_box_rows(N, b_mn) * kBK + 2 * kSfBytes;
   if (tiles * p.split > 0x7fffffff) return static_cast<int>(cudaErrorInvalidConfiguration);

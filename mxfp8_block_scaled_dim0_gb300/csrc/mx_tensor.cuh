@@ -298,4 +298,35 @@ __device__ __forceinline__ void store_out8(void* out, int f32, int64_t at, const
   }
 }
 
+// A warp's box of 32 rows x 128 bytes of results (ITEM bytes each), in the swizzled
+// order that a tensor map expects, to rows of N at (m, n) of `out`, whose rows no map
+// can describe: a row at a time, in words where rows begin on a word.
+template <int ITEM>
+__device__ __forceinline__ void store_box(const uint8_t* box, void* out, int64_t m, int64_t n,
+                                          int64_t M, int64_t N, int lane, const Span& sp) {
+  const int rows = static_cast<int>(M - m < 32 ? M - m : 32);
+  const int cols = static_cast<int>(N - n < 128 / ITEM ? N - n : 128 / ITEM);
+  uint8_t* at = static_cast<uint8_t*>(out) + (m * N + n) * ITEM;
+  const int64_t pitch = N * ITEM;
+  if (ITEM == 4 || (N & 1) == 0) {
+    constexpr int kPer = 4 / ITEM;
+    const bool in = lane * kPer < cols;
+#pragma unroll 8
+    for (int r = 0; r < rows; ++r, at += pitch) {
+      const uint32_t v = *reinterpret_cast<const uint32_t*>(box + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) +
+                                                            (lane & 3) * 4);
+      if (in && in_span(sp, at + 4 * lane, 4)) *reinterpret_cast<uint32_t*>(at + 4 * lane) = v;
+    }
+  } else {
+#pragma unroll 4
+    for (int r = 0; r < rows; ++r, at += pitch)
+#pragma unroll
+      for (int e = lane; e < 64; e += 32) {
+        const uint16_t v = *reinterpret_cast<const uint16_t*>(box + r * 128 + (((e >> 3) ^ (r & 7)) << 4) +
+                                                              (e & 7) * 2);
+        if (e < cols && in_span(sp, at + 2 * e, 2)) *reinterpret_cast<uint16_t*>(at + 2 * e) = v;
+      }
+  }
+}
+
 }  // namespace mx

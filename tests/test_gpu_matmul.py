@@ -238,3 +238,19 @@ def test_refusals():
     with pytest.raises(mx.MXError) as e:
         mx.mx_matmul(q, a[1], torch.zeros((96, 48), dtype=torch.uint8, device="cuda"), b[1], out)
     assert e.value.code == mx.MX_ERR_SHAPE
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=["bf16", "f32"])
+@pytest.mark.parametrize("N", [1001, 1002, 1004, 1023, 1026])
+@pytest.mark.parametrize("M,K", [(2501, 160), (2470, 4192)])
+def test_rows_off_the_boundary(M, N, K, dtype):
+    """Enough tiles for the pairs, rows of results that begin anywhere."""
+    a, b = operand(M, K, M + N), operand(N, K, N + 1)
+    check(a, b, product(a, b, dtype))
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=["bf16", "f32"])
+@pytest.mark.parametrize("M,N,K", [(500, 701, 800), (161, 1022, 1024), (16640, 333, 64), (33, 2817, 96)])
+def test_few_tiles_off_the_boundary(M, N, K, dtype):
+    a, b = operand(M, K, M + N), operand(N, K, N + 1)
+    check(a, b, product(a, b, dtype))

@@ -120,3 +120,20 @@ def test_layer_norm_gives_up(D, at):
 @pytest.mark.parametrize("M,D", [(6100, 1021), (330, 8190)])
 def test_layer_norm_of_many_rows(M, D):
     test_layer_norm(M, D)
+
+
+@pytest.mark.parametrize("M,N,K", [(2501, 1001, 160), (2501, 1002, 96), (300, 701, 160)])
+def test_matmul_off_the_boundary(M, N, K):
+    test_matmul(M, N, K)
+
+
+def test_matmul_off_the_boundary_gives_up():
+    a, b = mx.cast_dim0(rnd((2501, 1024), 1)), mx.cast_dim0(rnd((1001, 1024), 2))
+    want = mx.matmul(*a, *b)
+    with checked():
+        mx.mx_selftest_arm_stall(5)
+        mx.matmul(*a, *b)
+        assert mx.mx_watchdog(clear=True) == 1
+        assert torch.equal(mx.matmul(*a, *b), want)
+        assert mx.mx_watchdog(clear=True) == 0
+        assert mx.mx_bounds_check(clear=True) == 0

@@ -17,7 +17,7 @@
 //
 // Every tensor crosses the memory bus once: 5 bytes a value forward with the save
 // and backward from it, 6 backward from bf16.  16640 x 5120: forward with the save
-// 74 us (5.8 TB/s), backward from 8 bits 89 us (4.8 TB/s, the gradient kernel's
+// 72 us (6.0 TB/s), backward from 8 bits 88 us (4.8 TB/s, the gradient kernel's
 // 5 us in it), from bf16 85 us (6.0 TB/s); 1 x 4096 forward 2.4 us.  Forward is
 // bound by the way through shared memory (waits for its loads, 52% of the issue
 // slots taken), backward by issue and by the few warps that dw and db leave room for.
@@ -195,11 +195,14 @@ __global__ void __launch_bounds__(R == 1 ? kRingThreads : kBackThreads, 1)
   clear_padding(ring, places, stage_bytes, 16 * span.total, 2 * sh.pitch);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   float* params = reinterpret_cast<float*>(ring + places * stage_bytes);   // w, then b
-  if (p.staged) {
+  auto stage = [&] {
+    if (!p.staged) return;
     stage_params<ODD>(params, static_cast<const W*>(p.w), span.lead, p.D, sh.pitch);
     stage_params<ODD>(params + sh.pitch, static_cast<const W*>(p.b), span.lead, p.b ? p.D : 0,
                       sh.pitch);
-  }
+  };
+  const bool early = ODD || sh.warps < 4;      // see below
+  if (early) stage();
   __syncthreads();
 
   uint8_t* mine = ring + g * sh.stages * stage_bytes;
@@ -225,6 +228,33 @@ __global__ void __launch_bounds__(R == 1 ? kRingThreads : kBackThreads, 1)
       }
       issue(issued, r0 + issued * step);
     }
+
+  // While the first rows come: the parameters (16640 x 5120 60.2 -> 55.3 us, with the
+  // save 74.0 -> 71.9).  Their loads first are quicker for short rows (16640 x 1024
+  // with the save 15.7 and 16.9 us), with a lead (16640 x 4099 64.0 and 66.7), and
+  // backward (16640 x 5120 88.3 and 94.7).
+  if (!early) stage();
+  if constexpr (SAVE) {
+    // Zeros for the scales of rows past the matrix.  16 bytes of a scale tile hold
+    // rows c, c + 32, c + 64 and c + 96.  (At the kernel's end and by one CTA, a
+    // word at a time: 8 x 13344 11.7 us, 4.6 so.)
+    const int m = static_cast<int>(p.M & 127);
+    uint8_t* s = p.s + (p.M >> 7) * 512 * p.s_words;
+    if (m)
+      for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < 32 * p.s_words;
+           i += gridDim.x * blockDim.x) {
+        const int c = i & 31;
+        if (c >= m) {
+          if (in_span(p.sp_s, s + 16 * i, 16)) *reinterpret_cast<uint4*>(s + 16 * i) = make_uint4(0, 0, 0, 0);
+          continue;
+        }
+#pragma unroll
+        for (int g = 1; g < 4; ++g)
+          if (c + 32 * g >= m && in_span(p.sp_s, s + 16 * i + 4 * g, 4))
+            *reinterpret_cast<uint32_t*>(s + 16 * i + 4 * g) = 0;
+      }
+  }
+  if (!early) __syncthreads();
 
   const float inv = 1.0f / static_cast<float>(p.D);
   // Piece i of this thread is piece first + 32 i of the row (a warp's pieces lie
@@ -367,14 +397,6 @@ __global__ void __launch_bounds__(R == 1 ? kRingThreads : kBackThreads, 1)
       }
     }
   }
-  if (SAVE && blockIdx.x == 0) {
-    // Rows of scales past the matrix: zero.
-    const int64_t n = ((p.M + 127) / 128 * 128 - p.M) * p.s_words;
-    for (int64_t i = threadIdx.x; i < n; i += blockDim.x) {
-      uint8_t* s = p.s + blocked_offset(p.M + i / p.s_words, (i % p.s_words) * 4, 4 * p.s_words);
-      if (in_span(p.sp_s, s, 4)) *reinterpret_cast<uint32_t*>(s) = 0;
-    }
-  }
   if (tid == 0 && abort_flag) {
     // Gave up: the copies still in flight land (bounded) before the CTA ends.
     for (int j = issued > sh.stages ? issued - sh.stages : 0; j < issued; ++j)
@@ -475,7 +497,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) norm_back_kernel(const NormBa
   // under one are waited for where it ends.  A warp's scales are 2 V words of
   // four, one to a lane (past the row its last word: the values there are 0).
   uint32_t words_next;
-  const int word = min(grp.warp * 2 * V + (lane & (2 * V - 1)), p.s_words - 1) * 512;
+  const int word = min(grp.warp * 2 * V + min(lane, 2 * V - 1), p.s_words - 1) * 512;
   const int byte = (lane >> 2 & 3) * 8;
   float mean_next, rstd_next;
   auto fetch = [&](int64_t r) {
@@ -777,14 +799,17 @@ int run_norm_back(NormBackParams p, int num_sms, int* grid, cudaStream_t stream)
 // carry many more rows, as past 1024 and 8192: backward, 32 / 40 values, 16640 x
 // 1021 44.5 / 34.0 us, 8000 x 8190 108 / 95.8, 16640 x 2050 60.4 / 54.4 (1.6 times
 // the rows), but 4000 x 6001 38.2 / 42.5 (1.5 times); forward 30.0 / 19.6, 80.4 /
-// 63.1, 40.1 / 33.4, 25.0 / 23.3.
+// 63.1, 40.1 / 33.4, 25.0 / 23.3.  24 where they take no more warps: with the save,
+// forward, 16640 x 768 14.7 -> 12.5 us, 16640 x 1536 29.2 -> 24.3, backward 22.8 ->
+// 19.2, 40.4 -> 33.7; but 16640 x 2560, four warps and not three, 41.0 -> 45.4.
 int values_of(int width, int64_t M, int num_sms, int64_t few, bool odd) {
   if (width > kNormMaxWidth) return 40;
   const int64_t values = (M + num_sms - 1) / num_sms * width;
   if (width <= 256 || (width <= 4096 && values < 8192)) return 8;
   if (width <= 512 || (width <= 8192 && values < few)) return 16;
-  const int rows32 = 16 / ((width + 1023) / 1024), rows40 = 16 / ((width + 1279) / 1280);
-  return odd && 5 * rows40 >= 8 * rows32 ? 40 : 32;
+  auto warps = [width](int n) { return (width + 32 * n - 1) / (32 * n); };
+  if (odd && 5 * (16 / warps(40)) >= 8 * (16 / warps(32))) return 40;
+  return warps(24) == warps(32) ? 24 : 32;
 }
 
 template <bool SAVE, bool ODD, typename W>
@@ -798,6 +823,7 @@ int pick_norm(const NormParams& p, int num_sms, cudaStream_t stream) {
       // 59.7 us, 4096 x 16383 70.8 -> 63.0, but 16640 x 1021 19.6 -> 20.2.
       return p.D > 8000 ? run_norm<SAVE, ODD, W, 40, 2>(p, num_sms, stream)
                         : run_norm<SAVE, ODD, W, 40>(p, num_sms, stream);
+  if (n == 24) return run_norm<SAVE, ODD, W, 24, 2>(p, num_sms, stream);
   return run_norm<SAVE, ODD, W, 32, 2>(p, num_sms, stream);
 }
 
@@ -808,6 +834,7 @@ int pick_norm_back(const NormBackParams& p, int num_sms, int* grid, cudaStream_t
   if (n == 16) return run_norm_back<SAVE, ODD, W, 16>(p, num_sms, grid, stream);
   if constexpr (ODD)
     if (n == 40) return run_norm_back<SAVE, ODD, W, 40>(p, num_sms, grid, stream);
+  if (n == 24) return run_norm_back<SAVE, ODD, W, 24>(p, num_sms, grid, stream);
   return run_norm_back<SAVE, ODD, W, 32>(p, num_sms, grid, stream);
 }
 

@@ -169,9 +169,14 @@ __device__ __forceinline__ void load_param_pairs(const uint16_t* p, f32x2* v) {
 // free of bank conflicts.
 template <bool ODD, typename W>
 __device__ __forceinline__ void stage_params(float* dst, const W* src, int lead, int D, int pitch) {
-  for (int c = threadIdx.x; c < pitch / 8; c += blockDim.x) {
-    f32x2 v[4] = {0, 0, 0, 0};
-    if constexpr (ODD) {
+  const int threads = static_cast<int>(blockDim.x);
+  auto put = [&](int c, const f32x2* v) {
+    reinterpret_cast<ulonglong2*>(dst)[c] = make_ulonglong2(v[0], v[1]);
+    reinterpret_cast<ulonglong2*>(dst)[pitch / 8 + c] = make_ulonglong2(v[2], v[3]);
+  };
+  if constexpr (ODD) {
+    for (int c = threadIdx.x; c < pitch / 8; c += threads) {
+      f32x2 v[4];
       float f[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -180,11 +185,22 @@ __device__ __forceinline__ void stage_params(float* dst, const W* src, int lead,
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[j] = pair(f[2 * j], f[2 * j + 1]);
-    } else if (8 * c < D) {
-      load_param_pairs(src + 8 * c, v);
+      put(c, v);
     }
-    reinterpret_cast<ulonglong2*>(dst)[c] = make_ulonglong2(v[0], v[1]);
-    reinterpret_cast<ulonglong2*>(dst)[pitch / 8 + c] = make_ulonglong2(v[2], v[3]);
+  } else {
+    const int n = D >> 3;
+    const f32x2 zero[4] = {0, 0, 0, 0};
+    for (int c = n + threadIdx.x; c < pitch / 8; c += threads) put(c, zero);
+    // Two pieces' loads at a time, without a condition (past the end: the last).
+    constexpr int kAtOnce = 2;
+    for (int c = threadIdx.x; c < n; c += kAtOnce * threads) {
+      f32x2 v[kAtOnce][4];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) load_param_pairs(src + 8 * min(c + k * threads, n - 1), v[k]);
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k)
+        if (c + k * threads < n) put(c + k * threads, v[k]);
+    }
   }
 }
 

@@ -327,7 +327,8 @@ def test_refusals():
 
 # Enough rows that each SM works through many, with every share of a row to a
 # thread; lengths just past a multiple of 1024, and off the 16-byte boundary.
-MANY = [(6100, 1021), (3100, 2050), (330, 8190), (2500, 4104), (6100, 1504), (1300, 5127)]
+MANY = [(6100, 1021), (3100, 2050), (330, 8190), (2500, 4104), (6100, 1504), (1300, 5127),
+        (10000, 640), (6100, 1361), (3100, 2296)]
 
 
 @pytest.mark.parametrize("M,D", MANY)
@@ -339,7 +340,8 @@ def test_many_rows(M, D):
     check_backward(dy, x, w, mean, rstd, backward(dy, x, None, w, mean, rstd))
 
 
-@pytest.mark.parametrize("M,D", [(2600, 5120), (330, 16384), (1300, 8224)])
+@pytest.mark.parametrize("M,D", [(2600, 5120), (330, 16384), (1300, 8224), (10001, 640), (6100, 1504),
+                                 (3100, 2304)])
 def test_many_saved_rows(M, D):
     x, dy = rnd((M, D), 3, scale=2.0, shift=0.5), rnd((M, D), 4, scale=1e-2)
     w = rnd((D,), 1, BF, 0.2, 1.0)
@@ -357,3 +359,15 @@ def test_neighbours_among_many_rows(M, D):
     x[1::2], dy[1::2], mean[1::2], rstd[1::2] = (float("nan"),) * 4
     assert torch.equal(forward(x, w, b, False)[0][::2], y[::2])
     assert torch.equal(backward(dy, x, None, w, mean, rstd)[0][::2], dx[::2])
+
+
+@pytest.mark.parametrize("M", [1, 31, 32, 33, 97, 127, 129, 250])
+def test_scales_of_rows_past_the_matrix(M):
+    x, w = rnd((M, 416), M), rnd((416,), 1, F32)
+    _, _, _, q, s = mx.layer_norm(x, w, save=True)
+    q0, s0 = mx.cast_dim0(x.contiguous()) if M % 32 == 0 else (None, None)
+    rows = (M + 127) // 128 * 128
+    at = plain64.blocked_at(rows, 16, "cuda")
+    assert bool((s[at[M:]] == 0).all()) and bool((s[at[:, 13:]] == 0).all())
+    if s0 is not None:
+        assert torch.equal(s, s0) and torch.equal(q, q0)

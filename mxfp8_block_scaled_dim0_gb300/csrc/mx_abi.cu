@@ -454,10 +454,10 @@ int mx_matmul(const void* qa, const void* sa_blk, const void* qb, const void* sb
   const bool pairs = mx::matmul_pairs(M, N, sms);
   mx::MatmulMaps maps;
   const int64_t tiles_k = cdiv(K, 128);
-  auto operand = [&](CUtensorMap* m, const void* q, int64_t rows, bool mn) {
+  auto operand = [&](CUtensorMap* m, const void* q, int64_t rows, bool mn, int tile) {
     return encode_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, q, mn ? rows : K, mn ? K : rows,
                      mn ? rows : K, 128,
-                     static_cast<uint32_t>(pairs ? 128 : mx::matmul_box_rows(rows, mn)),
+                     static_cast<uint32_t>(pairs ? 128 : mx::matmul_box_rows(rows, mn, tile)),
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
   };
   auto scales = [&](CUtensorMap* m, const void* s, int64_t rows, uint32_t box) {
@@ -465,8 +465,8 @@ int mx_matmul(const void* qa, const void* sa_blk, const void* qb, const void* sb
                      tiles_k * 512, 128, box, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                      CU_TENSOR_MAP_SWIZZLE_NONE);
   };
-  if (int rc = operand(&maps.a, qa, M, a_mn)) return rc;
-  if (int rc = operand(&maps.b, qb, N, b_mn)) return rc;
+  if (int rc = operand(&maps.a, qa, M, a_mn, 128)) return rc;
+  if (int rc = operand(&maps.b, qb, N, b_mn, mx::matmul_tile_cols(M, N, K, b_mn, sms))) return rc;
   if (int rc = scales(&maps.sa, sa_blk, M, 1)) return rc;
   if (int rc = scales(&maps.sb, sb_blk, N, pairs ? 2 : 1)) return rc;
   if (!mx::matmul_mapped(N, f32)) {

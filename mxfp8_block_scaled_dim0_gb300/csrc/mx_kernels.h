@@ -111,7 +111,7 @@ int launch_group_offsets(const int32_t* offs, int G, int64_t M, int64_t* row_off
 int launch_scales_to_blocked(const uint8_t* s, int64_t R, int64_t C, uint8_t* out,
                              cudaStream_t stream);
 // MX product (mx_matmul.cu).  qa and qb: boxes of 128 bytes x 128 rows (without
-// matmul_pairs(): matmul_box_rows()), 128B swizzle (rows along the contraction
+// matmul_pairs(): matmul_box_rows() of tiles of 128 and matmul_tile_cols()), 128B swizzle (rows along the contraction
 // where a_mn / b_mn); sa and sb: their
 // blocked scales as rows of 128x4 tiles (32-bit words), boxes of one 512-byte
 // tile, with matmul_pairs() sb boxes of two rows' tiles; with matmul_mapped(), out:
@@ -120,7 +120,8 @@ struct MatmulMaps {
   CUtensorMap a, b, sa, sb, out;
 };
 bool matmul_mapped(int64_t N, bool out_f32);
-int matmul_box_rows(int64_t rows, bool mn);
+int matmul_box_rows(int64_t rows, bool mn, int tile);
+int matmul_tile_cols(int64_t M, int64_t N, int64_t K, bool b_mn, int num_sms);
 bool matmul_pairs(int64_t M, int64_t N, int num_sms);
 int launch_matmul(const MatmulMaps& maps, int64_t M, int64_t N, int64_t K, bool a_mn, bool b_mn,
                   void* out, bool out_f32, int num_sms, cudaStream_t stream);

@@ -39,11 +39,11 @@
 // (839 in single tiles, eight values a thread), 2000 x 3001 x 1024 14.0 (30.0; 11.5 at
 // 3008).
 //
-// tile_matmul_kernel: one 128 x 128 tile of C per cluster of S CTAs, the
+// tile_matmul_kernel: one 128 x 128 (or 64) tile of C per cluster of S CTAs, the
 // contraction cut into S equal runs of 128-step blocks; each CTA leaves its
 // partial tile in its shared memory, and each then sums 128 / S of the tile's
 // rows over the S CTAs in rank order (fixed order: the same bits every run).
-// 160 x 1024 x 1024 takes 5.4 us, 1 x 8192 x 5120 9.2: latency (loads, the chain of
+// 160 x 1024 x 1024 takes 4.9 us, 1 x 8192 x 5120 9.7: latency (loads, the chain of
 // a tile's MMAs, the stores), not bandwidth.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -62,8 +62,50 @@ __device__ int g_matmul_watchdog = 0;
 // Rows of an operand's load box in the tile kernel: no more than there are (a box
 // past the operand's end is filled with zeros at the price of a load).  What a
 // narrower box leaves in shared memory only reaches results that are not stored.
-int matmul_box_rows(int64_t rows, bool mn) {
-  return mn || rows >= 128 ? 128 : static_cast<int>((rows + 7) & ~int64_t{7});
+int matmul_box_rows(int64_t rows, bool mn, int tile) {
+  return mn || rows >= tile ? tile : static_cast<int>((rows + 7) & ~int64_t{7});
+}
+
+namespace {
+
+// The tile kernel's tiles: columns, and CTAs that share a tile's contraction.  Reckoned
+// for operands stored by row whatever the order, so that the order does not change
+// the sums.
+struct TileShape {
+  int cols, split;
+};
+
+// The quickest as reckoned in ns from what was measured: 220 for 128 contraction
+// steps, 500 more for the stores of 128 columns, and for joining (partial sums through
+// distributed shared memory, two cluster barriers) 400 and 19 for each row of 128
+// results.  160 x 1024 x 1024: 5.7 us in 128 columns, 5.1 in 64, 7.1 in two CTAs;
+// 64 x 8192 x 5120: 11.9 in 128 columns and two CTAs, 13.3 in 64; 32 x 32 x 16640: 34
+// whole, 8.4 in eight.  Clusters of eight only up to 96 CTAs, of four up to 128: more of
+// them do not all find room at once (512 x 512 x 16640, 128 CTAs: 15.8 us in four, 24.5
+// in eight; 38 x 2319 x 2112, 148 CTAs in clusters of four: 11.1 us, 76 7.5).
+TileShape tile_shape(int64_t M, int64_t N, int64_t k_blocks, int num_sms) {
+  TileShape best = {128, 1};
+  int64_t least = 500 + k_blocks * 220;
+  for (int cols = 128; cols >= 64; cols /= 2) {
+    const int64_t tiles = (M + 127) / 128 * ((N + cols - 1) / cols);
+    for (int s = 1; s <= 8 && s <= k_blocks; s *= 2) {
+      if (tiles * s > (s == 8 ? 96 : s == 4 ? 128 : num_sms)) break;
+      const int64_t cost = (cols == 128 ? 500 : 0) + (k_blocks + s - 1) / s * 220 +
+                           (s > 1 ? 400 + 19 * (M < 128 ? M : 128) * cols / 128 : 0);
+      if (cost < least) {
+        least = cost;
+        best = {cols, s};
+      }
+    }
+  }
+  return best;
+}
+
+}  // namespace
+
+// Columns of the tile kernel's tiles (an operand stored by column comes in whole 128).
+int matmul_tile_cols(int64_t M, int64_t N, int64_t K, bool b_mn, int num_sms) {
+  return b_mn ? 128 : tile_shape(M, N, (K + 127) / 128, num_sms).cols;
 }
 
 // Whether a tensor map can describe rows of N results.
@@ -84,13 +126,13 @@ struct MatmulParams {
   int last_steps;      // 32-step MMAs of the last block, 1..4
   int m_tiles, n_tiles;
   int split;           // CTAs of a cluster along the contraction (tile kernel)
-  int stages;          // of the load ring (tile kernel)
   int out_f32;
   int a_mn, b_mn;      // operand stored with its rows contiguous
   int run;             // blocks summed in tensor memory at a time (pair kernel)
   int band;            // M-tiles of a band (pair kernel)
   int mapped;          // maps.out describes the result's rows
   int load_bytes;      // of a stage (tile kernel)
+  int cols;            // of a tile, 64 or 128 (tile kernel)
   Span sp_out;
   int64_t stall_at;
   uint64_t stall_ns;
@@ -98,16 +140,16 @@ struct MatmulParams {
 
 // ---- one tile per cluster ------------------------------------------------------
 
-// Six stages where a CTA has an SM to itself (1024^3: 5.3 us, 6.2 with three;
-// 64 x 8192 x 5120: 11.5 and 14.4).  With three, and 256 columns of tensor memory,
-// two CTAs fit an SM, so that one starts while the other stores.
-constexpr int kTileStages = 6, kFewStages = 3;
+// What has more tiles than there are SMs goes to the pairs, so that a CTA has an SM to
+// itself and its ring may take most of the shared memory (1024^3: 5.3 us, 6.2 with three
+// stages).
+constexpr int kTileStages = 6;
 constexpr int kTileStageBytes = 2 * kBoxBytes + 2 * kSfBytes;
 constexpr int kTileThreads = 192;           // loads, MMA, four epilogue warps
 constexpr int kPitch = 132;                 // floats a row of the partial tile
-static_assert(kTile * kPitch * 4 <= kFewStages * kTileStageBytes, "partial tile fits the ring");
+static_assert(kTile * kPitch * 4 <= kTileStages * kTileStageBytes, "partial tile fits the ring");
 
-__global__ void __launch_bounds__(kTileThreads, 2)
+__global__ void __launch_bounds__(kTileThreads, 1)
     tile_matmul_kernel(const __grid_constant__ MatmulMaps maps, const MatmulParams p) {
   asm volatile("griddepcontrol.launch_dependents;");
   extern __shared__ uint8_t smem_raw[];
@@ -118,14 +160,14 @@ __global__ void __launch_bounds__(kTileThreads, 2)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_rank());
   const int tile = blockIdx.x / p.split;
-  const int mt = tile % p.m_tiles, nt = tile / p.m_tiles;
+  const int mt = tile % p.m_tiles, n0 = tile / p.m_tiles * p.cols;
   // Blocks of this CTA: equal runs, the first ones one longer.
   const int per = p.k_blocks / p.split, more = p.k_blocks % p.split;
   const int kb0 = rank * per + (rank < more ? rank : more);
   const int nkb = per + (rank < more ? 1 : 0);
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < p.stages; ++s) {
+    for (int s = 0; s < kTileStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
@@ -155,29 +197,32 @@ __global__ void __launch_bounds__(kTileThreads, 2)
           mbar_wait(&stall_bar, 0u, &abort_flag, p.stall_ns);
           break;
         }
-        if (i >= p.stages && !mbar_wait(&empty[s], turn ^ 1u, &abort_flag)) break;
+        if (i >= kTileStages && !mbar_wait(&empty[s], turn ^ 1u, &abort_flag)) break;
         uint8_t* st = ring + s * kTileStageBytes;
         const int kb = kb0 + i;
         mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(p.load_bytes));
         tma_load_2d(st, &maps.a, p.a_mn ? mt * kTile : kb * kBK, p.a_mn ? kb * kBK : mt * kTile,
                     &full[s]);
-        tma_load_2d(st + kBoxBytes, &maps.b, p.b_mn ? nt * kTile : kb * kBK,
-                    p.b_mn ? kb * kBK : nt * kTile, &full[s]);
+        tma_load_2d(st + kBoxBytes, &maps.b, p.b_mn ? n0 : kb * kBK, p.b_mn ? kb * kBK : n0,
+                    &full[s]);
         tma_load_2d(st + 2 * kBoxBytes, &maps.sa, kb * 128, mt, &full[s]);
-        tma_load_2d(st + 2 * kBoxBytes + kSfBytes, &maps.sb, kb * 128, nt, &full[s]);
-        if (++s == p.stages) {
+        tma_load_2d(st + 2 * kBoxBytes + kSfBytes, &maps.sb, kb * 128, n0 / kTile, &full[s]);
+        if (++s == kTileStages) {
           s = 0;
           turn ^= 1u;
         }
       }
       // Gave up: the copies already issued land before the CTA moves on.
       if (i < nkb)
-        for (int j = i > p.stages ? i - p.stages : 0; j < i; ++j)
-          mbar_drain(&full[j % p.stages], static_cast<uint32_t>((j / p.stages) & 1));
+        for (int j = i > kTileStages ? i - kTileStages : 0; j < i; ++j)
+          mbar_drain(&full[j % kTileStages], static_cast<uint32_t>((j / kTileStages) & 1));
     }
   } else if (warp == 1) {
     if (elect_one()) {
-      const uint32_t idesc = mxf8_idesc(128, 128, p.a_mn, p.b_mn);
+      const uint32_t idesc = mxf8_idesc(128, p.cols, p.a_mn, p.b_mn);
+      // The scales of 32 rows of B take a column of tensor memory: a tile of 64 columns
+      // reads the first or the last two of its rows' four.
+      const uint32_t t_sfb_here = t_sfb + (n0 % kTile) / 32;
       const uint32_t step_a = p.a_mn ? kStepMN : kStepK, step_b = p.b_mn ? kStepMN : kStepK;
       int s = 0;
       uint32_t turn = 0;
@@ -193,9 +238,9 @@ __global__ void __launch_bounds__(kTileThreads, 2)
         for (int k = 0; k < 4; ++k)
           if (k < steps)
             mma_mxf8<1>(tmem, da + step_a * k, db + step_b * k, mxf8_idesc_step(idesc, k), t_sfa,
-                        t_sfb, i + k > 0);
+                        t_sfb_here, i + k > 0);
         tcgen05_commit<1>(&empty[s]);
-        if (++s == p.stages) {
+        if (++s == kTileStages) {
           s = 0;
           turn ^= 1u;
         }
@@ -209,7 +254,6 @@ __global__ void __launch_bounds__(kTileThreads, 2)
   __syncthreads();
   tcgen05_fence_after();
   const bool ok = abort_flag == 0;
-  const int64_t n0 = static_cast<int64_t>(nt) * kTile;
   const int quarter = warp & 3;
   const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
   if (p.split == 1) {
@@ -220,7 +264,7 @@ __global__ void __launch_bounds__(kTileThreads, 2)
       uint8_t* so = ring + quarter * 4 * kStageOut;
       const int per = p.out_f32 ? 32 : 64;              // columns of a box
 #pragma unroll 1
-      for (int c = 0; c < 128; c += 32) {
+      for (int c = 0; c < p.cols; c += 32) {
         if (n0 + c >= p.N) break;
         uint32_t v[32];
         tmem_ld_32(tmem + lanes + c, v);
@@ -245,14 +289,14 @@ __global__ void __launch_bounds__(kTileThreads, 2)
       fence_proxy_async_smem();
       __syncwarp();
       if (!p.mapped) {
-        for (int c = 0; c < 128 && n0 + c < p.N; c += per) {
+        for (int c = 0; c < p.cols && n0 + c < p.N; c += per) {
           const uint8_t* box = so + c / per * kStageOut;
           if (p.out_f32) store_box<4>(box, p.out, m, n0 + c, p.M, p.N, lane, p.sp_out);
           else store_box<2>(box, p.out, m, n0 + c, p.M, p.N, lane, p.sp_out);
         }
       } else if (lane == 0) {
-        for (int c = 0; c < 128 && n0 + c < p.N; c += per)
-          tma_store_2d(&maps.out, static_cast<int>(n0) + c, static_cast<int>(m), so + c / per * kStageOut);
+        for (int c = 0; c < p.cols && n0 + c < p.N; c += per)
+          tma_store_2d(&maps.out, n0 + c, static_cast<int>(m), so + c / per * kStageOut);
         bulk_commit();
         bulk_wait<0>();
       }
@@ -270,7 +314,7 @@ __global__ void __launch_bounds__(kTileThreads, 2)
   if (warp >= 2) {
     const int row = quarter * 32 + lane;
 #pragma unroll 1
-    for (int c = 0; c < 128; c += 32) {
+    for (int c = 0; c < p.cols; c += 32) {
       uint32_t v[32];
       tmem_ld_32(tmem + lanes + c, v);
       tmem_ld_wait();
@@ -288,8 +332,9 @@ __global__ void __launch_bounds__(kTileThreads, 2)
   const int64_t m0 = static_cast<int64_t>(mt) * kTile + rank * rows;
   const bool vec = (p.N & 7) == 0;
   if (ok) {
-    for (int i = threadIdx.x; i < rows * 16; i += kTileThreads) {
-      const int r = i >> 4, c = (i & 15) * 8;
+    const int shift = p.cols == 128 ? 4 : 3, pieces = 1 << shift;      // of eight, a row
+    for (int i = threadIdx.x; i < rows * pieces; i += kTileThreads) {
+      const int r = i >> shift, c = (i & (pieces - 1)) * 8;
       const int64_t m = m0 + r, n = n0 + c;
       if (m >= p.M || n >= p.N) continue;
       const uint32_t at = smem_u32(part + (rank * rows + r) * kPitch + c);
@@ -639,27 +684,12 @@ int launch_matmul(const MatmulMaps& maps, int64_t M, int64_t N, int64_t K, bool 
     return out_f32 ? launch_pairs<true>(maps, p, num_sms, stream)
                    : launch_pairs<false>(maps, p, num_sms, stream);
   p.m_tiles = static_cast<int>((M + kTile - 1) / kTile);
-  p.n_tiles = static_cast<int>((N + kTile - 1) / kTile);
+  const TileShape shape = tile_shape(M, N, p.k_blocks, num_sms);
+  p.cols = b_mn ? 128 : shape.cols;
+  p.split = shape.split;
+  p.n_tiles = static_cast<int>((N + p.cols - 1) / p.cols);
   const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
-  // The contraction is cut in 2, 4 or 8 where that is estimated to be quicker: a
-  // block of 128 steps takes about 0.2 us of a CTA that waits for its loads,
-  // joining up to 0.4 us + 2.4 us for 128 rows (64 KB of partial sums a CTA, two
-  // cluster barriers).  160 x 1024 x 1024: 5.4 us whole, 7.1 in two; 160 x 1024 x
-  // 4096: 11.3 us whole, 9.1 in four; 32 x 32 x 16640: 34 us whole, 8.5 in eight.
-  // Clusters of eight only up to 96 CTAs: 128 of them do not all find room at
-  // once (512 x 512 x 16640: 15.8 us in four, 24.5 in eight).
-  p.split = 1;
-  const int64_t join = 2 + 12 * (M < 128 ? M : 128) / 128;        // in blocks
-  int64_t best = p.k_blocks;
-  for (int s = 2; s <= 8 && s <= p.k_blocks; s *= 2) {
-    const int64_t cost = (p.k_blocks + s - 1) / s + join;
-    if (cost < best && tiles * s <= (s == 8 ? 96 : num_sms)) {
-      best = cost;
-      p.split = s;
-    }
-  }
-  p.stages = tiles * p.split <= num_sms ? kTileStages : kFewStages;
-  p.load_bytes = matmul_box_rows(M, a_mn) * kBK + matmul_box_rows(N, b_mn) * kBK + 2 * kSfBytes;
+  p.load_bytes = (matmul_box_rows(M, a_mn, kTile) + matmul_box_rows(N, b_mn, p.cols)) * kBK + 2 * kSfBytes;
   if (tiles * p.split > 0x7fffffff) return static_cast<int>(cudaErrorInvalidConfiguration);
   static DeviceCache attr_cache;
   const int attr = attr_cache.get([] {
@@ -671,7 +701,7 @@ int launch_matmul(const MatmulMaps& maps, int64_t M, int64_t N, int64_t K, bool 
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles * p.split));
   cfg.blockDim = dim3(kTileThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(p.stages * kTileStageBytes + 1024);
+  cfg.dynamicSmemBytes = static_cast<size_t>(kTileStages * kTileStageBytes + 1024);
   cfg.stream = stream;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -254,3 +254,13 @@ def test_rows_off_the_boundary(M, N, K, dtype):
 def test_few_tiles_off_the_boundary(M, N, K, dtype):
     a, b = operand(M, K, M + N), operand(N, K, N + 1)
     check(a, b, product(a, b, dtype))
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=["bf16", "f32"])
+@pytest.mark.parametrize("M,N,K", [(160, 1024, 1024), (160, 1000, 4096), (79, 4624, 1856), (126, 600, 1600),
+                                   (499, 40, 1984), (25, 1736, 864), (38, 2312, 2112), (512, 512, 512),
+                                   (1, 200, 224), (130, 72, 8224)])
+def test_few_tiles(M, N, K, dtype):
+    """Tiles of 64 columns and of 128, whole and cut."""
+    a, b = operand(M, K, M + N), operand(N, K, N + 1)
+    check(a, b, product(a, b, dtype))

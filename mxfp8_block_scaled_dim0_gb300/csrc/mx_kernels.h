@@ -111,11 +111,11 @@ int launch_group_offsets(const int32_t* offs, int G, int64_t M, int64_t* row_off
 int launch_scales_to_blocked(const uint8_t* s, int64_t R, int64_t C, uint8_t* out,
                              cudaStream_t stream);
 // MX product (mx_matmul.cu).  qa and qb: boxes of 128 bytes x 128 rows (without
-// matmul_pairs(): matmul_box_rows() of tiles of 128 and matmul_tile_cols()), 128B swizzle (rows along the contraction
-// where a_mn / b_mn); sa and sb: their
-// blocked scales as rows of 128x4 tiles (32-bit words), boxes of one 512-byte
-// tile, with matmul_pairs() sb boxes of two rows' tiles; with matmul_mapped(), out:
-// boxes of 128 bytes x 32 rows, 128B swizzle.
+// matmul_pairs(): matmul_box_rows() of a tile of 128 rows of A, of matmul_tile_cols()
+// of B), 128B swizzle (rows along the contraction where a_mn / b_mn); sa and sb: their
+// blocked scales as rows of 128x4 tiles (32-bit words), boxes of one 512-byte tile,
+// with matmul_pairs() sb boxes of two rows' tiles; with matmul_mapped(), out: boxes of
+// 128 bytes x 32 rows, 128B swizzle.
 struct MatmulMaps {
   CUtensorMap a, b, sa, sb, out;
 };

@@ -1,9 +1,10 @@
 // torch_call.cpp -- the allocating wrappers of the training operators, and of the 2D
-// casts whose outputs they take, as plain CPython functions: they look the arguments over, allocate the outputs with
-// torch's allocator and call the C ABI on torch's current stream.
+// casts whose outputs they take, as plain CPython functions: they look the arguments
+// over, allocate the outputs with torch's allocator and call the C ABI on torch's
+// current stream.
 //
 // An operator on a few tokens takes the GPU two to five microseconds; a wrapper
-// in Python takes 9 to 23 (a torch.empty alone 1.5 to 4).  These take 3 to 6.
+// in Python takes 9 to 23 (a torch.empty alone 1.5 to 4).  These take 4 to 9.
 //
 // The first arguments are addresses of C ABI functions (of whichever build of
 // the library the binding has loaded).  Each function returns its outputs, the

@@ -13,12 +13,26 @@ everything that the backward pass needs of the forward pass is kept as MX bytes:
     the activation's output, its dim1 cast (for dW2)        33/32 F
     the norm's statistics                                   8
 
-half of what bf16 would take (4 D + 6 F).  Run as a program, it trains the block
-for a few steps on the current GPU and prints the loss and the bytes kept.
+half of what bf16 would take (4 D + 6 F).  The operators' results carry no graph, so
+the block can be differentiated once; a second derivative raises an error.  Run as a
+program, it trains the block for a few steps on the current GPU and prints the loss
+and the bytes kept.
 """
 import torch
 
 import mxfp8_block_scaled_dim0_gb300 as mx
+
+
+class _Once(torch.autograd.Function):
+    """Its inputs but the first, as results that cannot be differentiated."""
+
+    @staticmethod
+    def forward(ctx, anchor, *grads):
+        return tuple(g.view_as(g) for g in grads)
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("FeedForward has no second derivative")
 
 
 class _Block(torch.autograd.Function):
@@ -37,7 +51,16 @@ class _Block(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dy):
-        (xq, xs, mean, rstd, n1, ns1, gq, gs, h1, hs1, norm_w, a1, as1, b1, bs1) = ctx.saved_tensors
+        with torch.no_grad():
+            grads = _Block.gradients(dy, *ctx.saved_tensors)
+        if torch.is_grad_enabled():
+            # create_graph=True.  The gradients depend on x and the weights even where
+            # dy is a constant: the anchor, not dy, brings them into the graph.
+            grads = _Once.apply(torch.empty(0, requires_grad=True), *grads)
+        return (*grads, None)
+
+    @staticmethod
+    def gradients(dy, xq, xs, mean, rstd, n1, ns1, gq, gs, h1, hs1, norm_w, a1, as1, b1, bs1):
         dy = dy.contiguous()
         d0, ds0, d1, ds1 = mx.cast_dim0_dim1(dy)
         dw2 = mx.matmul(d1, ds1, h1, hs1)
@@ -46,7 +69,7 @@ class _Block(torch.autograd.Function):
         dw1 = mx.matmul(e1, es1, n1, ns1)
         dn = mx.matmul(e0, es0, a1, as1)
         dx, dw, db = mx.layer_norm_backward(dn, (xq, xs), norm_w, mean, rstd)
-        return dy + dx, dw, db, dw1, dw2, None
+        return dy + dx, dw, db, dw1, dw2
 
 
 class FeedForward(torch.nn.Module):

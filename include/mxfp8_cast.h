@@ -304,7 +304,8 @@ int mx_layer_norm(const void* x, const void* w, const void* b, int32_t w_type, i
                   void* stream);
 
 /* Its backward pass, from x itself or from the saved input (x is then what
- * (q0, s0_blk) stand for, mean and rstd still those of the forward pass):
+ * (q0, s0_blk) stand for, mean and rstd still those of the forward pass; bytes of
+ * s0_blk that belong to no block reach no result):
  *   xh = (x - mean) rstd, g = dy w
  *   dx = rstd (g - (1/D) sum g - xh (1/D) sum g xh), rounded once to bf16
  *   dw = sum over rows of dy xh, db = sum over rows of dy, summed in fp32 in a

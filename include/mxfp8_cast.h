@@ -278,8 +278,9 @@ int mx_cast_rowwise(const void* x, int64_t M, int64_t K, void* q, void* scale, v
  * A NaN scale (0xFF) or element makes the results that use it NaN; sums
  * beyond the output type's range give infinity, sums below 2^-126 may come out as
  * zero.  Sums run in the tensor core's accumulator, which cuts bits off where
- * fp32 would round (1.5e-6 of the 2-norm after 16640 steps); large fp32 outputs (from
- * about 38 tiles of 256 x 256) are summed 4096 steps at a time (2.9e-7).
+ * fp32 would round; for an fp32 output over 4096 steps at most, and those are added
+ * up in fp32 (2.3e-7 of the 2-norm after 131072 steps, 1.4e-6 where all terms have
+ * one sign, at any size of the output).
  * A call gives the same bits every time. */
 int mx_matmul(const void* qa, const void* sa_blk, const void* qb, const void* sb_blk, int64_t M,
               int64_t N, int64_t K, int32_t orders, void* out, int32_t out_type, void* stream);

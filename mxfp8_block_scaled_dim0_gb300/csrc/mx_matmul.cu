@@ -25,10 +25,11 @@
 // holds two results of 256 columns that overlap in 16, and the scales in the
 // last 16; the eight epilogue warps of a CTA take a result into registers at
 // once, and the next tile's MMAs run while they store it.  For an fp32 result longer
-// sums are cut into runs of 4096 steps that the epilogue adds up in registers:
-// the tensor core's accumulator cuts bits off at every addition, an error
-// that grows with the run (3.7e-7 in the 2-norm at 4096 steps, 1.5e-6 at
-// 16640); a bf16 result does not notice either.  16640 x 8192 x 5120 takes 365 us
+// sums, in this kernel and the next, are cut into runs of at most 4096 steps that the
+// epilogue adds up in registers: the tensor core's accumulator cuts bits off at every
+// addition, an error that grows with the run.  Over 16640 steps, in the 2-norm: random
+// signs 1.8e-7 (one run 1.2e-6, a plain fp32 product 1.9e-7), one sign 8.8e-7 (9.9e-6,
+// 8.2e-7).  A bf16 result does not notice.  16640 x 8192 x 5120 takes 365 us
 // (3.8 PFLOP/s); launched again and again 461 us (3.0), where the GPU's power limit
 // sets the clock.  The tensor cores are the bound (busy in 78% of all cycles at
 // 8192 x 8192 x 4096); the rest goes to a launch's first loads, to the last tiles'
@@ -40,9 +41,11 @@
 // 3008).
 //
 // tile_matmul_kernel: one 128 x 128 (or 64) tile of C per cluster of S CTAs, the
-// contraction cut into S equal runs of 128-step blocks; each CTA leaves its
+// contraction cut into S equal shares of 128-step blocks; each CTA leaves its
 // partial tile in its shared memory, and each then sums 128 / S of the tile's
-// rows over the S CTAs in rank order (fixed order: the same bits every run).
+// rows over the S CTAs in rank order (fixed order: the same bits every time).  The runs
+// of long fp32 sums cost 5%: 1536 x 1536 x 16640 37.8 -> 40.1 us, 1024 x 1024 x 65536
+// 72.6 -> 76.2.
 // 160 x 1024 x 1024 takes 4.9 us, 1 x 8192 x 5120 9.7: latency (loads, the chain of
 // a tile's MMAs, the stores), not bandwidth.
 #include <cuda_bf16.h>
@@ -118,6 +121,7 @@ constexpr int kTile = 128;                  // rows of one operand box
 constexpr int kBoxBytes = kTile * kBK;      // 16 KB
 constexpr int kSfBytes = 512;               // one 128x4 blocked scale tile
 constexpr int kStageOut = 4096;             // 32 rows x 128 bytes on their way out
+constexpr int kRun = 32;                    // blocks of a run, summed in tensor memory, for fp32
 
 struct MatmulParams {
   void* out;
@@ -128,7 +132,7 @@ struct MatmulParams {
   int split;           // CTAs of a cluster along the contraction (tile kernel)
   int out_f32;
   int a_mn, b_mn;      // operand stored with its rows contiguous
-  int run;             // blocks summed in tensor memory at a time (pair kernel)
+  int run;             // blocks summed in tensor memory at a time, at most
   int band;            // M-tiles of a band (pair kernel)
   int mapped;          // maps.out describes the result's rows
   int load_bytes;      // of a stage (tile kernel)
@@ -149,11 +153,21 @@ constexpr int kTileThreads = 192;           // loads, MMA, four epilogue warps
 constexpr int kPitch = 132;                 // floats a row of the partial tile
 static_assert(kTile * kPitch * 4 <= kTileStages * kTileStageBytes, "partial tile fits the ring");
 
+// Where run r of n blocks' equal runs ends.
+__device__ __forceinline__ int run_end(int n, int runs, int r) {
+  return static_cast<int>(static_cast<int64_t>(n) * (r + 1) / runs);
+}
+
+// RUNS: a CTA's contraction is cut into equal runs of at most p.run blocks, summed in
+// two places of tensor memory in turn; the epilogue warps add the runs up in
+// registers, a run's place being read while the next one's MMAs go on.
+template <bool RUNS>
 __global__ void __launch_bounds__(kTileThreads, 1)
     tile_matmul_kernel(const __grid_constant__ MatmulMaps maps, const MatmulParams p) {
   asm volatile("griddepcontrol.launch_dependents;");
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full[kTileStages], empty[kTileStages], done, stall_bar;
+  __shared__ __align__(8) uint64_t ready[2], drained[2];     // RUNS: the places
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
   uint8_t* ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -161,16 +175,23 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int rank = static_cast<int>(cluster_rank());
   const int tile = blockIdx.x / p.split;
   const int mt = tile % p.m_tiles, n0 = tile / p.m_tiles * p.cols;
-  // Blocks of this CTA: equal runs, the first ones one longer.
+  // Blocks of this CTA: equal shares, the first ones one longer.
   const int per = p.k_blocks / p.split, more = p.k_blocks % p.split;
   const int kb0 = rank * per + (rank < more ? rank : more);
   const int nkb = per + (rank < more ? 1 : 0);
+  const int runs = RUNS ? (nkb + p.run - 1) / p.run : 1;
+  constexpr uint32_t kTmemCols = RUNS ? 512 : 256;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kTileStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
+    if (RUNS)
+      for (int j = 0; j < 2; ++j) {
+        mbar_init(&ready[j], 1);
+        mbar_init(&drained[j], 4);            // the epilogue warps
+      }
     mbar_init(&done, 1);
     mbar_init(&stall_bar, 1);
     abort_flag = 0;
@@ -180,13 +201,17 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     prefetch_tmap(&maps.sa);
     prefetch_tmap(&maps.sb);
   }
-  if (warp == 1) tmem_alloc<1>(&tmem_base, 256);
+  if (warp == 1) tmem_alloc<1>(&tmem_base, kTmemCols);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   tcgen05_fence_before();
   __syncthreads();
   tcgen05_fence_after();
   const uint32_t tmem = tmem_base;
-  const uint32_t t_sfa = tmem + 128, t_sfb = tmem + 132;
+  const uint32_t t_sfa = tmem + kTmemCols / 2, t_sfb = t_sfa + 4;
+  const int quarter = warp & 3;
+  const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+  // This lane's row of the runs before the last.
+  float sums[RUNS ? kTile : 1] = {};
 
   if (warp == 0) {
     if (elect_one()) {
@@ -226,7 +251,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const uint32_t step_a = p.a_mn ? kStepMN : kStepK, step_b = p.b_mn ? kStepMN : kStepK;
       int s = 0;
       uint32_t turn = 0;
+      int run = 0, begin = 0, end = run_end(nkb, runs, 0);     // this run and its blocks
+      uint32_t d = tmem;
       for (int i = 0; i < nkb; ++i) {
+        if (RUNS && i == end) {
+          tcgen05_commit<1>(&ready[run & 1]);
+          begin = end;
+          end = run_end(nkb, runs, ++run);
+          d = tmem + (run & 1) * kTile;
+          if (run >= 2 && !mbar_wait(&drained[run & 1], static_cast<uint32_t>((run >> 1) - 1) & 1u,
+                                     &abort_flag))
+            break;
+        }
         if (!mbar_wait(&full[s], turn, &abort_flag)) break;
         tcgen05_fence_after();
         const uint32_t st = smem_u32(ring + s * kTileStageBytes);
@@ -237,8 +273,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           if (k < steps)
-            mma_mxf8<1>(tmem, da + step_a * k, db + step_b * k, mxf8_idesc_step(idesc, k), t_sfa,
-                        t_sfb_here, i + k > 0);
+            mma_mxf8<1>(d, da + step_a * k, db + step_b * k, mxf8_idesc_step(idesc, k), t_sfa,
+                        t_sfb_here, i > begin || k > 0);
         tcgen05_commit<1>(&empty[s]);
         if (++s == kTileStages) {
           s = 0;
@@ -248,14 +284,40 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       tcgen05_commit<1>(&done);
       mbar_drain(&done, 0u, kWaitLimitNs);   // every MMA issued has finished
     }
+  } else if (RUNS) {
+    for (int run = 0; run < runs - 1; ++run) {
+      if (!mbar_wait(&ready[run & 1], static_cast<uint32_t>(run >> 1) & 1u, &abort_flag)) break;
+      tcgen05_fence_after();
+      const uint32_t at = tmem + lanes + (run & 1) * kTile;
+#pragma unroll
+      for (int c = 0; c < kTile; c += 16) {
+        if (c >= p.cols) break;
+        uint32_t v[16];
+        tmem_ld_16(at + c, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) sums[(RUNS ? c : 0) + (RUNS ? j : 0)] += __uint_as_float(v[j]);
+      }
+      tcgen05_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&drained[run & 1]);
+    }
   }
   __syncwarp();
   // All roles meet here; by now this CTA's MMAs and copies are finished.
   __syncthreads();
   tcgen05_fence_after();
   const bool ok = abort_flag == 0;
-  const int quarter = warp & 3;
-  const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+  // Columns c .. c + 32 of this lane's row: the last run and, RUNS, those before it.
+  const uint32_t last = tmem + lanes + ((runs - 1) & 1) * kTile;
+  auto get = [&](int c, uint32_t (&v)[32]) {
+    tmem_ld_32(last + c, v);
+    tmem_ld_wait();
+    if constexpr (RUNS)
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(sums[c + j] + __uint_as_float(v[j]));
+  };
+  constexpr int kUnroll = RUNS ? 4 : 1;      // sums are registers: c must be a constant
   if (p.split == 1) {
     // 32 rows at a time and warp through shared memory, and a tensor map where one
     // can describe the result, 128 bytes of a row a box.
@@ -263,12 +325,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     if (warp >= 2 && ok && m < p.M) {
       uint8_t* so = ring + quarter * 4 * kStageOut;
       const int per = p.out_f32 ? 32 : 64;              // columns of a box
-#pragma unroll 1
-      for (int c = 0; c < p.cols; c += 32) {
-        if (n0 + c >= p.N) break;
+#pragma unroll kUnroll
+      for (int c = 0; c < kTile; c += 32) {
+        if (c >= p.cols || n0 + c >= p.N) break;
         uint32_t v[32];
-        tmem_ld_32(tmem + lanes + c, v);
-        tmem_ld_wait();
+        get(c, v);
         uint8_t* row = so + c / per * kStageOut + lane * 128;
         if (p.out_f32) {
 #pragma unroll
@@ -305,7 +366,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     __syncthreads();
     if (warp == 1) {
       tcgen05_fence_after();
-      tmem_dealloc<1>(tmem, 256);
+      tmem_dealloc<1>(tmem, kTmemCols);
     }
     if (threadIdx.x == 0 && !ok) atomicOr(&g_matmul_watchdog, 1);
     return;
@@ -313,11 +374,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   float* part = reinterpret_cast<float*>(ring);
   if (warp >= 2) {
     const int row = quarter * 32 + lane;
-#pragma unroll 1
-    for (int c = 0; c < p.cols; c += 32) {
+#pragma unroll kUnroll
+    for (int c = 0; c < kTile; c += 32) {
+      if (c >= p.cols) break;
       uint32_t v[32];
-      tmem_ld_32(tmem + lanes + c, v);
-      tmem_ld_wait();
+      get(c, v);
       uint4* dst = reinterpret_cast<uint4*>(part + row * kPitch + c);
 #pragma unroll
       for (int j = 0; j < 8; ++j)
@@ -358,7 +419,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
   }
   cluster_sync();                             // peers have read this CTA's partial tile
-  if (warp == 1) tmem_dealloc<1>(tmem, 256);
+  if (warp == 1) tmem_dealloc<1>(tmem, kTmemCols);
   if (threadIdx.x == 0 && !ok) atomicOr(&g_matmul_watchdog, 1);
 }
 
@@ -635,7 +696,7 @@ static int launch_pairs(const MatmulMaps& maps, MatmulParams p, int num_sms, cud
   p.m_tiles = static_cast<int>((p.M + 255) / 256);
   p.n_tiles = static_cast<int>((p.N + 255) / 256);
   // Equal runs: a short last one would leave no time to read the one before.
-  const int runs = F32 ? (p.k_blocks + 31) / 32 : 1;
+  const int runs = F32 ? (p.k_blocks + kRun - 1) / kRun : 1;
   p.run = (p.k_blocks + runs - 1) / runs;
   p.band = 8;
   static DeviceCache attr_cache;
@@ -662,6 +723,33 @@ static int launch_pairs(const MatmulMaps& maps, MatmulParams p, int num_sms, cud
   cfg.attrs = at;
   cfg.numAttrs = 2;
   return static_cast<int>(cudaLaunchKernelEx(&cfg, pair_matmul_kernel<F32>, maps, p));
+}
+
+template <bool RUNS>
+static int launch_tiles(const MatmulMaps& maps, const MatmulParams& p, int64_t ctas,
+                        cudaStream_t stream) {
+  static DeviceCache attr_cache;
+  const int attr = attr_cache.get([] {
+    return static_cast<int>(cudaFuncSetAttribute(
+        tile_matmul_kernel<RUNS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        kTileStages * kTileStageBytes + 1024));
+  });
+  if (attr != 0) return attr;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(kTileThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(kTileStages * kTileStageBytes + 1024);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = static_cast<unsigned>(p.split);
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  return static_cast<int>(cudaLaunchKernelEx(&cfg, tile_matmul_kernel<RUNS>, maps, p));
 }
 
 int launch_matmul(const MatmulMaps& maps, int64_t M, int64_t N, int64_t K, bool a_mn,
@@ -691,28 +779,11 @@ int launch_matmul(const MatmulMaps& maps, int64_t M, int64_t N, int64_t K, bool 
   const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
   p.load_bytes = (matmul_box_rows(M, a_mn, kTile) + matmul_box_rows(N, b_mn, p.cols)) * kBK + 2 * kSfBytes;
   if (tiles * p.split > 0x7fffffff) return static_cast<int>(cudaErrorInvalidConfiguration);
-  static DeviceCache attr_cache;
-  const int attr = attr_cache.get([] {
-    return static_cast<int>(cudaFuncSetAttribute(
-        tile_matmul_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-        kTileStages * kTileStageBytes + 1024));
-  });
-  if (attr != 0) return attr;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles * p.split));
-  cfg.blockDim = dim3(kTileThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(kTileStages * kTileStageBytes + 1024);
-  cfg.stream = stream;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = static_cast<unsigned>(p.split);
-  at[1].val.clusterDim.y = 1;
-  at[1].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 2;
-  return static_cast<int>(cudaLaunchKernelEx(&cfg, tile_matmul_kernel, maps, p));
+  // The longest of a cluster's shares, in blocks.
+  p.run = kRun;
+  return out_f32 && (p.k_blocks + p.split - 1) / p.split > kRun
+             ? launch_tiles<true>(maps, p, tiles * p.split, stream)
+             : launch_tiles<false>(maps, p, tiles * p.split, stream);
 }
 
 int out_of_bounds_matmul(bool clear) { return read_out_of_bounds(clear); }

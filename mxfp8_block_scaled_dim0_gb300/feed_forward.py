@@ -23,6 +23,13 @@ import torch
 import mxfp8_block_scaled_dim0_gb300 as mx
 
 
+def _dense(t):
+    """t, or a copy of it where the operators could not read it in place: rows
+    apart, transposed, or off the 16-byte boundary."""
+    t = t.contiguous()
+    return t.clone() if t.data_ptr() % 16 else t
+
+
 class _Once(torch.autograd.Function):
     """Its inputs but the first, as results that cannot be differentiated."""
 
@@ -61,7 +68,7 @@ class _Block(torch.autograd.Function):
 
     @staticmethod
     def gradients(dy, xq, xs, mean, rstd, n1, ns1, gq, gs, h1, hs1, norm_w, a1, as1, b1, bs1):
-        dy = dy.contiguous()
+        dy = _dense(dy)
         d0, ds0, d1, ds1 = mx.cast_dim0_dim1(dy)
         dw2 = mx.matmul(d1, ds1, h1, hs1)
         dgu = mx.swiglu_backward(mx.matmul(d0, ds0, b1, bs1), (gq, gs))
@@ -92,7 +99,7 @@ class FeedForward(torch.nn.Module):
         x = x.reshape(-1, shape[-1])
         if x.shape[0] % 32:
             raise ValueError("the number of tokens must be a multiple of 32, got %d" % x.shape[0])
-        return _Block.apply(x, self.norm_w, self.norm_b, self.w1, self.w2, self.eps).reshape(shape)
+        return _Block.apply(_dense(x), self.norm_w, self.norm_b, self.w1, self.w2, self.eps).reshape(shape)
 
 
 def main(tokens=4096, dim=1024, hidden=4096, steps=5):

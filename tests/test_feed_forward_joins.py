@@ -102,3 +102,16 @@ def test_second_derivatives_are_refused(block):
             assert torch.equal(a, b) and not b.requires_grad
             with pytest.raises(RuntimeError, match="no second derivative"):
                 a.square().sum().backward(retain_graph=True)
+
+
+def test_inputs_of_any_layout(block):
+    """x or the gradient of y transposed, expanded, or off the 16-byte boundary."""
+    x = torch.randn(64, 64, dtype=torch.float64)
+    shifted = torch.randn(64 * 64 + 1, dtype=torch.float64)[1:].view(64, 64)
+    dy = torch.randn(64, 64, dtype=torch.float64)
+    for v in (x.t(), x[::2], shifted, x[:1].expand(32, 64)):
+        check(block, v, lambda y: (y * dy[:len(v)]).sum())
+    check(block, x, lambda y: (y.t() * dy).sum())
+    check(block, x, lambda y: y.sum())
+    head = torch.randn(1, dtype=torch.float64)
+    check(block, x, lambda y: (torch.cat([head, y.reshape(-1)]) * torch.arange(4097)).sum())

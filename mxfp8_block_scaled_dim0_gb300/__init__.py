@@ -16,13 +16,14 @@ Convenience wrappers (``cast_dim0_dim1``, ``cast_dim0``, ``cast_dim1``,
 ``swiglu``, ``swiglu_backward``) allocate outputs with torch and call the same
 entry points; the 2D casts and the last five in compiled code
 (``_torch_call.so``), which hands every call it does not take as it stands to
-the checked functions here.  ``feed_forward`` is a block of a network trained
+the checked functions here; without it these take all calls.  ``feed_forward`` is a block of a network trained
 with them.
 """
 import ctypes
 import functools
 import importlib.util
 import os
+import warnings
 
 import torch
 
@@ -114,25 +115,31 @@ def _lib():
         # Addresses that the compiled wrappers call.
         lib.addresses = {name: ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
                          for name in sig}
-        _LIB = lib
         _load_call()
+        _LIB = lib               # last: another thread that sees it finds the wrappers too
     return _LIB
 
 
-# The compiled wrappers of the training operators (csrc/torch_call.cpp).
+# The compiled wrappers (csrc/torch_call.cpp); None: not built.
 _CALL = None
 
 
 def _load_call():
+    """Without the compiled wrappers the checked functions serve every call, some
+    10 us of host time slower."""
     global _CALL
-    if _CALL is None:
-        if not os.path.exists(CALL_PATH):
-            raise ImportError("_torch_call.so is not built (expected at %s); build it with "
-                              "`python -m mxfp8_block_scaled_dim0_gb300.build`" % CALL_PATH)
+    if _CALL is not None:
+        return
+    try:
         spec = importlib.util.spec_from_file_location("_torch_call", CALL_PATH)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
-        _CALL = module
+    except (ImportError, OSError) as e:
+        warnings.warn("the compiled wrappers (%s) do not load, calls go through Python: %s; build them "
+                      "with `python -m mxfp8_block_scaled_dim0_gb300.build`" % (CALL_PATH, e),
+                      RuntimeWarning, stacklevel=3)
+        return
+    _CALL = module
 
 
 def library():
@@ -663,6 +670,8 @@ def cast_rowwise(x, stream=None):
 def _compiled(name, *args):
     """The outputs of compiled wrapper `name`, or None."""
     lib = _LIB or _lib()
+    if _CALL is None:
+        return None
     r = getattr(_CALL, name)(lib.addresses["mx_" + name], *args)
     if type(r) is int:
         raise MXError(r, "mx_" + name)

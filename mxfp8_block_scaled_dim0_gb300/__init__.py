@@ -15,7 +15,7 @@ Convenience wrappers (``cast_dim0_dim1``, ``cast_dim0``, ``cast_dim1``,
 ``cast_rowwise``, ``matmul``, ``layer_norm``, ``layer_norm_backward``,
 ``swiglu``, ``swiglu_backward``) allocate outputs with torch and call the same
 entry points; the 2D casts and the last five in compiled code
-(``_torch_call.so``), which hands every call it does not take as it stands to
+(``_torch_call.*.so``), which hands every call it does not take as it stands to
 the checked functions here; without it these take all calls.  ``feed_forward`` is a block of a network trained
 with them.
 """
@@ -23,13 +23,17 @@ import ctypes
 import functools
 import importlib.util
 import os
+import sys
 import warnings
 
 import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmxfp8_cast.so")
-CALL_PATH = os.path.join(_PKG, "_torch_call.so")
+# The compiled wrappers use torch's classes as they lie in memory: each torch has its
+# own file, and one of another torch is not found.
+CALL_PATH = os.path.join(_PKG, "_torch_call.%s.torch-%s.so"
+                         % (sys.implementation.cache_tag, torch.__version__))
 
 MX_OK = 0
 MX_ERR_NULL = -1

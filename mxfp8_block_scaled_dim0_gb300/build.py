@@ -22,9 +22,6 @@ LIB = os.path.join(PKG, "libmxfp8_cast.so")
 # the tests run parity cases through it.
 OBJ_DIR_BOUNDS = os.path.join(PKG, "_build_bounds")
 LIB_BOUNDS = os.path.join(PKG, "libmxfp8_cast_bounds.so")
-# The allocating wrappers of the training operators (CPython functions on torch's
-# C++ API, host code only).
-CALL = os.path.join(PKG, "_torch_call.so")
 SOURCES = ["mx_cast.cu", "mx_blocked.cu", "mx_dequant.cu", "mx_scaled.cu", "mx_matmul.cu",
            "mx_norm.cu", "mx_swiglu.cu", "mx_abi.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -67,17 +64,19 @@ def _compile(src, verbose_ptxas=False, bounds=False):
 
 
 def build_call(force: bool = False) -> str:
-    """Compile _torch_call.so against the torch that runs this."""
+    """Compile the allocating wrappers (CPython functions on torch's C++ API, host code
+    only) against the torch that runs this."""
+    from mxfp8_block_scaled_dim0_gb300 import CALL_PATH
     src = os.path.join(CSRC, "torch_call.cpp")
-    if not force and not _stale(CALL, [src, os.path.abspath(__file__)]):
-        return CALL
+    if not force and not _stale(CALL_PATH, [src, os.path.abspath(__file__)]):
+        return CALL_PATH
     import sysconfig
     import torch
     root = os.path.dirname(torch.__file__)
     inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api",
                                                        "include"),
            os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
-    tmp = CALL + ".tmp.%d" % os.getpid()
+    tmp = CALL_PATH + ".tmp.%d" % os.getpid()
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
            "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
            "-I", sysconfig.get_paths()["include"], *sum((["-isystem", i] for i in inc), []), src,
@@ -86,8 +85,8 @@ def build_call(force: bool = False) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("compiling %s failed:\n%s\n%s" % (src, r.stdout, r.stderr))
-    os.replace(tmp, CALL)
-    return CALL
+    os.replace(tmp, CALL_PATH)
+    return CALL_PATH
 
 
 def build(force: bool = False, verbose_ptxas: bool = False, bounds: bool = False) -> str:
@@ -124,5 +123,6 @@ def _build_library(force, verbose_ptxas, bounds) -> str:
 
 
 if __name__ == "__main__":
+    sys.path.insert(0, ROOT)          # run as a file, too
     print(build(force="--force" in sys.argv, verbose_ptxas="-v" in sys.argv,
                 bounds="--bounds" in sys.argv))

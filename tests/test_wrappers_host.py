@@ -1,4 +1,7 @@
 """Loading of the binding with and without its compiled wrappers."""
+import os
+import subprocess
+import sys
 import threading
 import time
 
@@ -56,3 +59,35 @@ def test_another_thread_sees_the_wrappers_with_the_library(unloaded, monkeypatch
     for t in threads:
         t.join()
     assert not failed, failed
+
+
+OTHER_TORCH = """
+import subprocess, warnings
+import torch
+torch.__version__ = torch.torch_version.TorchVersion("9.9.9")
+import mxfp8_block_scaled_dim0_gb300 as mx
+from mxfp8_block_scaled_dim0_gb300 import build
+with warnings.catch_warnings(record=True) as seen:
+    warnings.simplefilter("always")
+    mx.library()
+assert mx._CALL is None and len(seen) == 1, seen
+ran = []
+def run(cmd, **kwargs):
+    ran.append(cmd)
+    return subprocess.CompletedProcess(cmd, 1, "", "not run")
+build.subprocess.run = run
+try:
+    build.build_call()
+except RuntimeError as e:
+    assert "not run" in str(e)
+assert len(ran) == 1, ran
+"""
+
+
+def test_wrappers_of_another_torch_are_neither_loaded_nor_kept():
+    """They are compiled against one torch's classes: under another they are built
+    anew, and until then not loaded."""
+    mxbuild.build()
+    r = subprocess.run([sys.executable, "-c", OTHER_TORCH], cwd=os.path.dirname(mxbuild.PKG),
+                       capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr

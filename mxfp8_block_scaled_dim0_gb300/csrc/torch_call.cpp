@@ -4,7 +4,9 @@
 // current stream.
 //
 // An operator on a few tokens takes the GPU two to five microseconds; a wrapper
-// in Python takes 9 to 23 (a torch.empty alone 1.5 to 4).  These take 4 to 9.
+// in Python takes 9 to 23 (a torch.empty alone 1.5 to 4).  These take 4 to 9, an
+// allocation for every output included: outputs in one storage save up to a
+// microsecond, but keeping or saving one then keeps or saves all.
 //
 // The first arguments are addresses of C ABI functions (of whichever build of
 // the library the binding has loaded).  Each function returns its outputs, the
@@ -80,29 +82,6 @@ Tensor empty(at::IntArrayRef size, ScalarType type, int dev) {
   return Tensor(at::detail::empty_cuda(size, type, at::Device(at::kCUDA, static_cast<int8_t>(dev)),
                                        std::nullopt));
 }
-
-// Tensors that are kept and dropped together in one allocation (an allocation of
-// megabytes takes the host up to 4 us): each begins at a multiple of 256 bytes.
-class Bundle {
- public:
-  // Reserves room; the tensor itself comes from take(), in the same order.
-  void add(int64_t bytes) { total_ += (bytes + 255) / 256 * 256; }
-  Tensor take(at::IntArrayRef size, ScalarType type, int dev) {
-    if (!base_.defined()) base_ = empty({total_}, at::kByte, dev);
-    const auto meta = c10::scalarTypeToTypeMeta(type);
-    Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(base_.storage()),
-                                                        base_.key_set(), meta);
-    const int64_t item = static_cast<int64_t>(meta.itemsize());
-    t.unsafeGetTensorImpl()->set_storage_offset(used_ / item);
-    t.unsafeGetTensorImpl()->set_sizes_contiguous(size);
-    used_ += (t.numel() * item + 255) / 256 * 256;
-    return t;
-  }
-
- private:
-  Tensor base_;
-  int64_t total_ = 0, used_ = 0;
-};
 
 void* ptr(const Tensor* t) { return t ? t->data_ptr() : nullptr; }
 
@@ -190,19 +169,11 @@ PyObject* layer_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Py_RETURN_NONE;
   const int dev = common_device({x, w, b});
   if (dev < 0) Py_RETURN_NONE;
-  const int64_t scales = blocked_bytes(M, D / 32);
-  Bundle kept;
-  kept.add(4 * M);
-  kept.add(4 * M);
+  Tensor y = empty({M, D}, at::kBFloat16, dev), mean = empty({M}, at::kFloat, dev),
+         rstd = empty({M}, at::kFloat, dev), q, s;
   if (save) {
-    kept.add(M * D);
-    kept.add(scales);
-  }
-  Tensor y = empty({M, D}, at::kBFloat16, dev), mean = kept.take({M}, at::kFloat, dev),
-         rstd = kept.take({M}, at::kFloat, dev), q, s;
-  if (save) {
-    q = kept.take({M, D}, at::kByte, dev);
-    s = kept.take({scales}, at::kByte, dev);
+    q = empty({M, D}, at::kByte, dev);
+    s = empty({blocked_bytes(M, D / 32)}, at::kByte, dev);
   }
   const int rc = unlocked(address<Fn>(a[0]), ptr(x), ptr(w), ptr(b), wt == at::kFloat ? kF32 : kBF16,
                           M, D, static_cast<float>(eps), y.data_ptr(),
@@ -239,12 +210,9 @@ PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   }
   const int dev = common_device({dy, x, q, s, w, mean, rstd});
   if (dev < 0) Py_RETURN_NONE;
-  Bundle grads;
-  grads.add(4 * D);
-  grads.add(4 * D);
-  Tensor dx = empty({M, D}, at::kBFloat16, dev), dw = grads.take({D}, wt, dev), db,
+  Tensor dx = empty({M, D}, at::kBFloat16, dev), dw = empty({D}, wt, dev), db,
          work = empty({address<int64_t (*)(int64_t, int64_t)>(a[1])(M, D)}, at::kByte, dev);
-  if (bias) db = grads.take({D}, wt, dev);
+  if (bias) db = empty({D}, wt, dev);
   const int rc = unlocked(address<Fn>(a[0]), ptr(dy), ptr(x), ptr(q), ptr(s), ptr(w),
                           wt == at::kFloat ? kF32 : kBF16, static_cast<const float*>(ptr(mean)),
                           static_cast<const float*>(ptr(rstd)), M, D, dx.data_ptr(), dw.data_ptr(),
@@ -267,12 +235,8 @@ PyObject* swiglu(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (dev < 0) Py_RETURN_NONE;
   Tensor h = empty({M, F}, at::kBFloat16, dev), q, s;
   if (save) {
-    const int64_t scales = blocked_bytes(M, 2 * F / 32);
-    Bundle kept;
-    kept.add(2 * M * F);
-    kept.add(scales);
-    q = kept.take({M, 2 * F}, at::kByte, dev);
-    s = kept.take({scales}, at::kByte, dev);
+    q = empty({M, 2 * F}, at::kByte, dev);
+    s = empty({blocked_bytes(M, 2 * F / 32)}, at::kByte, dev);
   }
   const int rc = unlocked(address<Fn>(a[0]), ptr(gu), M, F, h.data_ptr(),
                           save ? q.data_ptr() : nullptr, save ? s.data_ptr() : nullptr, stream(dev));
@@ -318,11 +282,7 @@ PyObject* cast(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int64_t M = x->size(0), K = x->size(1), R = DIM1 ? K : M, C = DIM1 ? M : K;
   const int dev = common_device({x});
   if (dev < 0) Py_RETURN_NONE;
-  const int64_t scales = blocked_bytes(R, C / 32);
-  Bundle out;
-  out.add(R * C);
-  out.add(scales);
-  Tensor q = out.take({R, C}, at::kByte, dev), s = out.take({scales}, at::kByte, dev);
+  Tensor q = empty({R, C}, at::kByte, dev), s = empty({blocked_bytes(R, C / 32)}, at::kByte, dev);
   const int rc = unlocked(address<Fn>(a[0]), ptr(x), M, K, q.data_ptr(), s.data_ptr(), stream(dev));
   return rc ? PyLong_FromLong(rc) : wrapped({q, s});
   END_HANDLE_TH_ERRORS
@@ -338,14 +298,8 @@ PyObject* cast_both(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int64_t M = x->size(0), K = x->size(1);
   const int dev = common_device({x});
   if (dev < 0) Py_RETURN_NONE;
-  const int64_t n0 = blocked_bytes(M, K / 32), n1 = blocked_bytes(K, M / 32);
-  Bundle rows, cols;
-  rows.add(M * K);
-  rows.add(n0);
-  cols.add(M * K);
-  cols.add(n1);
-  Tensor q0 = rows.take({M, K}, at::kByte, dev), s0 = rows.take({n0}, at::kByte, dev),
-         q1 = cols.take({K, M}, at::kByte, dev), s1 = cols.take({n1}, at::kByte, dev);
+  Tensor q0 = empty({M, K}, at::kByte, dev), s0 = empty({blocked_bytes(M, K / 32)}, at::kByte, dev),
+         q1 = empty({K, M}, at::kByte, dev), s1 = empty({blocked_bytes(K, M / 32)}, at::kByte, dev);
   const int rc = unlocked(address<Fn>(a[0]), ptr(x), M, K, q0.data_ptr(), s0.data_ptr(),
                           q1.data_ptr(), s1.data_ptr(), stream(dev));
   return rc ? PyLong_FromLong(rc) : wrapped({q0, s0, q1, s1});

@@ -11,12 +11,14 @@
 // The first arguments are addresses of C ABI functions (of whichever build of
 // the library the binding has loaded).  Each function returns its outputs, the
 // C ABI's error code as an int, or None, before anything was done, where the
-// arguments are not exactly what it knows: contiguous CUDA tensors of the right
-// types and shapes on the current device.  The binding's checked path then takes
-// over, which works or raises the error that says what is wrong.
+// arguments are not exactly what it knows (contiguous CUDA tensors of the right
+// types and shapes on the current device) or a dispatch mode is on.  The binding's
+// checked path then takes over, which works or raises the error that says what is
+// wrong.
 #include <Python.h>
 
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/impl/TorchDispatchModeTLS.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -68,8 +70,10 @@ bool holds_bytes(const Tensor* t, int64_t n) {
 
 int64_t blocked_bytes(int64_t R, int64_t C) { return (R + 127) / 128 * 128 * ((C + 3) / 4 * 4); }
 
-// Index of the current device if all tensors live there, or -1.
+// Index of the current device if all tensors live there, or -1; -1 too where a
+// dispatch mode is on: it shall see the allocations, which here go past the dispatcher.
 int common_device(std::initializer_list<const Tensor*> ts) {
+  if (c10::impl::TorchDispatchModeTLS::any_modes_set()) return -1;
   for (const Tensor* t : ts)
     if (t && !t->is_cuda()) return -1;
   const int dev = c10::cuda::current_device();

@@ -38,8 +38,7 @@ struct SwigluParams {
   Span sp_out, sp_q, sp_s;
 };
 
-// 1 / (1 + exp(-g)).  exp(-g) overflows to infinity below g = -88.7, which gives
-// 0; a sigmoid under 2^-126 is flushed to 0.
+// 1 / (1 + exp(-g)) of a gate that is not low.
 __device__ __forceinline__ float sigmoid(float g) {
   float e, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
@@ -52,6 +51,48 @@ __device__ __forceinline__ f32x2 sigmoid2(f32x2 g) {
   unpair(g, lo, hi);
   return pair(sigmoid(lo), sigmoid(hi));
 }
+
+// Low gates.  Below g = -87.3 the sigmoid leaves fp32's normal range, and from -88.7
+// down exp(-g) overflows, while g sg u may be an ordinary number.  From kLow down sg is
+// exp(g), to fp32: the results of kLow's sigmoid, to which they are proportional, are
+// multiplied by exp(g - kLow), in two halves that stay in range.
+constexpr float kLow = -80.0f;
+
+__device__ __forceinline__ float low_result(float v, float g) {
+  float f;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"((g - kLow) * (0.5f * 1.4426950408889634f)));
+  return v * f * f;
+}
+
+__device__ __forceinline__ float low_gated(float g, float u) {
+  return low_result(g * sigmoid(kLow) * u, g);
+}
+
+__device__ __forceinline__ void gated_back(float d, float g, float u, float& dg, float& du) {
+  const bool low = g < kLow;
+  const float s = sigmoid(low ? kLow : g);
+  const float a = g * s;
+  du = d * a;
+  dg = d * u * (s + a * (1.0f - s));
+  if (low) {
+    du = low_result(du, g);
+    dg = low_result(dg, g);
+  }
+}
+
+// The largest of words of two bf16 gates each, halves apart.  As unsigned numbers the
+// negative ones lie above the positive ones, in order of their size.
+__device__ __forceinline__ uint32_t lowest2(const uint4& w) {
+  return __vmaxu2(__vmaxu2(w.x, w.y), __vmaxu2(w.z, w.w));
+}
+__device__ __forceinline__ bool any_low(uint32_t lowest) {
+  constexpr uint32_t kBits = 0xC2A0u << 16;              // kLow
+  return lowest > (kBits | 0xFFFFu) || lowest << 16 > kBits;
+}
+
+// Whether a block with this scale byte can hold a gate below kLow: at 2^-3 its largest
+// magnitude, 448, stands for 56.
+__device__ __forceinline__ bool may_be_low(uint32_t sbyte) { return sbyte >= 127 - 2; }
 
 // A warp's place: row r, piece `run` of the row, walked in steps of the whole
 // grid without a division.  Rows in 32 bits (M < 2^31), so that an address is one
@@ -75,6 +116,13 @@ struct Place {
   }
 };
 
+// blockIdx.x, read so that the compiler does not keep what it made of it the first time.
+__device__ __forceinline__ uint32_t again() {
+  uint32_t b;
+  asm volatile("mov.u32 %0, %%ctaid.x;" : "=r"(b));
+  return b;
+}
+
 __device__ __forceinline__ int64_t wide(uint32_t r, int n) {
   return static_cast<int64_t>(static_cast<uint64_t>(r) * static_cast<uint32_t>(n));
 }
@@ -86,6 +134,80 @@ __device__ __forceinline__ int64_t scale_row(uint32_t r, int cols4) {
 }
 __device__ __forceinline__ int scale_block(int b) { return (b >> 2) * 512 + (b & 3); }
 
+// Gate and up value e of row r.
+template <bool SAVE>
+__device__ __forceinline__ float2 gate_and_up(const SwigluParams& p, uint32_t r, int e) {
+  auto value = [&](int at) {
+    if constexpr (SAVE) {
+      float lo, hi;
+      e4m3x2_get(p.q[wide(r, 2 * p.F) + at], lo, hi);
+      return lo * scale_mult(p.s[scale_row(r, p.s_cols4) + scale_block(at >> 5)]);
+    } else {
+      return __uint_as_float(static_cast<uint32_t>(p.gu[wide(r, 2 * p.F) + at]) << 16);
+    }
+  };
+  return make_float2(value(e), value(e + p.F));
+}
+
+__device__ __forceinline__ uint16_t to_bf16(float v) {
+  return static_cast<uint16_t>(pack_bf16(v, 0.0f));
+}
+
+// Low gates are worked on apart from the pieces, from their inputs in memory, a value
+// at a time.
+//
+// Forward, at the kernel's end, by threads that have met one: in the loop even a
+// branch that is not taken costs 1024 x 4096 0.4 of 3.8 us and 8000 x 8191 5 of 84.
+// The n values from column c of row r:
+__device__ __forceinline__ void low_gates(const SwigluParams& p, uint32_t r, int c, int n) {
+#pragma unroll 1
+  for (int k = c; k < c + n; ++k) {
+    const float2 x = gate_and_up<false>(p, r, k);
+    uint16_t* h = p.out + wide(r, p.F) + k;
+    if (x.x < kLow && in_span(p.sp_out, h, 2)) *h = to_bf16(low_gated(x.x, x.y));
+  }
+}
+
+__device__ __forceinline__ void low_gates8(const SwigluParams& p, uint32_t r, int c) {
+  Piece<8> g;
+  g.load(p.gu + wide(r, 2 * p.F) + c);
+  if (any_low(lowest2(g.w))) low_gates(p, r, c, 8);
+}
+
+// In place of what the pieces' arithmetic made of them, before it is stored: forward by
+// rows with the save, where the block's scale tells (4096 x 4096 19.8 us; at the end,
+// which takes registers through the loop, 20.2, without low gates 19.1), ...
+__device__ __forceinline__ void low_gates_in(const SwigluParams& p, uint32_t r, int c, uint4& h) {
+  uint32_t w[4] = {h.x, h.y, h.z, h.w};
+  uint16_t* v = reinterpret_cast<uint16_t*>(w);
+#pragma unroll 1
+  for (int k = 0; k < 8; ++k) {
+    const float2 x = gate_and_up<false>(p, r, c + k);
+    if (x.x < kLow) v[k] = to_bf16(low_gated(x.x, x.y));
+  }
+  h = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// ... and backward, whose result may lie where gu does.  (Both ways in registers: 57
+// and not 48.)
+template <bool SAVE>
+__device__ __forceinline__ void low_gates_back(const SwigluParams& p, uint32_t r, int c, uint4& dg,
+                                               uint4& du) {
+  uint32_t w[8] = {dg.x, dg.y, dg.z, dg.w, du.x, du.y, du.z, du.w};
+  uint16_t* v = reinterpret_cast<uint16_t*>(w);
+#pragma unroll 1
+  for (int k = 0; k < 8; ++k) {
+    const float2 x = gate_and_up<SAVE>(p, r, c + k);
+    if (!(x.x < kLow)) continue;
+    float a, b;
+    gated_back(__uint_as_float(static_cast<uint32_t>(p.dh[wide(r, p.F) + c + k]) << 16), x.x, x.y, a, b);
+    v[k] = to_bf16(a);
+    v[8 + k] = to_bf16(b);
+  }
+  dg = make_uint4(w[0], w[1], w[2], w[3]);
+  du = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
 // Rows whose halves are a multiple of 8 values: pieces of eight, as pairs.  The
 // next piece's loads are issued before this one is worked on, without a condition
 // (past the matrix its last row, past the row its first piece: not used), for
@@ -93,12 +215,13 @@ __device__ __forceinline__ int scale_block(int b) { return (b >> 2) * 512 + (b &
 // with two pieces' loads and no prefetch, 182 us so, 215 us with two pieces of
 // prefetch (98 registers).
 template <bool SAVE>
-__global__ void __launch_bounds__(kThreads) swiglu_rows8_kernel(const SwigluParams p) {
+__global__ void __launch_bounds__(kThreads, SAVE ? 0 : 6) swiglu_rows8_kernel(const SwigluParams p) {
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
   Place at(blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), gridDim.x * (kThreads / 32), p.runs);
   const uint32_t M = static_cast<uint32_t>(p.M);
+  uint32_t lowest = 0;                         // of this thread's gates, without the save
   Piece<8> next_g, next_u;
   auto fetch = [&]() {
     const int c = (at.run * 32 + lane) * 8;
@@ -116,6 +239,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_rows8_kernel(const SwigluPara
     at.next();
     fetch();
     const bool live = r < M && c < p.F;
+    bool low = false;
     f32x2 g[4], u[4];
     if constexpr (SAVE) {
       if (!live) {
@@ -129,6 +253,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_rows8_kernel(const SwigluPara
       uint32_t sg, su;
       const uint2 qg = mx_cast_pairs(pg.w, g, sg);
       const uint2 qu = mx_cast_pairs(pu.w, u, su);
+      low = may_be_low(sg);
       uint8_t* q = p.q + wide(r, 2 * p.F) + c;
       if (live && in_span(p.sp_q, q, 8) && in_span(p.sp_q, q + p.F, 8)) {
         *reinterpret_cast<uint2*>(q) = qg;
@@ -151,9 +276,18 @@ __global__ void __launch_bounds__(kThreads) swiglu_rows8_kernel(const SwigluPara
     if (!live) continue;
 #pragma unroll
     for (int j = 0; j < 4; ++j) g[j] = mul2(mul2(g[j], sigmoid2(g[j])), u[j]);
+    if (!SAVE) lowest = __vmaxu2(lowest, lowest2(pg.w));
     uint16_t* h = p.out + wide(r, p.F) + c;
-    if (in_span(p.sp_out, h, 16)) *reinterpret_cast<uint4*>(h) = pack_pairs(g);
+    uint4 w = pack_pairs(g);
+    if (SAVE && low) low_gates_in(p, r, c, w);
+    if (in_span(p.sp_out, h, 16)) *reinterpret_cast<uint4*>(h) = w;
   }
+  if (!SAVE && any_low(lowest))
+    for (at = Place(again() * (kThreads / 32) + (threadIdx.x >> 5), gridDim.x * (kThreads / 32), p.runs);
+         at.r < M; at.next()) {
+      const int c = (at.run * 32 + lane) * 8;
+      if (c < p.F) low_gates8(p, at.r, c);
+    }
 }
 
 // The forward pass with the save on many rows whose halves are whole 128x4 scale
@@ -170,6 +304,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_tiles_kernel(const SwigluPara
   const uint32_t M = static_cast<uint32_t>(p.M);
   // The place is a tile: r its 128 rows, run its 128 columns.
   Place at(blockIdx.x, gridDim.x, p.runs);
+  uint32_t largest = 0;                        // scale of this thread's gates
   const uint32_t tiles = static_cast<uint32_t>(p.rows) >> 7;
   const int row0 = warp * 2 * kSteps + (lane >> 4), col = (lane & 15) * 8;
   Piece<8> next_g, next_u;
@@ -214,6 +349,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_tiles_kernel(const SwigluPara
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) g[j] = mul2(mul2(g[j], sigmoid2(g[j])), u[j]);
+      largest = max(largest, sg);
       uint16_t* h = p.out + wide(r, p.F) + c;
       if (in_span(p.sp_out, h, 16)) *reinterpret_cast<uint4*>(h) = pack_pairs(g);
     }
@@ -226,6 +362,13 @@ __global__ void __launch_bounds__(kThreads) swiglu_tiles_kernel(const SwigluPara
         *reinterpret_cast<uint4*>(s) = *reinterpret_cast<const uint4*>(&scales[turn][half][lane * 16]);
     }
   }
+  if (may_be_low(largest))
+    for (at = Place(again(), gridDim.x, p.runs); at.r < tiles; at.next())
+#pragma unroll 1
+      for (int step = 0; step < kSteps; ++step) {
+        const uint32_t r = at.r * 128 + row0 + 2 * step;
+        if (r < M) low_gates8(p, r, at.run * 128 + col);
+      }
 }
 
 // Loads ahead as in swiglu_rows8_kernel.
@@ -264,6 +407,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_back_rows8_kernel(const Swigl
     const int c = (at.run * 32 + lane) * 8;
     f32x2 d[4], g[4], u[4];
     get_pairs(next_d.w, d);
+    const bool low = SAVE ? may_be_low(next_sg) : any_low(lowest2(next_g.w));
     if constexpr (SAVE) {
       mx_get_pairs(next_qg, next_sg, g);
       mx_get_pairs(next_qu, next_su, u);
@@ -282,10 +426,12 @@ __global__ void __launch_bounds__(kThreads) swiglu_back_rows8_kernel(const Swigl
       g[j] = mul2(d[j], a);
     }
     if (c >= p.F) continue;
+    uint4 dg = pack_pairs(u), du = pack_pairs(g);
+    if (low) low_gates_back<SAVE>(p, r, c, dg, du);
     uint16_t* o = p.out + wide(r, 2 * p.F) + c;
     if (in_span(p.sp_out, o, 16) && in_span(p.sp_out, o + p.F, 16)) {
-      *reinterpret_cast<uint4*>(o) = pack_pairs(u);
-      *reinterpret_cast<uint4*>(o + p.F) = pack_pairs(g);
+      *reinterpret_cast<uint4*>(o) = dg;
+      *reinterpret_cast<uint4*>(o + p.F) = du;
     }
   }
 }
@@ -298,6 +444,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_kernel(const SwigluParams p) 
   const int lane = threadIdx.x & 31;
   Place at(blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), gridDim.x * (kThreads / 32), p.runs);
   const uint32_t M = static_cast<uint32_t>(p.M);
+  float lowest = 0.0f;                         // of this thread's gates
   for (; at.r < M; at.next()) {
     const uint16_t* x = p.gu + wide(at.r, 2 * p.F);
     uint16_t* out = p.out + wide(at.r, p.F);
@@ -319,9 +466,18 @@ __global__ void __launch_bounds__(kThreads) swiglu_kernel(const SwigluParams p) 
       pu[i].get(u);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) h[j] = g[j] * sigmoid(g[j]) * u[j];
+      lowest = fminf(fminf(lowest, g[0]), g[VEC - 1]);
       store_bf16<VEC>(out + c, h, p.sp_out);
     }
   }
+  if (lowest < kLow)
+    for (at = Place(again() * (kThreads / 32) + (threadIdx.x >> 5), gridDim.x * (kThreads / 32), p.runs);
+         at.r < M; at.next())
+#pragma unroll 1
+      for (int i = 0; i < kOdd; ++i) {
+        const int c = (at.run * 32 * kOdd + lane + i * 32) * VEC;
+        if (c < p.F) low_gates(p, at.r, c, VEC);
+      }
 }
 
 template <int VEC>
@@ -360,6 +516,9 @@ __global__ void __launch_bounds__(kThreads) swiglu_back_kernel(const SwigluParam
         du[j] = d[j] * a;
         dg[j] = d[j] * u[j] * (s + a * (1.0f - s));
       }
+      if (fminf(g[0], g[VEC - 1]) < kLow)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) gated_back(d[j], g[j], u[j], dg[j], du[j]);
       store_bf16<VEC>(out + c, dg, p.sp_out);
       store_bf16<VEC>(out + p.F + c, du, p.sp_out);
     }

@@ -21,10 +21,10 @@
 // The pair's two SMs share one MMA (cta_group::2): each loads 128 rows of A and
 // 128 of B for every 128 contraction steps and holds 128 rows of the result,
 // so a byte of shared memory feeds twice the products that one CTA's tile
-// would.  Loads run five stages ahead of the MMAs.  Tensor memory (512 columns)
-// holds two results of 256 columns that overlap in 16, and the scales in the
-// last 16; the eight epilogue warps of a CTA take a result into registers at
-// once, and the next tile's MMAs run while they store it.  For an fp32 result longer
+// would.  Loads run five stages ahead of the MMAs.  Tensor memory holds a result of
+// 256 columns and the scales; the eight epilogue warps of a CTA take a result into
+// registers at once, and the next tile's MMAs, which wait for that, run while they
+// store it.  (Two results do not fit beside the scales.)  For an fp32 result longer
 // sums, in this kernel and the next, are cut into runs of at most 4096 steps that the
 // epilogue adds up in registers: the tensor core's accumulator cuts bits off at every
 // addition, an error that grows with the run.  Over 16640 steps, in the 2-norm: random
@@ -429,9 +429,8 @@ constexpr int kPairStages = 5;
 constexpr int kPairStageBytes = 2 * kBoxBytes + 3 * kSfBytes;
 constexpr int kPairStrideBytes = 34 * 1024;   // 1024-byte aligned boxes
 constexpr int kPairThreads = 320;             // loads, MMA, eight epilogue warps
-constexpr int kBufCols = 240;                 // second result's first column
 constexpr int kPairSmem = kPairStages * kPairStrideBytes + 8 * kStageOut + 1024;
-constexpr uint32_t kSfaCol = 496, kSfbCol = 500;
+constexpr uint32_t kSfaCol = 256, kSfbCol = 260;
 
 struct Tiles {
   int m_tiles, n_tiles, band;
@@ -450,7 +449,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     pair_matmul_kernel(const __grid_constant__ MatmulMaps maps, const MatmulParams p) {
   asm volatile("griddepcontrol.launch_dependents;");
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t full[kPairStages], empty[kPairStages], ready[2], drained, done,
+  __shared__ __align__(8) uint64_t full[kPairStages], empty[kPairStages], ready, drained, done,
       stall_bar;
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag, issued;
@@ -467,8 +466,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       mbar_init(&full[s], 1);                 // in the leader, for both CTAs' loads
       mbar_init(&empty[s], 1);
     }
-    mbar_init(&ready[0], 1);
-    mbar_init(&ready[1], 1);
+    mbar_init(&ready, 1);
     mbar_init(&drained, 16);                  // the epilogue warps of both, in the leader
     mbar_init(&done, 1);
     mbar_init(&stall_bar, 1);
@@ -537,7 +535,6 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             break;
           }
           tcgen05_fence_after();
-          const uint32_t d = tmem + ((item & 1) ? kBufCols : 0);
           const int k1 = min(k0 + p.run, p.k_blocks);
           for (int kb = k0; kb < k1; ++kb, ++i) {
             const int s = i % kPairStages;
@@ -555,11 +552,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               if (k < steps)
-                mma_mxf8<2>(d, da + step_a * k, db + step_b * k, mxf8_idesc_step(idesc, k),
+                mma_mxf8<2>(tmem, da + step_a * k, db + step_b * k, mxf8_idesc_step(idesc, k),
                             tmem + kSfaCol, tmem + kSfbCol, kb > k0 || k > 0);
             tcgen05_commit<2>(&empty[s]);
           }
-          if (ok) tcgen05_commit<2>(&ready[item & 1]);
+          if (ok) tcgen05_commit<2>(&ready);
         }
       }
       tcgen05_commit<2>(&done);
@@ -586,12 +583,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           for (int j = 0; j < 32; ++j) v[x][j] = 0;
       }
       for (int k0 = 0; k0 < p.k_blocks; k0 += p.run, ++item) {
-        if (!mbar_wait(&ready[item & 1], static_cast<uint32_t>((item >> 1) & 1), &abort_flag)) {
+        if (!mbar_wait(&ready, static_cast<uint32_t>(item & 1), &abort_flag)) {
           ok = false;
           break;
         }
         tcgen05_fence_after();
-        const uint32_t at = tmem + lanes + ((item & 1) ? kBufCols : 0) + half * 128;
+        const uint32_t at = tmem + lanes + half * 128;
         if constexpr (!F32) {
 #pragma unroll
           for (int x = 0; x < 2; ++x) {

@@ -16,8 +16,12 @@ Convenience wrappers (``cast_dim0_dim1``, ``cast_dim0``, ``cast_dim1``,
 ``swiglu``, ``swiglu_backward``) allocate outputs with torch and call the same
 entry points; the 2D casts and the last five in compiled code
 (``_torch_call.*.so``), which hands every call it does not take as it stands to
-the checked functions here; without it these take all calls.  ``feed_forward`` is a block of a network trained
-with them.
+the checked functions here; without it these take all calls.  ``feed_forward``
+is a block of a network trained with them.
+
+No function here takes part in autograd: results carry no graph, whatever their
+inputs require.  ``feed_forward`` shows the ``autograd.Function`` that joins the
+forward and backward operators.
 """
 import ctypes
 import functools

@@ -46,7 +46,7 @@
 // rows over the S CTAs in rank order (fixed order: the same bits every time).  The runs
 // of long fp32 sums cost 5%: 1536 x 1536 x 16640 37.8 -> 40.1 us, 1024 x 1024 x 65536
 // 72.6 -> 76.2.
-// 160 x 1024 x 1024 takes 4.9 us, 1 x 8192 x 5120 9.7: latency (loads, the chain of
+// 160 x 1024 x 1024 takes 4.9 us, 1 x 8192 x 5120 9.3: latency (loads, the chain of
 // a tile's MMAs, the stores), not bandwidth.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

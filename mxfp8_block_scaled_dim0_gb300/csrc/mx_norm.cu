@@ -17,8 +17,8 @@
 //
 // Every tensor crosses the memory bus once: 5 bytes a value forward with the save
 // and backward from it, 6 backward from bf16.  16640 x 5120: forward with the save
-// 72 us (6.0 TB/s), backward from 8 bits 88 us (4.8 TB/s, the gradient kernel's
-// 5 us in it), from bf16 85 us (6.0 TB/s); 1 x 4096 forward 2.4 us.  Forward is
+// 72 us (6.0 TB/s), backward from 8 bits 89 us (4.8 TB/s, the gradient kernel's
+// 5 us in it), from bf16 86 us (5.9 TB/s); 1 x 4096 forward 2.4 us.  Forward is
 // bound by the way through shared memory (waits for its loads, 52% of the issue
 // slots taken), backward by issue and by the few warps that dw and db leave room for.
 //

@@ -7,8 +7,8 @@
 // A warp works on 32 pieces of a row's gate half and the same pieces of its up
 // half (256 columns where the width is a multiple of 8).  Every byte is read
 // and written once, which is what bounds the kernels: 16640 x 8192, forward 123 us
-// (6.7 TB/s), with the save 171 us (6.4), backward from 8 bits 168 us (6.5), from
-// bf16 208 us (6.5).  The exponential and the division go through the fast
+// (6.7 TB/s), with the save 171 us (6.4), backward from 8 bits 168.5 us (6.5), from
+// bf16 206 us (6.6).  The exponential and the division go through the fast
 // hardware functions, whose error (a few units of 2^-22) is far below the
 // bf16 rounding of the results.
 #include <cuda_runtime.h>

@@ -37,7 +37,7 @@ LIB_PATH = os.path.join(_PKG, "libmxfp8_cast.so")
 # The compiled wrappers use torch's classes as they lie in memory: each torch has its
 # own file, and one of another torch is not found.
 CALL_PATH = os.path.join(_PKG, "_torch_call.%s.torch-%s.so"
-                         % (sys.implementation.cache_tag, torch.__version__))
+                         % (sys.implementation.cache_tag, torch.__version__.replace("+", "-")))
 
 MX_OK = 0
 MX_ERR_NULL = -1

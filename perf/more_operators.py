@@ -134,7 +134,8 @@ def prepare(case, seed):
         st["b"] = _operand(_weights(g, case["N"], K), 4)
     elif op == "gated":
         st["a"] = _operand(_hidden(g, M, K), case["bits"])
-        st["b"] = _operand(_weights(g, 2 * case["F"], K), case["bits"])
+        st["gate"] = _operand(_weights(g, case["F"], K), case["bits"])
+        st["up"] = _operand(_weights(g, case["F"], K), case["bits"])
     else:
         F = case["F"]
         st["a"] = _operand(_gradient(g, M, K), case["bits"])
@@ -224,15 +225,15 @@ def _plain(st):
     if op == "product":
         c = _values(st["a"], 4) @ _values(st["b"], 4).t()
         return dict(c=c.to(torch.bfloat16 if case["out"] == "bf16" else torch.float32))
-    F = case["F"]
-    p = _values(st["a"], case["bits"]) @ _values(st["b"], case["bits"]).t()
+    F, a = case["F"], _values(st["a"], case["bits"])
     if op == "gated":
-        g, u = p[:, :F], p[:, F:]
+        g, u = (a @ _values(st[w], case["bits"]).t() for w in ("gate", "up"))
         out = dict(h=(g / (1 + torch.exp(-g)) * u).to(torch.bfloat16))
         if case["save"]:
-            q, s = _operand(p, 8)
+            q, s = _operand(torch.cat([g, u], 1), 8)
             out["q"], out["s"] = q.view(torch.float8_e4m3fn), s.view(torch.float8_e8m0fnu)
         return out
+    p = a @ _values(st["b"], case["bits"]).t()
     gu = _values(st["saved"], 8) if case["saved"] == 8 else st["saved"].float()
     g, u = gu[:, :F], gu[:, F:]
     sg = 1 / (1 + torch.exp(-g))
@@ -260,9 +261,10 @@ def _own(st):
         return dict(c=mx.matmul_fp4(*st["a"], *st["b"],
                                     torch.bfloat16 if case["out"] == "bf16" else torch.float32))
     if op == "gated":
+        w = zip(st["gate"], st["up"])
         if not case["save"]:
-            return dict(h=mx.matmul_swiglu(*st["a"], *st["b"], bits=case["bits"]))
-        h, q, s = mx.matmul_swiglu(*st["a"], *st["b"], save=True, bits=case["bits"])
+            return dict(h=mx.matmul_swiglu(*st["a"], *w, bits=case["bits"]))
+        h, q, s = mx.matmul_swiglu(*st["a"], *w, save=True, bits=case["bits"])
         return dict(h=h, q=q.view(torch.float8_e4m3fn), s=s.view(torch.float8_e8m0fnu))
     return dict(dgu=mx.matmul_swiglu_backward(*st["a"], *st["b"], st["saved"], bits=case["bits"]))
 
@@ -347,16 +349,17 @@ def exact(case, seed):
     if op == "dequant":
         return dict(x=_exact_values(st["a"], 4))
     bits = case.get("bits", 4)
-    p = torch.mm(_exact_values(st["a"], bits), _exact_values(st["b"], bits).t())
+    a = _exact_values(st["a"], bits)
+    if op == "gated":
+        g, u = (torch.mm(a, _exact_values(st[w], bits).t()) for w in ("gate", "up"))
+        out = dict(h=g * torch.sigmoid(g) * u)
+        if case["save"]:
+            out["q"], out["s"] = _exact_saved(torch.cat([g, u], 1)), None
+        return out
+    p = torch.mm(a, _exact_values(st["b"], bits).t())
     if op == "product":
         return dict(c=p)
     F = case["F"]
-    if op == "gated":
-        g, u = p.split(F, 1)
-        out = dict(h=g * torch.sigmoid(g) * u)
-        if case["save"]:
-            out["q"], out["s"] = _exact_saved(p), None
-        return out
     gu = _exact_values(st["saved"], 8) if case["saved"] == 8 else st["saved"].to(torch.float64)
     g, u = gu.split(F, 1)
     sg = torch.sigmoid(g)

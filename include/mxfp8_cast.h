@@ -1,8 +1,9 @@
 /*
  * mxfp8_cast.h -- C ABI of libmxfp8_cast.so: MX-FP8 (e4m3 elements, e8m0
- * block scales, blocks of 32) quantisation of bf16 matrices on sm_103a, and the
- * operators that train on such values: products of two MX operands, layer norm
- * and gated SiLU whose inputs are saved for the backward pass in MX-FP8.
+ * block scales, blocks of 32) and MX-FP4 (e2m1 elements) quantisation of bf16
+ * matrices on sm_103a, and the operators that work on such values: products of two
+ * MX operands, alone or joined with the gated SiLU, layer norm and gated SiLU whose
+ * inputs are saved for the backward pass in MX-FP8.
  *
  * Conventions for every entry point below
  *   - All data pointers are DEVICE pointers of the calling thread's current
@@ -73,6 +74,13 @@ enum {
 enum {
   MX_BF16 = 0,
   MX_F32 = 1
+};
+
+/* Element formats of operands that may have either: e4m3, a byte an element, or e2m1,
+ * two to a byte. */
+enum {
+  MX_E4M3 = 0,
+  MX_E2M1 = 1
 };
 
 /* Storage orders of mx_matmul's operands. */
@@ -342,6 +350,90 @@ int mx_swiglu(const void* gu, int64_t M, int64_t F, void* h, void* q0, void* s0_
 int mx_swiglu_backward(const void* dh, const void* gu, const void* q0, const void* s0_blk,
                        int64_t M, int64_t F, void* dgu, void* stream);
 
+/* MX-FP4 casts: the casts above with e2m1 elements (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign),
+ * a quarter of bf16's bytes.  The pages have no counterpart;
+ * OCP Microscaling Formats v1.0 defines the format, its blocks of 32 and its e8m0 scales.
+ *   scale byte s = clamp(floor(log2 amax) - 2, -127, 127) + 127; amax = 0 gives s = 0;
+ *                  a block holding Inf or NaN gives s = 0xFF
+ *   q_i          = e2m1(x_i * 2^(127 - s)), round to nearest even, saturated to +-6 (6 for
+ *                  every element of an Inf/NaN block, whose value is its scale's NaN)
+ * Two elements share a byte, the first in the low four bits.  Directions, blocked scales
+ * and padding as for mx_cast_dim0, mx_cast_dim1 and mx_cast_dim0_dim1:
+ *   x       bf16 (M x K), row-major                      [in]
+ *   q0      M x K/2 bytes                                [out]
+ *   s0_blk  mx_blocked_bytes(M, K/32) bytes, e8m0        [out]
+ *   q1      K x M/2 bytes: q1[k][m/2] holds X[m][k] and X[m+1][k]  [out]
+ *   s1_blk  mx_blocked_bytes(K, M/32) bytes, e8m0        [out]
+ *   M, K    K % 32 == 0; M % 32 == 0, or for dim0 alone any M >= 1; <= 2^31 - 256 */
+int mx_cast_fp4_dim0(const void* x, int64_t M, int64_t K, void* q0, void* s0_blk, void* stream);
+int mx_cast_fp4_dim1(const void* x, int64_t M, int64_t K, void* q1, void* s1_blk, void* stream);
+int mx_cast_fp4_dim0_dim1(const void* x, int64_t M, int64_t K, void* q0, void* s0_blk, void* q1,
+                          void* s1_blk, void* stream);
+
+/* MX-FP4 dequantisation to bf16, as mx_dequant_blocked: e2m1 times 2^(s - 127), rounded once
+ * (exact but for magnitudes of 2^128 or more, which give infinity; scale 0xFF gives NaN).
+ *   q       R x C/2 bytes                                [in]
+ *   R, C    R >= 1, C % 32 == 0, C >= 32, R, C <= 2^31 - 256
+ *   s_blk   mx_blocked_bytes(R, C/32) bytes, e8m0        [in]
+ *   out     R x C bf16                                   [out] */
+int mx_dequant_fp4(const void* q, int64_t R, int64_t C, const void* s_blk, void* out, void* stream);
+
+/* Product of two MX-FP4 operands, as mx_matmul at twice its rate:
+ *   out[m][n] = sum_k A[m][k] B[n][k]
+ * The three products of a linear layer take the same casts as there; both operands are
+ * stored by row.
+ *   qa      M x K/2 bytes, e2m1, blocks of 32 along rows    [in]
+ *   sa_blk  mx_blocked_bytes(M, K/32) bytes, e8m0           [in]
+ *   qb      N x K/2 bytes, e2m1                             [in]
+ *   sb_blk  mx_blocked_bytes(N, K/32) bytes, e8m0           [in]
+ *   M, N    >= 1 (any); K % 64 == 0 (the tensor cores take 64 steps at a time), K >= 64;
+ *           all <= 2^31 - 256
+ *   out     M x N values of out_type (MX_BF16 or MX_F32)    [out]
+ * Sums, NaN scales and ranges as mx_matmul. */
+int mx_matmul_fp4(const void* qa, const void* sa_blk, const void* qb, const void* sb_blk, int64_t M,
+                  int64_t N, int64_t K, void* out, int32_t out_type, void* stream);
+
+/* The first half of a gated feed-forward layer in one kernel: both projections of MX
+ * operands, the activation and the product.
+ *   g = X Wg^T, u = X Wu^T, summed in fp32
+ *   h = g u / (1 + exp(-g)), from the sums, rounded once to bf16
+ * g and u do not reach memory unless they are saved for the backward pass, in 8 bits: the
+ * layout of mx_swiglu's save, (M x 2F) rows [g | u], each value rounded once from its sum.
+ * The pages have no counterpart (see mx_layer_norm).
+ *   qx      M x K elements of `format`, blocks of 32 along rows (mx_cast_dim0 or
+ *           mx_cast_fp4_dim0 of X)                          [in]
+ *   sx_blk  mx_blocked_bytes(M, K/32) bytes, e8m0           [in]
+ *   qg, qu  F x K elements of `format` each: Wg, Wu         [in]
+ *   sg_blk, su_blk  mx_blocked_bytes(F, K/32) bytes each    [in]
+ *           (with F % 128 == 0 the two halves of a cast of [Wg; Wu], bytes and scales, are
+ *           these operands)
+ *   M, F, K M >= 1; F % 32 == 0, 32 <= F <= 2^24; K % 32 == 0 (MX_E2M1: 64), K >= 32 (64);
+ *           M, K <= 2^31 - 256
+ *   format  MX_E4M3 or MX_E2M1, of all operands
+ *   h       bf16 (M x F)                                    [out]
+ *   q0, s0_blk  both NULL, or [g | u] saved: M x 2F bytes, e4m3, and
+ *           mx_blocked_bytes(M, 2F/32) bytes                [out] */
+int mx_matmul_swiglu(const void* qx, const void* sx_blk, const void* qg, const void* sg_blk,
+                     const void* qu, const void* su_blk, int64_t M, int64_t F, int64_t K,
+                     int32_t format, void* h, void* q0, void* s0_blk, void* stream);
+
+/* Its backward pass, through the layer's second projection y = h W2^T: from the gradient of
+ * y to that of [g | u], in one kernel; the gradient of h does not reach memory.
+ *   dh = dY W2, summed in fp32
+ *   sg = 1 / (1 + exp(-g)), dg = dh u sg (1 + g (1 - sg)), du = dh g sg, rounded once to bf16
+ *   qdy     M x K elements of `format`, blocks along rows (the dim0 cast of dY)  [in]
+ *   sdy_blk mx_blocked_bytes(M, K/32) bytes, e8m0           [in]
+ *   qw      F x K elements of `format`: W2 transposed (the dim1 cast of W2, K x F)  [in]
+ *   sw_blk  mx_blocked_bytes(F, K/32) bytes, e8m0           [in]
+ *   gu      bf16 (M x 2F), or NULL with q0, s0_blk given    [in]
+ *   dgu     bf16 (M x 2F): dg | du                          [out]
+ * Sizes and format as mx_matmul_swiglu.  The weights' gradients are products of the casts of
+ * dY and dgu (mx_matmul, mx_matmul_fp4). */
+int mx_matmul_swiglu_backward(const void* qdy, const void* sdy_blk, const void* qw,
+                              const void* sw_blk, int64_t M, int64_t F, int64_t K, int32_t format,
+                              const void* gu, const void* q0, const void* s0_blk, void* dgu,
+                              void* stream);
+
 /* Size helpers (host only, no CUDA calls).  Return -1 for invalid sizes. */
 int64_t mx_blocked_bytes(int64_t R, int64_t C);
 /* dim 0: (M + 128*G) * ceil4(K/32); dim 1: ceil128(K) * (ceil(M/32) + 4*G). */
@@ -396,9 +488,10 @@ int mx_selftest_watchdog(int64_t wait_ns, void* stream);
  * mx_cast_dim0, mx_cast_dim1, mx_cast_grouped_m and the 3D casts; the
  * bulk-staged kernel of mx_cast_rowwise, used for K <= 24576; the tiled
  * kernel of mx_dequant_blocked, used for C >= 1024; the kernels of mx_matmul,
- * mx_layer_norm and the first of mx_layer_norm_backward).  In that launch the
+ * mx_matmul_fp4, mx_matmul_swiglu, mx_matmul_swiglu_backward, mx_cast_fp4_dim1,
+ * mx_cast_fp4_dim0_dim1, mx_layer_norm and the first of mx_layer_norm_backward).  In that launch the
  * thread of CTA 0 that issues its loads waits, at its `at`-th tile (rowwise:
- * step; mx_matmul: block of 128 contraction steps; layer norm: row of its first
+ * step; products: block of 128 contraction bytes; layer norm: row of its first
  * group), on a barrier that nothing completes, for at most `wait_ns` nanoseconds
  * (1e3 .. 1e10).  The wait gives up, the CTA stops every role, lets the
  * copies it has in flight land, sets the word read by mx_watchdog(), and the

@@ -1,5 +1,5 @@
-"""MX-FP8 casts of bf16 matrices, and operators that train on their outputs, on
-sm_103a (GB300): Python binding.
+"""MX-FP8 and MX-FP4 casts of bf16 matrices, and operators that work on their outputs,
+on sm_103a (GB300): Python binding.
 
 Thin ctypes layer over the C ABI of ``libmxfp8_cast.so`` (declared in
 ``include/mxfp8_cast.h``).  Functions named like the C entry points take torch
@@ -12,11 +12,13 @@ raises.
 Convenience wrappers (``cast_dim0_dim1``, ``cast_dim0``, ``cast_dim1``,
 ``cast_grouped_m``, ``cast_3d_dim1``, ``cast_3d_dim0``, ``cast_3d_dim0_dim1``,
 ``scales_to_blocked``, ``dequant_blocked``, ``cast_tensorwise``,
-``cast_rowwise``, ``matmul``, ``layer_norm``, ``layer_norm_backward``,
-``swiglu``, ``swiglu_backward``) allocate outputs with torch and call the same
-entry points; the 2D casts and the last five in compiled code
-(``_torch_call.*.so``), which hands every call it does not take as it stands to
-the checked functions here; without it these take all calls.  ``feed_forward``
+``cast_rowwise``, ``cast_fp4_dim0``, ``cast_fp4_dim1``, ``cast_fp4_dim0_dim1``,
+``dequant_fp4``, ``matmul``, ``matmul_fp4``, ``matmul_swiglu``,
+``matmul_swiglu_backward``, ``layer_norm``, ``layer_norm_backward``, ``swiglu``,
+``swiglu_backward``) allocate outputs with torch and call the same entry points; the 2D
+MX casts and all from ``dequant_fp4`` on in compiled code (``_torch_call.*.so``), which
+hands every call it does not take as it stands to the checked functions here; without it
+these take all calls.  ``feed_forward``
 is a block of a network trained with them.
 
 No function here takes part in autograd: results carry no graph, whatever their
@@ -58,7 +60,9 @@ ABI_SYMBOLS = (
     "mx_strerror", "mx_last_cuda_error", "mx_watchdog",
     "mx_selftest_watchdog", "mx_selftest_arm_stall", "mx_cast_dim0_dim1_noalloc",
     "mx_matmul", "mx_layer_norm", "mx_layer_norm_backward", "mx_layer_norm_backward_work_bytes",
-    "mx_swiglu", "mx_swiglu_backward",
+    "mx_swiglu", "mx_swiglu_backward", "mx_cast_fp4_dim0", "mx_cast_fp4_dim1",
+    "mx_cast_fp4_dim0_dim1", "mx_dequant_fp4", "mx_matmul_fp4", "mx_matmul_swiglu",
+    "mx_matmul_swiglu_backward",
 )
 
 
@@ -104,6 +108,14 @@ def _lib():
             "mx_layer_norm_backward_work_bytes": ([I64, I64], I64),
             "mx_swiglu": ([P, I64, I64, P, P, P, P], ctypes.c_int),
             "mx_swiglu_backward": ([P, P, P, P, I64, I64, P, P], ctypes.c_int),
+            "mx_cast_fp4_dim0": ([P, I64, I64, P, P, P], ctypes.c_int),
+            "mx_cast_fp4_dim1": ([P, I64, I64, P, P, P], ctypes.c_int),
+            "mx_cast_fp4_dim0_dim1": ([P, I64, I64, P, P, P, P, P], ctypes.c_int),
+            "mx_dequant_fp4": ([P, I64, I64, P, P, P], ctypes.c_int),
+            "mx_matmul_fp4": ([P, P, P, P, I64, I64, I64, P, I32, P], ctypes.c_int),
+            "mx_matmul_swiglu": ([P, P, P, P, P, P, I64, I64, I64, I32, P, P, P, P], ctypes.c_int),
+            "mx_matmul_swiglu_backward": ([P, P, P, P, I64, I64, I64, I32, P, P, P, P, P],
+                                          ctypes.c_int),
             "mx_blocked_bytes": ([I64, I64], I64),
             "mx_grouped_m_scale_bytes": ([I64, I64, I32, I32], I64),
             "mx_3d_scale_bytes": ([I64, I64, I64], I64),
@@ -218,11 +230,15 @@ def _call(name, dev, stream, *args):
 BF16 = (torch.bfloat16,)
 BYTES = tuple(d for d in (torch.uint8, getattr(torch, "float8_e4m3fn", None),
                           getattr(torch, "float8_e8m0fnu", None)) if d is not None)
+# Bytes of two e2m1 values.
+BYTES4 = (torch.uint8,) + ((torch.float4_e2m1fn_x2,) if hasattr(torch, "float4_e2m1fn_x2") else ())
 I32 = (torch.int32,)
 I64 = (torch.int64,)
 F32 = (torch.float32,)
 # Element types of arguments that may have either, as the C ABI numbers them.
 TYPES = {torch.bfloat16: 0, torch.float32: 1}
+# Formats of operands, by their elements' bits, as the C ABI numbers them.
+FORMATS = {8: 0, 4: 1}
 
 
 def _dev_tensor(t, name, nbytes=None, dtypes=None, ndim=None):
@@ -421,6 +437,111 @@ def mx_matmul(qa, sa_blk, qb, sb_blk, out, stream=None):
     dev = _device(qa, sa_blk, qb, sb_blk, out)
     _call("mx_matmul", dev, stream, _ptr(qa), _ptr(sa_blk), _ptr(qb), _ptr(sb_blk), M, N, K, orders,
           _ptr(out), TYPES[out.dtype])
+
+
+def mx_cast_fp4_dim0(x, q0, s0_blk, stream=None):
+    """MX-FP4 cast of bf16 x (M x K) along its rows: q0 (M x K/2 bytes)."""
+    _dev_tensor(x, "x", dtypes=BF16, ndim=2)
+    M, K = x.shape
+    _dev_tensor(q0, "q0", M * K // 2, BYTES4)
+    _dev_tensor(s0_blk, "s0_blk", mx_blocked_bytes(M, K // 32), BYTES)
+    _call("mx_cast_fp4_dim0", _device(x, q0, s0_blk), stream, _ptr(x), M, K, _ptr(q0), _ptr(s0_blk))
+
+
+def mx_cast_fp4_dim1(x, q1, s1_blk, stream=None):
+    """MX-FP4 cast of bf16 x (M x K) along its columns: q1 (K x M/2 bytes)."""
+    _dev_tensor(x, "x", dtypes=BF16, ndim=2)
+    M, K = x.shape
+    _dev_tensor(q1, "q1", M * K // 2, BYTES4)
+    _dev_tensor(s1_blk, "s1_blk", mx_blocked_bytes(K, M // 32), BYTES)
+    _call("mx_cast_fp4_dim1", _device(x, q1, s1_blk), stream, _ptr(x), M, K, _ptr(q1), _ptr(s1_blk))
+
+
+def mx_cast_fp4_dim0_dim1(x, q0, s0_blk, q1, s1_blk, stream=None):
+    """Both MX-FP4 casts of bf16 x (M x K) in one read."""
+    _dev_tensor(x, "x", dtypes=BF16, ndim=2)
+    M, K = x.shape
+    _dev_tensor(q0, "q0", M * K // 2, BYTES4)
+    _dev_tensor(q1, "q1", M * K // 2, BYTES4)
+    _dev_tensor(s0_blk, "s0_blk", mx_blocked_bytes(M, K // 32), BYTES)
+    _dev_tensor(s1_blk, "s1_blk", mx_blocked_bytes(K, M // 32), BYTES)
+    dev = _device(x, q0, s0_blk, q1, s1_blk)
+    _call("mx_cast_fp4_dim0_dim1", dev, stream, _ptr(x), M, K, _ptr(q0), _ptr(s0_blk), _ptr(q1),
+          _ptr(s1_blk))
+
+
+def mx_dequant_fp4(q, s_blk, out, stream=None):
+    """bf16 out (R x C) = e2m1 q (R x C/2 bytes) times 2^(scale - 127)."""
+    _dev_tensor(q, "q", dtypes=BYTES4, ndim=2)
+    R, C = q.shape[0], 2 * q.shape[1]
+    _dev_tensor(s_blk, "s_blk", mx_blocked_bytes(R, C // 32), BYTES)
+    _shaped(out, "out", (R, C), BF16)
+    _call("mx_dequant_fp4", _device(q, s_blk, out), stream, _ptr(q), R, C, _ptr(s_blk), _ptr(out))
+
+
+def _by_row(q, s_blk, name, bits):
+    """Checks an MX operand of `bits` stored by row; its (rows, steps)."""
+    if bits not in FORMATS:
+        raise ValueError("bits must be 8 or 4, got %r" % (bits,))
+    _dev_tensor(q, "q" + name, dtypes=BYTES if bits == 8 else BYTES4, ndim=2)
+    R, K = q.shape[0], q.shape[1] * (8 // bits)
+    _dev_tensor(s_blk, "s%s_blk" % name, mx_blocked_bytes(R, K // 32), BYTES)
+    return R, K
+
+
+def _same_steps(name_a, Ka, name_b, Kb):
+    if Ka != Kb:
+        raise ValueError("q%s and q%s must have equal rows, got %d and %d values"
+                         % (name_a, name_b, Ka, Kb))
+
+
+def mx_matmul_fp4(qa, sa_blk, qb, sb_blk, out, stream=None):
+    """out (M x N, bf16 or float32) = A B^T of MX-FP4 operands: qa (M x K/2) and qb
+    (N x K/2) bytes with their blocked scales, K a multiple of 64."""
+    M, K = _by_row(qa, sa_blk, "a", 4)
+    N, Kb = _by_row(qb, sb_blk, "b", 4)
+    _same_steps("a", K, "b", Kb)
+    _shaped(out, "out", (M, N), tuple(TYPES))
+    dev = _device(qa, sa_blk, qb, sb_blk, out)
+    _call("mx_matmul_fp4", dev, stream, _ptr(qa), _ptr(sa_blk), _ptr(qb), _ptr(sb_blk), M, N, K,
+          _ptr(out), TYPES[out.dtype])
+
+
+def mx_matmul_swiglu(qx, sx_blk, qg, sg_blk, qu, su_blk, h, q0=None, s0_blk=None, bits=8,
+                     stream=None):
+    """h (M x F, bf16) = silu(X Wg^T) X Wu^T of MX operands X (M x K), Wg and Wu (F x K) with
+    elements of `bits`; with q0 and s0_blk both projections' results are saved in 8 bits, as
+    mx_swiglu saves its input."""
+    M, K = _by_row(qx, sx_blk, "x", bits)
+    F, Kg = _by_row(qg, sg_blk, "g", bits)
+    Fu, Ku = _by_row(qu, su_blk, "u", bits)
+    _same_steps("x", K, "g", Kg)
+    _same_steps("x", K, "u", Ku)
+    if F != Fu:
+        raise ValueError("qg and qu must have equally many rows, got %d and %d" % (F, Fu))
+    _shaped(h, "h", (M, F), BF16)
+    _saved(q0, s0_blk, M, 2 * F)
+    dev = _device(qx, sx_blk, qg, sg_blk, qu, su_blk, h, q0, s0_blk)
+    _call("mx_matmul_swiglu", dev, stream, _ptr(qx), _ptr(sx_blk), _ptr(qg), _ptr(sg_blk), _ptr(qu),
+          _ptr(su_blk), M, F, K, FORMATS[bits], _ptr(h), _ptr(q0), _ptr(s0_blk))
+
+
+def mx_matmul_swiglu_backward(qdy, sdy_blk, qw, sw_blk, gu, q0, s0_blk, dgu, bits=8, stream=None):
+    """dgu (M x 2F, bf16), the gradient of [g | u], from that of y = h W2^T: MX operands dY
+    (M x K) and W2^T (F x K) with elements of `bits`, and gu (bf16), or with gu None the
+    saved (q0, s0_blk)."""
+    M, K = _by_row(qdy, sdy_blk, "dy", bits)
+    F, Kw = _by_row(qw, sw_blk, "w", bits)
+    _same_steps("dy", K, "w", Kw)
+    if (gu is None) == (q0 is None):
+        raise ValueError("give gu, or q0 and s0_blk")
+    if gu is not None:
+        _shaped(gu, "gu", (M, 2 * F), BF16)
+    _saved(q0, s0_blk, M, 2 * F)
+    _shaped(dgu, "dgu", (M, 2 * F), BF16)
+    dev = _device(qdy, sdy_blk, qw, sw_blk, gu, q0, s0_blk, dgu)
+    _call("mx_matmul_swiglu_backward", dev, stream, _ptr(qdy), _ptr(sdy_blk), _ptr(qw), _ptr(sw_blk),
+          M, F, K, FORMATS[bits], _ptr(gu), _ptr(q0), _ptr(s0_blk), _ptr(dgu))
 
 
 def _shaped(t, name, shape, dtypes):
@@ -714,6 +835,138 @@ def matmul(qa, sa_blk, qb, sb_blk, out_dtype=torch.bfloat16, stream=None):
         out = torch.empty((qa.shape[0], qb.shape[0]), dtype=out_dtype, device=qa.device)
         mx_matmul(qa, sa_blk, qb, sb_blk, out)
     return out
+
+
+def cast_fp4_dim0(x, stream=None):
+    """Returns (q0 (M, K/2), s0_blk) as uint8 tensors, two e2m1 values a byte."""
+    if stream is not None:
+        with _on_stream(stream, x):
+            return cast_fp4_dim0(x)
+    r = _compiled("cast_fp4_dim0", x)
+    if r is not None:
+        return r
+    M, K = x.shape
+    q0 = torch.empty((M, K // 2), dtype=torch.uint8, device=x.device)
+    s0 = _u8(mx_blocked_bytes(M, K // 32), x.device)
+    mx_cast_fp4_dim0(x, q0, s0)
+    return q0, s0
+
+
+def cast_fp4_dim1(x, stream=None):
+    """Returns (q1 (K, M/2), s1_blk)."""
+    if stream is not None:
+        with _on_stream(stream, x):
+            return cast_fp4_dim1(x)
+    r = _compiled("cast_fp4_dim1", x)
+    if r is not None:
+        return r
+    M, K = x.shape
+    q1 = torch.empty((K, M // 2), dtype=torch.uint8, device=x.device)
+    s1 = _u8(mx_blocked_bytes(K, M // 32), x.device)
+    mx_cast_fp4_dim1(x, q1, s1)
+    return q1, s1
+
+
+def cast_fp4_dim0_dim1(x, stream=None):
+    """Returns (q0 (M, K/2), s0_blk, q1 (K, M/2), s1_blk)."""
+    if stream is not None:
+        with _on_stream(stream, x):
+            return cast_fp4_dim0_dim1(x)
+    r = _compiled("cast_fp4_dim0_dim1", x)
+    if r is not None:
+        return r
+    M, K = x.shape
+    q0 = torch.empty((M, K // 2), dtype=torch.uint8, device=x.device)
+    q1 = torch.empty((K, M // 2), dtype=torch.uint8, device=x.device)
+    s0 = _u8(mx_blocked_bytes(M, K // 32), x.device)
+    s1 = _u8(mx_blocked_bytes(K, M // 32), x.device)
+    mx_cast_fp4_dim0_dim1(x, q0, s0, q1, s1)
+    return q0, s0, q1, s1
+
+
+def dequant_fp4(q, s_blk, stream=None):
+    """bf16 (R, C) of MX-FP4 bytes q (R, C/2)."""
+    if stream is not None:
+        with _on_stream(stream, q):
+            return dequant_fp4(q, s_blk)
+    out = _compiled("dequant_fp4", q, s_blk)
+    if out is None:
+        R, C2 = q.shape
+        out = torch.empty((R, 2 * C2), dtype=torch.bfloat16, device=q.device)
+        mx_dequant_fp4(q, s_blk, out)
+    return out
+
+
+def matmul_fp4(qa, sa_blk, qb, sb_blk, out_dtype=torch.bfloat16, stream=None):
+    """A B^T of MX-FP4 operands as a (M, N) tensor of out_dtype."""
+    if stream is not None:
+        with _on_stream(stream, qa):
+            return matmul_fp4(qa, sa_blk, qb, sb_blk, out_dtype)
+    if out_dtype not in TYPES:
+        raise TypeError("out_dtype must be one of %s, got %s"
+                        % (", ".join(str(d) for d in TYPES), out_dtype))
+    out = _compiled("matmul_fp4", qa, sa_blk, qb, sb_blk, TYPES[out_dtype])
+    if out is None:
+        out = torch.empty((qa.shape[0], qb.shape[0]), dtype=out_dtype, device=qa.device)
+        mx_matmul_fp4(qa, sa_blk, qb, sb_blk, out)
+    return out
+
+
+def _gate_and_up(qw, sw_blk, bits):
+    """(qg, sg_blk, qu, su_blk) of two pairs, or of the cast of [Wg; Wu] as views of it."""
+    if not isinstance(qw, torch.Tensor):
+        return qw[0], sw_blk[0], qw[1], sw_blk[1]
+    F2, K = _by_row(qw, sw_blk, "w", bits)
+    F = F2 // 2
+    if F2 % 256:
+        raise ValueError("the halves of %d rows of qw do not begin on a scale tile of 128 rows: cast "
+                         "them apart and give pairs (gate, up)" % F2)
+    n = mx_blocked_bytes(F, K // 32)
+    s = sw_blk.view(-1)
+    return qw[:F], s[:n], qw[F:], s[n:]
+
+
+def matmul_swiglu(qx, sx_blk, qw, sw_blk, save=False, bits=8, stream=None):
+    """h = silu(g) u, g = X Wg^T, u = X Wu^T, of MX operands with elements of `bits` (8 or 4):
+    X (M, K), and either Wg and Wu (F, K) as pairs (gate, up) of bytes and of scales, or,
+    with F a multiple of 128, [Wg; Wu] (2F, K) in one.  Returns h (M, F), with save=True
+    (h, q0, s0_blk): [g | u] saved in 8 bits for the backward pass."""
+    if stream is not None:
+        with _on_stream(stream, qx):
+            return matmul_swiglu(qx, sx_blk, qw, sw_blk, save, bits)
+    if bits not in FORMATS:
+        raise ValueError("bits must be 8 or 4, got %r" % (bits,))
+    r = _compiled("matmul_swiglu", qx, sx_blk, qw, sw_blk, FORMATS[bits], save)
+    if r is not None:
+        return r
+    qg, sg, qu, su = _gate_and_up(qw, sw_blk, bits)
+    M, F = qx.shape[0], qg.shape[0]
+    h = torch.empty((M, F), dtype=torch.bfloat16, device=qx.device)
+    if not save:
+        mx_matmul_swiglu(qx, sx_blk, qg, sg, qu, su, h, bits=bits)
+        return h
+    q0 = torch.empty((M, 2 * F), dtype=torch.uint8, device=qx.device)
+    s0 = _u8(mx_blocked_bytes(M, 2 * F // 32), qx.device)
+    mx_matmul_swiglu(qx, sx_blk, qg, sg, qu, su, h, q0, s0, bits)
+    return h, q0, s0
+
+
+def matmul_swiglu_backward(qdy, sdy_blk, qw, sw_blk, saved, bits=8, stream=None):
+    """The gradient of [g | u] (M, 2F) from that of y = h W2^T: MX operands dY (M, K) and
+    W2^T (F, K) with elements of `bits`.  saved: bf16 [g | u], or the forward pass's pair
+    (q0, s0_blk)."""
+    if stream is not None:
+        with _on_stream(stream, qdy):
+            return matmul_swiglu_backward(qdy, sdy_blk, qw, sw_blk, saved, bits)
+    if bits not in FORMATS:
+        raise ValueError("bits must be 8 or 4, got %r" % (bits,))
+    r = _compiled("matmul_swiglu_backward", qdy, sdy_blk, qw, sw_blk, FORMATS[bits], saved)
+    if r is not None:
+        return r
+    gu, q0, s0 = _split_saved(saved)
+    dgu = torch.empty((qdy.shape[0], 2 * qw.shape[0]), dtype=torch.bfloat16, device=qdy.device)
+    mx_matmul_swiglu_backward(qdy, sdy_blk, qw, sw_blk, gu, q0, s0, dgu, bits)
+    return dgu
 
 
 def layer_norm(x, w, b=None, eps=1e-5, save=False, stream=None):

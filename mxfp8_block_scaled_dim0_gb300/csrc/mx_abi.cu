@@ -218,6 +218,68 @@ int cast_3d(const void* w, int64_t E, int64_t N, int64_t K, void* q0, void* s0_b
   return launch_rc(mx::launch_cast_experts(maps, E, N, K, q0, s0_blk, s1_blk, sms, st));
 }
 
+// Shared body of the MX-FP4 casts: null conventions as cast_3d.
+int cast_fp4(const void* x, int64_t M, int64_t K, void* q0, void* s0_blk, void* q1, void* s1_blk,
+             void* stream) {
+  if (!aligned(x, 16) || !aligned(q0, 16) || !aligned(s0_blk, 16) || !aligned(q1, 16) ||
+      !aligned(s1_blk, 16))
+    return MX_ERR_ALIGN;
+  if (int rc = check_device({x, q0, s0_blk, q1, s1_blk})) return rc;
+  mx::CastFp4Maps maps;
+  if (q1) {
+    if (int rc = encode_2d(&maps.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x, K, M, K * 2, 64, 128,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
+      return rc;
+    if (int rc = encode_2d(&maps.q1, CU_TENSOR_MAP_DATA_TYPE_UINT8, q1, M / 2, K, M / 2, 64, 128,
+                           CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_SWIZZLE_64B))
+      return rc;
+  }
+  int sms = 0;
+  if (int rc = current_sm_count(&sms)) return rc;
+  return launch_rc(mx::launch_cast_fp4(&maps, x, M, K, q0, s0_blk, s1_blk, sms,
+                                       static_cast<cudaStream_t>(stream)));
+}
+
+// The maps of a product's operand of `rows` stored by row: boxes of 128 bytes x `box` rows, and
+// of a stage's scale tiles x `tiles` row tiles.
+int encode_operand(CUtensorMap* q_map, CUtensorMap* s_map, const void* q, const void* s, int64_t rows,
+                   int64_t K, bool fp4, int box, int tiles) {
+  const int64_t row = fp4 ? K / 2 : K, tiles_k = cdiv(K, 128);
+  if (int rc = encode_2d(q_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, q, row, rows, row, 128,
+                         static_cast<uint32_t>(box), CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
+    return rc;
+  return encode_2d(s_map, CU_TENSOR_MAP_DATA_TYPE_UINT32, s, tiles_k * 128, cdiv(rows, 128),
+                   tiles_k * 512, fp4 ? 256 : 128, static_cast<uint32_t>(tiles),
+                   CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+// Results (M x N) in boxes of 128 bytes x 32 rows.
+int encode_result(CUtensorMap* m, const void* out, int64_t M, int64_t N, bool f32) {
+  return encode_2d(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, out,
+                   N, M, N * (f32 ? 4 : 2), f32 ? 32 : 64, 32, CU_TENSOR_MAP_L2_PROMOTION_NONE);
+}
+
+// The halves of rows [gate | up] of 2F values of `size` bytes: boxes of 64 bytes x 32 rows.
+int encode_halves(mx::ProductMaps* maps, const void* gu, int64_t M, int64_t F,
+                  CUtensorMapDataType type, int size) {
+  for (int i = 0; i < 2; ++i)
+    if (int rc = encode_2d(i ? &maps->up : &maps->gate, type,
+                           static_cast<const uint8_t*>(gu) + i * F * size, F, M, 2 * F * size,
+                           static_cast<uint32_t>(64 / size), 32, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_64B))
+      return rc;
+  return MX_OK;
+}
+
+int check_gated(int64_t M, int64_t F, int64_t K, int32_t format) {
+  if (format != MX_E4M3 && format != MX_E2M1) return MX_ERR_TYPE;
+  const int64_t step = format == MX_E2M1 ? 64 : 32;
+  if (M < 1 || F < 32 || K < step || F % 32 != 0 || K % step != 0 || M > kMaxDim || K > kMaxDim ||
+      F > mx::kSwigluMaxWidth)
+    return MX_ERR_SHAPE;
+  return MX_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -279,14 +341,23 @@ int mx_watchdog(int clear) {
   int n = 0;
   rc = mx::read_norm_watchdog(&n, clear != 0);
   if (rc) return cuda_fail(rc);
-  return v | w | d | m | n;
+  int f[3] = {0, 0, 0};
+  rc = mx::read_fp4_watchdog(&f[0], clear != 0);
+  if (rc) return cuda_fail(rc);
+  rc = mx::read_matmul_fp4_watchdog(&f[1], clear != 0);
+  if (rc) return cuda_fail(rc);
+  rc = mx::read_matmul_swiglu_watchdog(&f[2], clear != 0);
+  if (rc) return cuda_fail(rc);
+  return v | w | d | m | n | f[0] | f[1] | f[2];
 }
 
 int mx_bounds_check(int clear) {
   const int parts[] = {mx::out_of_bounds_cast(clear != 0), mx::out_of_bounds_blocked(clear != 0),
                        mx::out_of_bounds_dequant(clear != 0), mx::out_of_bounds_scaled(clear != 0),
                        mx::out_of_bounds_matmul(clear != 0), mx::out_of_bounds_norm(clear != 0),
-                       mx::out_of_bounds_swiglu(clear != 0)};
+                       mx::out_of_bounds_swiglu(clear != 0), mx::out_of_bounds_fp4(clear != 0),
+                       mx::out_of_bounds_matmul_fp4(clear != 0),
+                       mx::out_of_bounds_matmul_swiglu(clear != 0)};
   int sum = 0;
   for (int v : parts) {
     if (v == -1) return -1;                     // release build: no checks compiled in
@@ -546,6 +617,131 @@ int mx_swiglu_backward(const void* dh, const void* gu, const void* q0, const voi
   if (int rc = current_sm_count(&sms)) return rc;
   const mx::SwigluArgs a = {gu, dh, dgu, const_cast<void*>(q0), const_cast<void*>(s0_blk), M, F};
   return launch_rc(mx::launch_swiglu_backward(a, sms, static_cast<cudaStream_t>(stream)));
+}
+
+int mx_cast_fp4_dim0(const void* x, int64_t M, int64_t K, void* q0, void* s0_blk, void* stream) {
+  if (!x || !q0 || !s0_blk) return MX_ERR_NULL;
+  if (M < 1 || K < 32 || K % 32 != 0 || M > kMaxDim || K > kMaxDim) return MX_ERR_SHAPE;
+  return cast_fp4(x, M, K, q0, s0_blk, nullptr, nullptr, stream);
+}
+
+int mx_cast_fp4_dim1(const void* x, int64_t M, int64_t K, void* q1, void* s1_blk, void* stream) {
+  if (!x || !q1 || !s1_blk) return MX_ERR_NULL;
+  if (int rc = check_2d_shape(M, K)) return rc;
+  return cast_fp4(x, M, K, nullptr, nullptr, q1, s1_blk, stream);
+}
+
+int mx_cast_fp4_dim0_dim1(const void* x, int64_t M, int64_t K, void* q0, void* s0_blk, void* q1,
+                          void* s1_blk, void* stream) {
+  if (!x || !q0 || !s0_blk || !q1 || !s1_blk) return MX_ERR_NULL;
+  if (int rc = check_2d_shape(M, K)) return rc;
+  return cast_fp4(x, M, K, q0, s0_blk, q1, s1_blk, stream);
+}
+
+int mx_dequant_fp4(const void* q, int64_t R, int64_t C, const void* s_blk, void* out, void* stream) {
+  if (!q || !s_blk || !out) return MX_ERR_NULL;
+  if (R < 1 || C < 32 || R > kMaxDim || C > kMaxDim || C % 32 != 0) return MX_ERR_SHAPE;
+  if (!aligned(q, 16) || !aligned(s_blk, 16) || !aligned(out, 16)) return MX_ERR_ALIGN;
+  if (int rc = check_device({q, s_blk, out})) return rc;
+  int sms = 0;
+  if (int rc = current_sm_count(&sms)) return rc;
+  return launch_rc(mx::launch_dequant_fp4(q, R, C, s_blk, out, sms, static_cast<cudaStream_t>(stream)));
+}
+
+int mx_matmul_fp4(const void* qa, const void* sa_blk, const void* qb, const void* sb_blk, int64_t M,
+                  int64_t N, int64_t K, void* out, int32_t out_type, void* stream) {
+  if (!qa || !sa_blk || !qb || !sb_blk || !out) return MX_ERR_NULL;
+  if (out_type != MX_BF16 && out_type != MX_F32) return MX_ERR_TYPE;
+  if (M < 1 || N < 1 || K < 64 || K % 64 != 0 || M > kMaxDim || N > kMaxDim || K > kMaxDim)
+    return MX_ERR_SHAPE;
+  if (!aligned(qa, 16) || !aligned(sa_blk, 16) || !aligned(qb, 16) || !aligned(sb_blk, 16) ||
+      !aligned(out, 16))
+    return MX_ERR_ALIGN;
+  if (int rc = check_device({qa, sa_blk, qb, sb_blk, out})) return rc;
+  int sms = 0;
+  if (int rc = current_sm_count(&sms)) return rc;
+  const bool f32 = out_type == MX_F32, pairs = mx::matmul_pairs(M, N, sms);
+  const int cols = mx::matmul_fp4_tile_cols(M, N, K, sms);
+  mx::ProductMaps maps;
+  if (int rc = encode_operand(&maps.a, &maps.sa, qa, sa_blk, M, K, true,
+                              pairs ? 128 : mx::matmul_box_rows(M, false, 128), 1))
+    return rc;
+  if (int rc = encode_operand(&maps.b, &maps.sb, qb, sb_blk, N, K, true,
+                              pairs ? 128 : mx::matmul_box_rows(N, false, cols), pairs ? 2 : 1))
+    return rc;
+  maps.b2 = maps.sb2 = maps.gate = maps.up = maps.a;      // not read
+  if (!mx::matmul_mapped(N, f32)) {
+    maps.out = maps.a;
+  } else if (int rc = encode_result(&maps.out, out, M, N, f32)) {
+    return rc;
+  }
+  return launch_rc(
+      mx::launch_matmul_fp4(maps, M, N, K, out, f32, sms, static_cast<cudaStream_t>(stream)));
+}
+
+int mx_matmul_swiglu(const void* qx, const void* sx_blk, const void* qg, const void* sg_blk,
+                     const void* qu, const void* su_blk, int64_t M, int64_t F, int64_t K,
+                     int32_t format, void* h, void* q0, void* s0_blk, void* stream) {
+  if (!qx || !sx_blk || !qg || !sg_blk || !qu || !su_blk || !h || !q0 != !s0_blk) return MX_ERR_NULL;
+  if (int rc = check_gated(M, F, K, format)) return rc;
+  if (!aligned(qx, 16) || !aligned(sx_blk, 16) || !aligned(qg, 16) || !aligned(sg_blk, 16) ||
+      !aligned(qu, 16) || !aligned(su_blk, 16) || !aligned(h, 16) || !aligned(q0, 16) ||
+      !aligned(s0_blk, 16))
+    return MX_ERR_ALIGN;
+  if (int rc = check_device({qx, sx_blk, qg, sg_blk, qu, su_blk, h, q0, s0_blk})) return rc;
+  int sms = 0;
+  if (int rc = current_sm_count(&sms)) return rc;
+  const bool fp4 = format == MX_E2M1, pairs = mx::matmul_pairs(M, 2 * F, sms);
+  mx::ProductMaps maps;
+  if (int rc = encode_operand(&maps.a, &maps.sa, qx, sx_blk, M, K, fp4,
+                              pairs ? 128 : mx::matmul_box_rows(M, false, 128), 1))
+    return rc;
+  if (int rc = encode_operand(&maps.b, &maps.sb, qg, sg_blk, F, K, fp4, pairs ? 128 : 64, 1)) return rc;
+  if (int rc = encode_operand(&maps.b2, &maps.sb2, qu, su_blk, F, K, fp4, pairs ? 128 : 64, 1))
+    return rc;
+  if (int rc = encode_result(&maps.out, h, M, F, false)) return rc;
+  maps.gate = maps.up = maps.out;
+  if (q0) {
+    if (int rc = encode_halves(&maps, q0, M, F, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1)) return rc;
+    if (M % 128 != 0 || F % 64 != 0) {
+      // The kernel writes the scales that there are; the padding is cleared first.
+      const cudaError_t e =
+          cudaMemsetAsync(s0_blk, 0, static_cast<size_t>(mx_blocked_bytes(M, 2 * F / 32)),
+                          static_cast<cudaStream_t>(stream));
+      if (e != cudaSuccess) return cuda_fail(static_cast<int>(e));
+    }
+  }
+  const mx::MatmulSwigluArgs a = {M, F, K, fp4, h, q0, s0_blk, nullptr};
+  return launch_rc(mx::launch_matmul_swiglu(maps, a, sms, static_cast<cudaStream_t>(stream)));
+}
+
+int mx_matmul_swiglu_backward(const void* qdy, const void* sdy_blk, const void* qw,
+                              const void* sw_blk, int64_t M, int64_t F, int64_t K, int32_t format,
+                              const void* gu, const void* q0, const void* s0_blk, void* dgu,
+                              void* stream) {
+  if (!qdy || !sdy_blk || !qw || !sw_blk || !dgu || !q0 != !s0_blk || !gu == !q0) return MX_ERR_NULL;
+  if (int rc = check_gated(M, F, K, format)) return rc;
+  if (!aligned(qdy, 16) || !aligned(sdy_blk, 16) || !aligned(qw, 16) || !aligned(sw_blk, 16) ||
+      !aligned(gu, 16) || !aligned(q0, 16) || !aligned(s0_blk, 16) || !aligned(dgu, 16))
+    return MX_ERR_ALIGN;
+  if (int rc = check_device({qdy, sdy_blk, qw, sw_blk, gu, q0, s0_blk, dgu})) return rc;
+  int sms = 0;
+  if (int rc = current_sm_count(&sms)) return rc;
+  const bool fp4 = format == MX_E2M1, pairs = mx::matmul_pairs(M, F, sms);
+  const int cols = mx::matmul_swiglu_back_tile_cols(M, F, K, fp4, sms);
+  mx::ProductMaps maps;
+  if (int rc = encode_operand(&maps.a, &maps.sa, qdy, sdy_blk, M, K, fp4,
+                              pairs ? 128 : mx::matmul_box_rows(M, false, 128), 1))
+    return rc;
+  if (int rc = encode_operand(&maps.b, &maps.sb, qw, sw_blk, F, K, fp4,
+                              pairs ? 128 : mx::matmul_box_rows(F, false, cols), pairs ? 2 : 1))
+    return rc;
+  if (int rc = encode_halves(&maps, dgu, M, F, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2)) return rc;
+  maps.b2 = maps.sb2 = maps.out = maps.gate;      // not read
+  const mx::MatmulSwigluArgs a = {M, F, K, fp4, dgu, const_cast<void*>(q0), const_cast<void*>(s0_blk),
+                                  gu};
+  return launch_rc(
+      mx::launch_matmul_swiglu_backward(maps, a, sms, static_cast<cudaStream_t>(stream)));
 }
 
 int mx_scales_to_blocked(const void* s, int64_t R, int64_t C, void* out, void* stream) {

@@ -126,6 +126,50 @@ bool matmul_pairs(int64_t M, int64_t N, int num_sms);
 int launch_matmul(const MatmulMaps& maps, int64_t M, int64_t N, int64_t K, bool a_mn, bool b_mn,
                   void* out, bool out_f32, int num_sms, cudaStream_t stream);
 int read_matmul_watchdog(int* out, bool clear);
+// Products with 4-bit operands (mx_matmul_fp4.cu) or joined with the gated SiLU
+// (mx_matmul_swiglu.cu), both by the kernels of mx_product.cuh.  a, b, sa, sb: as in
+// MatmulMaps, a stage's scales (two 512-byte tiles for 4-bit operands) a box.  The forward
+// gated product: b, sb gate and b2, sb2 up, in boxes of 128 rows (pairs) or 64 and of one
+// row tile.  out: as in MatmulMaps, bf16 boxes for the gated product.  gate, up: the
+// halves of the rows [gate | up]: boxes of 64 bytes x 32 rows, 64B swizzle, of the saved
+// bytes (forward) or of the gradient in bf16 (backward).
+struct ProductMaps {
+  CUtensorMap a, b, sa, sb, b2, sb2, out, gate, up;
+};
+int matmul_fp4_tile_cols(int64_t M, int64_t N, int64_t K, int num_sms);
+int launch_matmul_fp4(const ProductMaps& maps, int64_t M, int64_t N, int64_t K, void* out,
+                      bool out_f32, int num_sms, cudaStream_t stream);
+int read_matmul_fp4_watchdog(int* out, bool clear);
+int out_of_bounds_matmul_fp4(bool clear);
+// Forward: out = h, [gate | up] saved into q, s unless null.  Backward: gu, or q, s ->
+// out = the gradient of [gate | up].
+struct MatmulSwigluArgs {
+  int64_t M, F, K;
+  bool fp4;
+  void* out;
+  void* q;
+  void* s;
+  const void* gu;
+};
+int matmul_swiglu_back_tile_cols(int64_t M, int64_t F, int64_t K, bool fp4, int num_sms);
+int launch_matmul_swiglu(const ProductMaps& maps, const MatmulSwigluArgs& a, int num_sms,
+                         cudaStream_t stream);
+int launch_matmul_swiglu_backward(const ProductMaps& maps, const MatmulSwigluArgs& a, int num_sms,
+                                  cudaStream_t stream);
+int read_matmul_swiglu_watchdog(int* out, bool clear);
+int out_of_bounds_matmul_swiglu(bool clear);
+// MX-FP4 casts and dequantisation (mx_fp4.cu).  q0 / s0 null: dim1 only; q1 / s1 null:
+// dim0 only, which needs no maps.  x: boxes of 64 columns x 128 rows, 128B swizzle; q1: boxes
+// of 64 bytes x 128 rows, 64B swizzle.
+struct CastFp4Maps {
+  CUtensorMap x, q1;
+};
+int launch_cast_fp4(const CastFp4Maps* maps, const void* x, int64_t M, int64_t K, void* q0, void* s0,
+                    void* s1, int num_sms, cudaStream_t stream);
+int launch_dequant_fp4(const void* q, int64_t R, int64_t C, const void* s_blk, void* out, int num_sms,
+                       cudaStream_t stream);
+int read_fp4_watchdog(int* out, bool clear);
+int out_of_bounds_fp4(bool clear);
 // Layer norm (mx_norm.cu).  q / s null: the input is not saved; b null: no bias.
 struct LayerNormArgs {
   const void* x;

@@ -1,0 +1,44 @@
+// mx_matmul_fp4.cu -- the product of two MX-FP4 operands (e2m1, blocks of 32, e8m0 scales):
+// the kernels of mx_product.cuh with results in bf16 or fp32.
+#include "mx_product.cuh"
+
+namespace mx {
+
+int launch_matmul_fp4(const ProductMaps& maps, int64_t M, int64_t N, int64_t K, void* out,
+                      bool out_f32, int num_sms, cudaStream_t stream) {
+  ProductParams p = product_params(M, N, K, true);
+  p.out = out;
+  p.out_f32 = out_f32;
+  p.mapped = matmul_mapped(N, out_f32);
+  p.sp_out = make_span(out, static_cast<uint64_t>(M) * static_cast<uint64_t>(N) * (out_f32 ? 4 : 2));
+  // Longer fp32 sums go in runs of at most 4096 steps.
+  constexpr int kRun = 16;
+  if (matmul_pairs(M, N, num_sms)) {
+    p.m_tiles = static_cast<int>((M + 255) / 256);
+    p.n_tiles = static_cast<int>((N + 255) / 256);
+    if (!out_f32) return launch_pair_kernel<true, kPlain, false>(maps, p, num_sms, stream);
+    const int runs = (p.k_blocks + kRun - 1) / kRun;
+    p.run = (p.k_blocks + runs - 1) / runs;
+    return launch_pair_kernel<true, kPlain, true>(maps, p, num_sms, stream);
+  }
+  const TileChoice t = choose_tiles(M, N, p.k_blocks, num_sms);
+  p.cols = t.cols;
+  p.split = t.split;
+  p.m_tiles = static_cast<int>((M + 127) / 128);
+  p.n_tiles = static_cast<int>((N + t.cols - 1) / t.cols);
+  p.load_bytes = (matmul_box_rows(M, false, 128) + matmul_box_rows(N, false, t.cols)) * kBoxCols +
+                 2 * Shape<true, kPlain>::kSf * kSfBytes;
+  p.run = kRun;
+  return out_f32 && (p.k_blocks + p.split - 1) / p.split > kRun
+             ? launch_tile_kernel<true, kPlain, true>(maps, p, stream)
+             : launch_tile_kernel<true, kPlain, false>(maps, p, stream);
+}
+
+int matmul_fp4_tile_cols(int64_t M, int64_t N, int64_t K, int num_sms) {
+  return choose_tiles(M, N, (K + 255) / 256, num_sms).cols;
+}
+
+int out_of_bounds_matmul_fp4(bool clear) { return read_out_of_bounds(clear); }
+int read_matmul_fp4_watchdog(int* out, bool clear) { return read_product_word(out, clear); }
+
+}  // namespace mx

@@ -209,6 +209,12 @@ __device__ __forceinline__ uint32_t mxf8_idesc_step(uint32_t idesc, int k) {
   return idesc | (static_cast<uint32_t>(k) << 4) | (static_cast<uint32_t>(k) << 29);
 }
 
+// ... of a kind::mxf4 product: both operands e2m1, K-major, scales ue8m0.
+__device__ __forceinline__ uint32_t mxf4_idesc(int m, int n) {
+  return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | (1u << 23) |
+         (static_cast<uint32_t>(m >> 4) << 24);
+}
+
 // ---- block-scaled products -------------------------------------------------------
 
 // 512-byte scale tile -> four tensor-memory columns, repeated for the four
@@ -238,6 +244,28 @@ __device__ __forceinline__ void mma_mxf8(uint32_t d, uint64_t da, uint64_t db, u
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
         "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X "
+        "[%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(da), "l"(db), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
+        : "memory");
+}
+
+// The same for 4-bit operands: 64 contraction steps (32 bytes a row), two scales a row and
+// 64 steps.
+template <int CG>
+__device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t da, uint64_t db, uint32_t idesc,
+                                         uint32_t sfa, uint32_t sfb, bool accumulate) {
+  const uint32_t acc = accumulate ? 1u : 0u;
+  if (CG == 1)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X "
+        "[%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(da), "l"(db), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X "
         "[%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
         "l"(da), "l"(db), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
         : "memory");

@@ -1,4 +1,4 @@
-// torch_call.cpp -- the allocating wrappers of the training operators, and of the 2D
+// torch_call.cpp -- the allocating wrappers of the operators on MX operands, and of the 2D
 // casts whose outputs they take, as plain CPython functions: they look the arguments
 // over, allocate the outputs with torch's allocator and call the C ABI on torch's
 // current stream.
@@ -33,6 +33,7 @@ using at::ScalarType;
 using at::Tensor;
 
 constexpr int kBF16 = 0, kF32 = 1;           // MX_BF16, MX_F32
+constexpr int kE2M1 = 1;                     // MX_E2M1
 
 template <typename F>
 F address(PyObject* o) {
@@ -275,8 +276,8 @@ PyObject* swiglu_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// cast_dim0(fn, x), cast_dim1(fn, x): one direction's bytes and scales.
-template <bool DIM1>
+// cast_dim0(fn, x), cast_dim1(fn, x): one direction's bytes and scales; PER elements to a byte.
+template <bool DIM1, int PER>
 PyObject* cast(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   if (n != 2) Py_RETURN_NONE;
@@ -286,13 +287,14 @@ PyObject* cast(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int64_t M = x->size(0), K = x->size(1), R = DIM1 ? K : M, C = DIM1 ? M : K;
   const int dev = common_device({x});
   if (dev < 0) Py_RETURN_NONE;
-  Tensor q = empty({R, C}, at::kByte, dev), s = empty({blocked_bytes(R, C / 32)}, at::kByte, dev);
+  Tensor q = empty({R, C / PER}, at::kByte, dev), s = empty({blocked_bytes(R, C / 32)}, at::kByte, dev);
   const int rc = unlocked(address<Fn>(a[0]), ptr(x), M, K, q.data_ptr(), s.data_ptr(), stream(dev));
   return rc ? PyLong_FromLong(rc) : wrapped({q, s});
   END_HANDLE_TH_ERRORS
 }
 
 // cast_dim0_dim1(fn, x)
+template <int PER>
 PyObject* cast_both(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   if (n != 2) Py_RETURN_NONE;
@@ -302,30 +304,159 @@ PyObject* cast_both(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int64_t M = x->size(0), K = x->size(1);
   const int dev = common_device({x});
   if (dev < 0) Py_RETURN_NONE;
-  Tensor q0 = empty({M, K}, at::kByte, dev), s0 = empty({blocked_bytes(M, K / 32)}, at::kByte, dev),
-         q1 = empty({K, M}, at::kByte, dev), s1 = empty({blocked_bytes(K, M / 32)}, at::kByte, dev);
+  Tensor q0 = empty({M, K / PER}, at::kByte, dev),
+         s0 = empty({blocked_bytes(M, K / 32)}, at::kByte, dev),
+         q1 = empty({K, M / PER}, at::kByte, dev),
+         s1 = empty({blocked_bytes(K, M / 32)}, at::kByte, dev);
   const int rc = unlocked(address<Fn>(a[0]), ptr(x), M, K, q0.data_ptr(), s0.data_ptr(),
                           q1.data_ptr(), s1.data_ptr(), stream(dev));
   return rc ? PyLong_FromLong(rc) : wrapped({q0, s0, q1, s1});
   END_HANDLE_TH_ERRORS
 }
 
+// An MX operand stored by row, with its scales: its rows and steps.
+bool by_row(const Tensor* q, const Tensor* s, bool fp4, int64_t* rows, int64_t* steps) {
+  if (!q || q->dim() != 2 || !plain(*q) ||
+      !(fp4 ? q->scalar_type() == at::kByte : is_bytes(q->scalar_type())))
+    return false;
+  *rows = q->size(0);
+  *steps = q->size(1) * (fp4 ? 2 : 1);
+  return holds_bytes(s, blocked_bytes(*rows, *steps / 32));
+}
+
+// dequant_fp4(fn, q, s)
+PyObject* dequant_fp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 3) Py_RETURN_NONE;
+  using Fn = int (*)(const void*, int64_t, int64_t, const void*, void*, void*);
+  const Tensor *q = tensor(a[1]), *s = tensor(a[2]);
+  int64_t R = 0, C = 0;
+  if (!by_row(q, s, true, &R, &C)) Py_RETURN_NONE;
+  const int dev = common_device({q, s});
+  if (dev < 0) Py_RETURN_NONE;
+  Tensor out = empty({R, C}, at::kBFloat16, dev);
+  const int rc = unlocked(address<Fn>(a[0]), ptr(q), R, C, ptr(s), out.data_ptr(), stream(dev));
+  return rc ? PyLong_FromLong(rc) : THPVariable_Wrap(out);
+  END_HANDLE_TH_ERRORS
+}
+
+// matmul_fp4(fn, qa, sa, qb, sb, out_type)
+PyObject* matmul_fp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 6) Py_RETURN_NONE;
+  using Fn = int (*)(const void*, const void*, const void*, const void*, int64_t, int64_t, int64_t,
+                     void*, int32_t, void*);
+  const Tensor *qa = tensor(a[1]), *sa = tensor(a[2]), *qb = tensor(a[3]), *sb = tensor(a[4]);
+  const long type = PyLong_AsLong(a[5]);
+  int64_t M = 0, N = 0, K = 0, Kb = 0;
+  if (!by_row(qa, sa, true, &M, &K) || !by_row(qb, sb, true, &N, &Kb) || K != Kb) Py_RETURN_NONE;
+  const int dev = common_device({qa, sa, qb, sb});
+  if (dev < 0) Py_RETURN_NONE;
+  Tensor out = empty({M, N}, type == kF32 ? at::kFloat : at::kBFloat16, dev);
+  const int rc = unlocked(address<Fn>(a[0]), ptr(qa), ptr(sa), ptr(qb), ptr(sb), M, N, K,
+                          out.data_ptr(), static_cast<int32_t>(type), stream(dev));
+  return rc ? PyLong_FromLong(rc) : THPVariable_Wrap(out);
+  END_HANDLE_TH_ERRORS
+}
+
+// matmul_swiglu(fn, qx, sx, qw, sw, format, save): qw and sw tensors, or pairs (gate, up)
+PyObject* matmul_swiglu(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 7) Py_RETURN_NONE;
+  using Fn = int (*)(const void*, const void*, const void*, const void*, const void*, const void*,
+                     int64_t, int64_t, int64_t, int32_t, void*, void*, void*, void*);
+  const Tensor *qx = tensor(a[1]), *sx = tensor(a[2]), *qg = tensor(a[3]), *sg = tensor(a[4]),
+               *qu = nullptr, *su = nullptr;
+  const long format = PyLong_AsLong(a[5]);
+  const bool save = a[6] == Py_True, fp4 = format == kE2M1;
+  int64_t M = 0, F = 0, Fu = 0, K = 0, Kg = 0, Ku = 0;
+  if (!by_row(qx, sx, fp4, &M, &K) || !is_bool(a[6])) Py_RETURN_NONE;
+  if (!qg) {
+    if (!PyTuple_CheckExact(a[3]) || PyTuple_GET_SIZE(a[3]) != 2 || !PyTuple_CheckExact(a[4]) ||
+        PyTuple_GET_SIZE(a[4]) != 2)
+      Py_RETURN_NONE;
+    qg = tensor(PyTuple_GET_ITEM(a[3], 0));
+    qu = tensor(PyTuple_GET_ITEM(a[3], 1));
+    sg = tensor(PyTuple_GET_ITEM(a[4], 0));
+    su = tensor(PyTuple_GET_ITEM(a[4], 1));
+    if (!by_row(qu, su, fp4, &Fu, &Ku)) Py_RETURN_NONE;
+  }
+  if (!by_row(qg, sg, fp4, &F, &Kg) || K != Kg) Py_RETURN_NONE;
+  if (qu) {
+    if (F != Fu || K != Ku) Py_RETURN_NONE;
+  } else {
+    if (F % 256 != 0) Py_RETURN_NONE;
+    F /= 2;
+  }
+  const int dev = common_device({qx, sx, qg, sg, qu, su});
+  if (dev < 0) Py_RETURN_NONE;
+  const char *g = static_cast<const char*>(ptr(qg)), *gs = static_cast<const char*>(ptr(sg));
+  const void* u = qu ? ptr(qu) : g + F * qg->size(1);
+  const void* us = qu ? ptr(su) : gs + blocked_bytes(F, K / 32);
+  Tensor h = empty({M, F}, at::kBFloat16, dev), q, s;
+  if (save) {
+    q = empty({M, 2 * F}, at::kByte, dev);
+    s = empty({blocked_bytes(M, 2 * F / 32)}, at::kByte, dev);
+  }
+  const int rc = unlocked(address<Fn>(a[0]), ptr(qx), ptr(sx), g, gs, u, us, M, F, K,
+                          static_cast<int32_t>(format), h.data_ptr(), save ? q.data_ptr() : nullptr,
+                          save ? s.data_ptr() : nullptr, stream(dev));
+  if (rc) return PyLong_FromLong(rc);
+  return save ? wrapped({h, q, s}) : THPVariable_Wrap(h);
+  END_HANDLE_TH_ERRORS
+}
+
+// matmul_swiglu_backward(fn, qdy, sdy, qw, sw, format, gu or (q0, s0_blk))
+PyObject* matmul_swiglu_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 7) Py_RETURN_NONE;
+  using Fn = int (*)(const void*, const void*, const void*, const void*, int64_t, int64_t, int64_t,
+                     int32_t, const void*, const void*, const void*, void*, void*);
+  const Tensor *qdy = tensor(a[1]), *sdy = tensor(a[2]), *qw = tensor(a[3]), *sw = tensor(a[4]),
+               *gu = tensor(a[6]), *q = nullptr, *s = nullptr;
+  const long format = PyLong_AsLong(a[5]);
+  const bool fp4 = format == kE2M1;
+  int64_t M = 0, F = 0, K = 0, Kw = 0;
+  if (!by_row(qdy, sdy, fp4, &M, &K) || !by_row(qw, sw, fp4, &F, &Kw) || K != Kw) Py_RETURN_NONE;
+  if (gu) {
+    if (!is_2d(gu, at::kBFloat16, M, 2 * F)) Py_RETURN_NONE;
+  } else {
+    if (!PyTuple_CheckExact(a[6]) || PyTuple_GET_SIZE(a[6]) != 2) Py_RETURN_NONE;
+    q = tensor(PyTuple_GET_ITEM(a[6], 0));
+    s = tensor(PyTuple_GET_ITEM(a[6], 1));
+    if (!holds_bytes(q, 2 * M * F) || !holds_bytes(s, blocked_bytes(M, 2 * F / 32))) Py_RETURN_NONE;
+  }
+  const int dev = common_device({qdy, sdy, qw, sw, gu, q, s});
+  if (dev < 0) Py_RETURN_NONE;
+  Tensor out = empty({M, 2 * F}, at::kBFloat16, dev);
+  const int rc = unlocked(address<Fn>(a[0]), ptr(qdy), ptr(sdy), ptr(qw), ptr(sw), M, F, K,
+                          static_cast<int32_t>(format), ptr(gu), ptr(q), ptr(s), out.data_ptr(),
+                          stream(dev));
+  return rc ? PyLong_FromLong(rc) : THPVariable_Wrap(out);
+  END_HANDLE_TH_ERRORS
+}
+
+// A method of this name's C function.
+PyMethodDef method(const char* name, PyObject* (*f)(PyObject*, PyObject* const*, Py_ssize_t)) {
+  return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(f)), METH_FASTCALL, nullptr};
+}
+
 PyMethodDef kMethods[] = {
-    {"cast_dim0", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(cast<false>)), METH_FASTCALL,
-     nullptr},
-    {"cast_dim1", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(cast<true>)), METH_FASTCALL,
-     nullptr},
-    {"cast_dim0_dim1", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(cast_both)),
-     METH_FASTCALL, nullptr},
-    {"matmul", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(matmul)), METH_FASTCALL, nullptr},
-    {"layer_norm", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(layer_norm)), METH_FASTCALL,
-     nullptr},
-    {"layer_norm_backward",
-     reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(layer_norm_backward)), METH_FASTCALL,
-     nullptr},
-    {"swiglu", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(swiglu)), METH_FASTCALL, nullptr},
-    {"swiglu_backward", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(swiglu_backward)),
-     METH_FASTCALL, nullptr},
+    method("cast_dim0", cast<false, 1>),
+    method("cast_dim1", cast<true, 1>),
+    method("cast_dim0_dim1", cast_both<1>),
+    method("cast_fp4_dim0", cast<false, 2>),
+    method("cast_fp4_dim1", cast<true, 2>),
+    method("cast_fp4_dim0_dim1", cast_both<2>),
+    method("dequant_fp4", dequant_fp4),
+    method("matmul", matmul),
+    method("matmul_fp4", matmul_fp4),
+    method("matmul_swiglu", matmul_swiglu),
+    method("matmul_swiglu_backward", matmul_swiglu_backward),
+    method("layer_norm", layer_norm),
+    method("layer_norm_backward", layer_norm_backward),
+    method("swiglu", swiglu),
+    method("swiglu_backward", swiglu_backward),
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_torch_call", nullptr, -1, kMethods,

@@ -226,10 +226,11 @@ int cast_fp4(const void* x, int64_t M, int64_t K, void* q0, void* s0_blk, void* 
     return MX_ERR_ALIGN;
   if (int rc = check_device({x, q0, s0_blk, q1, s1_blk})) return rc;
   mx::CastFp4Maps maps;
+  if (int rc = encode_2d(&maps.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x, K, M, K * 2, 64, 128,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
+    return rc;
+  maps.q1 = maps.x;
   if (q1) {
-    if (int rc = encode_2d(&maps.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x, K, M, K * 2, 64, 128,
-                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
-      return rc;
     if (int rc = encode_2d(&maps.q1, CU_TENSOR_MAP_DATA_TYPE_UINT8, q1, M / 2, K, M / 2, 64, 128,
                            CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_SWIZZLE_64B))
       return rc;
@@ -645,7 +646,14 @@ int mx_dequant_fp4(const void* q, int64_t R, int64_t C, const void* s_blk, void*
   if (int rc = check_device({q, s_blk, out})) return rc;
   int sms = 0;
   if (int rc = current_sm_count(&sms)) return rc;
-  return launch_rc(mx::launch_dequant_fp4(q, R, C, s_blk, out, sms, static_cast<cudaStream_t>(stream)));
+  mx::DequantFp4Maps maps;
+  if (int rc = encode_2d(&maps.q, CU_TENSOR_MAP_DATA_TYPE_UINT8, q, C / 2, R, C / 2, 64, 128,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_SWIZZLE_NONE))
+    return rc;
+  if (int rc = encode_2d(&maps.out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, out, C, R, 2 * C, 64, 128,
+                         CU_TENSOR_MAP_L2_PROMOTION_NONE))
+    return rc;
+  return launch_rc(mx::launch_dequant_fp4(maps, q, R, C, s_blk, out, sms, static_cast<cudaStream_t>(stream)));
 }
 
 int mx_matmul_fp4(const void* qa, const void* sa_blk, const void* qb, const void* sb_blk, int64_t M,
@@ -660,7 +668,7 @@ int mx_matmul_fp4(const void* qa, const void* sa_blk, const void* qb, const void
   if (int rc = check_device({qa, sa_blk, qb, sb_blk, out})) return rc;
   int sms = 0;
   if (int rc = current_sm_count(&sms)) return rc;
-  const bool f32 = out_type == MX_F32, pairs = mx::matmul_pairs(M, N, sms);
+  const bool f32 = out_type == MX_F32, pairs = mx::product_pairs(M, N, sms);
   const int cols = mx::matmul_fp4_tile_cols(M, N, K, sms);
   mx::ProductMaps maps;
   if (int rc = encode_operand(&maps.a, &maps.sa, qa, sa_blk, M, K, true,
@@ -691,7 +699,7 @@ int mx_matmul_swiglu(const void* qx, const void* sx_blk, const void* qg, const v
   if (int rc = check_device({qx, sx_blk, qg, sg_blk, qu, su_blk, h, q0, s0_blk})) return rc;
   int sms = 0;
   if (int rc = current_sm_count(&sms)) return rc;
-  const bool fp4 = format == MX_E2M1, pairs = mx::matmul_pairs(M, 2 * F, sms);
+  const bool fp4 = format == MX_E2M1, pairs = mx::product_pairs(M, 2 * F, sms);
   mx::ProductMaps maps;
   if (int rc = encode_operand(&maps.a, &maps.sa, qx, sx_blk, M, K, fp4,
                               pairs ? 128 : mx::matmul_box_rows(M, false, 128), 1))
@@ -727,7 +735,7 @@ int mx_matmul_swiglu_backward(const void* qdy, const void* sdy_blk, const void* 
   if (int rc = check_device({qdy, sdy_blk, qw, sw_blk, gu, q0, s0_blk, dgu})) return rc;
   int sms = 0;
   if (int rc = current_sm_count(&sms)) return rc;
-  const bool fp4 = format == MX_E2M1, pairs = mx::matmul_pairs(M, F, sms);
+  const bool fp4 = format == MX_E2M1, pairs = mx::product_pairs(M, F, sms);
   const int cols = mx::matmul_swiglu_back_tile_cols(M, F, K, fp4, sms);
   mx::ProductMaps maps;
   if (int rc = encode_operand(&maps.a, &maps.sa, qdy, sdy_blk, M, K, fp4,

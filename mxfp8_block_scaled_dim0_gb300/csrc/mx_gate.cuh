@@ -8,7 +8,7 @@
 // (a few units of 2^-22) is far below the rounding of the results to 16 or 8 bits.
 #pragma once
 
-#include "mx_common.cuh"
+#include "mx_rows.cuh"
 
 namespace mx {
 
@@ -48,9 +48,85 @@ __device__ __forceinline__ void gated_back(float d, float g, float u, float& dg,
   }
 }
 
-// h of any gate.
-__device__ __forceinline__ float gated(float g, float u) {
-  return g < kLow ? low_gated(g, u) : g * sigmoid(g) * u;
+__device__ __forceinline__ f32x2 sigmoid2(f32x2 g) {
+  float lo, hi;
+  unpair(g, lo, hi);
+  return pair(sigmoid(lo), sigmoid(hi));
+}
+
+// The largest of words of two bf16 gates each, halves apart.  As unsigned numbers the
+// negative ones lie above the positive ones, in order of their size.
+__device__ __forceinline__ uint32_t lowest2(const uint4& w) {
+  return __vmaxu2(__vmaxu2(w.x, w.y), __vmaxu2(w.z, w.w));
+}
+__device__ __forceinline__ bool any_low(uint32_t lowest) {
+  constexpr uint32_t kBits = 0xC2A0u << 16;              // kLow
+  return lowest > (kBits | 0xFFFFu) || lowest << 16 > kBits;
+}
+
+// Whether a block with this scale byte can hold a gate below kLow: at 2^-3 its largest
+// magnitude, 448, stands for 56.
+__device__ __forceinline__ bool may_be_low(uint32_t sbyte) { return sbyte >= 127 - 2; }
+
+// The products' epilogues take the sigmoid of no less than kLow, which leaves the results of
+// low gates to be multiplied by this twice (1 for other gates), if there are any: no second
+// copy of the formulas in the code.
+__device__ __forceinline__ f32x2 low_factor2(f32x2 g) {
+  constexpr float kHalf = 0.5f * 1.4426950408889634f;
+  float lo, hi;
+  unpair(g, lo, hi);
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(lo) : "f"((fminf(lo, kLow) - kLow) * kHalf));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(hi) : "f"((fminf(hi, kLow) - kLow) * kHalf));
+  return pair(lo, hi);
+}
+
+__device__ __forceinline__ f32x2 sigmoid2_from_low(f32x2 g, float& lowest) {
+  float lo, hi;
+  unpair(g, lo, hi);
+  lowest = fminf(lowest, fminf(lo, hi));
+  return pair(sigmoid(fmaxf(lo, kLow)), sigmoid(fmaxf(hi, kLow)));
+}
+
+// Eight gates and ups -> h in bf16.
+__device__ __forceinline__ uint4 gated8(const f32x2 (&g)[4], const f32x2 (&u)[4]) {
+  f32x2 h[4];
+  float lowest = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) h[j] = mul2(mul2(g[j], sigmoid2_from_low(g[j], lowest)), u[j]);
+  if (lowest < kLow) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const f32x2 f = low_factor2(g[j]);
+      h[j] = mul2(mul2(h[j], f), f);
+    }
+  }
+  return pack_pairs(h);
+}
+
+// Eight dh, gates and ups -> dg and du in bf16; low: one of the gates may be below kLow.
+__device__ __forceinline__ void gated_back8(const f32x2 (&d)[4], const f32x2 (&g)[4], const f32x2 (&u)[4],
+                                            bool low, uint4& dg, uint4& du) {
+  const f32x2 one = pair(1.0f, 1.0f), minus = pair(-1.0f, -1.0f);
+  f32x2 a[4], b[4];
+  auto back = [&](int j, f32x2 s) {
+    const f32x2 t = mul2(g[j], s);
+    a[j] = mul2(mul2(d[j], u[j]), fma2(t, fma2(s, minus, one), s));    // s (1 + g (1 - s))
+    b[j] = mul2(d[j], t);
+  };
+#pragma unroll
+  for (int j = 0; j < 4; ++j) back(j, sigmoid2(g[j]));
+  if (low) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float lowest;
+      back(j, sigmoid2_from_low(g[j], lowest = 0.0f));
+      const f32x2 f = low_factor2(g[j]);
+      a[j] = mul2(mul2(a[j], f), f);
+      b[j] = mul2(mul2(b[j], f), f);
+    }
+  }
+  dg = pack_pairs(a);
+  du = pack_pairs(b);
 }
 
 }  // namespace mx

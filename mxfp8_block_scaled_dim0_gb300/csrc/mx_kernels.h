@@ -136,6 +136,7 @@ int read_matmul_watchdog(int* out, bool clear);
 struct ProductMaps {
   CUtensorMap a, b, sa, sb, b2, sb2, out, gate, up;
 };
+bool product_pairs(int64_t M, int64_t N, int num_sms);
 int matmul_fp4_tile_cols(int64_t M, int64_t N, int64_t K, int num_sms);
 int launch_matmul_fp4(const ProductMaps& maps, int64_t M, int64_t N, int64_t K, void* out,
                       bool out_f32, int num_sms, cudaStream_t stream);
@@ -159,14 +160,17 @@ int launch_matmul_swiglu_backward(const ProductMaps& maps, const MatmulSwigluArg
 int read_matmul_swiglu_watchdog(int* out, bool clear);
 int out_of_bounds_matmul_swiglu(bool clear);
 // MX-FP4 casts and dequantisation (mx_fp4.cu).  q0 / s0 null: dim1 only; q1 / s1 null:
-// dim0 only, which needs no maps.  x: boxes of 64 columns x 128 rows, 128B swizzle; q1: boxes
-// of 64 bytes x 128 rows, 64B swizzle.
+// dim0 only.  x, out: boxes of 64 columns x 128 rows, 128B swizzle; q1: boxes of 64 bytes x
+// 128 rows, 64B swizzle; q: the same without a swizzle.
 struct CastFp4Maps {
   CUtensorMap x, q1;
 };
+struct DequantFp4Maps {
+  CUtensorMap q, out;
+};
 int launch_cast_fp4(const CastFp4Maps* maps, const void* x, int64_t M, int64_t K, void* q0, void* s0,
                     void* s1, int num_sms, cudaStream_t stream);
-int launch_dequant_fp4(const void* q, int64_t R, int64_t C, const void* s_blk, void* out, int num_sms,
+int launch_dequant_fp4(const DequantFp4Maps& maps, const void* q, int64_t R, int64_t C, const void* s_blk, void* out, int num_sms,
                        cudaStream_t stream);
 int read_fp4_watchdog(int* out, bool clear);
 int out_of_bounds_fp4(bool clear);

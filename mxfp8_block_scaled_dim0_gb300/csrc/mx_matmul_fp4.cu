@@ -4,6 +4,15 @@
 
 namespace mx {
 
+// The pair kernel's 256 rows cost a few tokens' product their loads (128 rows of zeros in
+// either CTA): single tiles load only the rows that there are.  5120 4-bit steps, pairs and
+// tiles: 1 x 16384 17.3 and 10.3 us, 1 x 65536 53.6 and 39.1; 64 x 16384 13.3 and 12.2, but
+// 64 x 65536, more than a round of tiles, 37.7 and 46.8.
+bool product_pairs(int64_t M, int64_t N, int num_sms) {
+  if (!matmul_pairs(M, N, num_sms)) return false;
+  return M > 128 || (M > 32 && (N + 127) / 128 > num_sms);
+}
+
 int launch_matmul_fp4(const ProductMaps& maps, int64_t M, int64_t N, int64_t K, void* out,
                       bool out_f32, int num_sms, cudaStream_t stream) {
   ProductParams p = product_params(M, N, K, true);
@@ -11,9 +20,9 @@ int launch_matmul_fp4(const ProductMaps& maps, int64_t M, int64_t N, int64_t K, 
   p.out_f32 = out_f32;
   p.mapped = matmul_mapped(N, out_f32);
   p.sp_out = make_span(out, static_cast<uint64_t>(M) * static_cast<uint64_t>(N) * (out_f32 ? 4 : 2));
-  // Longer fp32 sums go in runs of at most 4096 steps.
-  constexpr int kRun = 16;
-  if (matmul_pairs(M, N, num_sms)) {
+  // Longer fp32 sums go in runs.
+  constexpr int kRun = kRunSteps / Shape<true, kPlain>::kSteps;
+  if (product_pairs(M, N, num_sms)) {
     p.m_tiles = static_cast<int>((M + 255) / 256);
     p.n_tiles = static_cast<int>((N + 255) / 256);
     if (!out_f32) return launch_pair_kernel<true, kPlain, false>(maps, p, num_sms, stream);

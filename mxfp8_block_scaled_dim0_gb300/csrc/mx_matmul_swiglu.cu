@@ -11,10 +11,17 @@ namespace {
 template <bool FP4>
 int launch_forward(const ProductMaps& maps, ProductParams& p, int num_sms,
                    cudaStream_t stream) {
-  if (matmul_pairs(p.M, 2 * p.N, num_sms)) {
+  // Saved sums go in runs.
+  constexpr int kRun = kSavedRunSteps / Shape<FP4, kSwiglu>::kSteps;
+  if (product_pairs(p.M, 2 * p.N, num_sms)) {
     p.m_tiles = static_cast<int>((p.M + 255) / 256);
     p.n_tiles = static_cast<int>((p.N + 127) / 128);
-    return launch_pair_kernel<FP4, kSwiglu, false>(maps, p, num_sms, stream);
+    if (p.q) {
+      const int runs = (p.k_blocks + kRun - 1) / kRun;
+      p.run = (p.k_blocks + runs - 1) / runs;
+    }
+    return p.q ? launch_pair_kernel<FP4, kSwiglu, true>(maps, p, num_sms, stream)
+               : launch_pair_kernel<FP4, kSwiglu, false>(maps, p, num_sms, stream);
   }
   const TileChoice t = choose_tiles(p.M, 2 * p.N, p.k_blocks, num_sms, 128);
   p.cols = t.cols;
@@ -23,12 +30,15 @@ int launch_forward(const ProductMaps& maps, ProductParams& p, int num_sms,
   p.n_tiles = static_cast<int>((2 * p.N + t.cols - 1) / t.cols);
   p.load_bytes = (matmul_box_rows(p.M, false, 128) + t.cols) * kBoxCols +
                  3 * Shape<FP4, kSwiglu>::kSf * kSfBytes;
-  return launch_tile_kernel<FP4, kSwiglu, false>(maps, p, stream);
+  p.run = kRun;
+  return p.q && (p.k_blocks + p.split - 1) / p.split > kRun
+             ? launch_tile_kernel<FP4, kSwiglu, true>(maps, p, stream)
+             : launch_tile_kernel<FP4, kSwiglu, false>(maps, p, stream);
 }
 
 template <bool FP4>
 int launch_backward(const ProductMaps& maps, ProductParams& p, int num_sms, cudaStream_t stream) {
-  if (matmul_pairs(p.M, p.N, num_sms)) {
+  if (product_pairs(p.M, p.N, num_sms)) {
     p.m_tiles = static_cast<int>((p.M + 255) / 256);
     p.n_tiles = static_cast<int>((p.N + 255) / 256);
     return p.q ? launch_pair_kernel<FP4, kSwigluBack, true>(maps, p, num_sms, stream)

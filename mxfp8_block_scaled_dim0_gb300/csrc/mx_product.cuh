@@ -110,10 +110,16 @@ __device__ __forceinline__ void block_scale(uint32_t amax, uint32_t& sbyte, floa
 
 __device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+
 // ---- one tile per cluster ------------------------------------------------------
 
 constexpr int kTileStages = 6;
-constexpr int kTileThreads = 192;           // loads, MMA, four epilogue warps
+// Loads, MMA, and epilogue warps: four, or eight where results are worked on.
+template <int EPI>
+constexpr int kTileThreads = EPI == kPlain ? 192 : 320;
 constexpr int kPitch = 132;                 // floats a row of the partial tile
 
 // Sums of eight neighbouring columns over the cluster's partial tiles, in rank order; the
@@ -136,10 +142,6 @@ __device__ __forceinline__ void cluster_sum8(const float* part, int split, float
       v[0] += lo[q].x; v[1] += lo[q].y; v[2] += lo[q].z; v[3] += lo[q].w;
       v[4] += hi[q].x; v[5] += hi[q].y; v[6] += hi[q].z; v[7] += hi[q].w;
     }
-}
-
-__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
-  return make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]), bf16x2(v[6], v[7]));
 }
 
 // Eight values of a 32-block that four neighbouring lanes hold, saved as MX-FP8; `in`: they
@@ -165,25 +167,45 @@ __device__ __forceinline__ void save8(const ProductParams& p, int64_t m, int64_t
   }
 }
 
-// Eight saved values: column c of [gate | up] of row m.
-__device__ __forceinline__ void saved8(const ProductParams& p, int64_t m, int64_t c, float (&v)[8]) {
-  f32x2 w[4];
-  if (p.q) {
-    const uint2 q = ld_q8(p.q + m * 2 * p.N + c);
-    mx_get_pairs(q, p.s[scale_at(m, c >> 5, p.s_cols4)], w);
-  } else {
-    get_pairs(__ldg(reinterpret_cast<const uint4*>(p.gu + m * 2 * p.N + c)), w);
+// Eight gates and ups of a row, column c on, as they lie in memory.
+struct Saved8 {
+  uint4 g, u;          // bf16, or e4m3 in the first two words
+  uint32_t s;          // both scales
+  __device__ __forceinline__ void load(const ProductParams& p, int64_t m, int64_t c) {
+    if (p.q) {
+      const uint8_t* q = p.q + m * 2 * p.N + c;
+      const uint2 a = ld_q8(q), b = ld_q8(q + p.N);
+      g.x = a.x;
+      g.y = a.y;
+      u.x = b.x;
+      u.y = b.y;
+      s = __ldg(p.s + scale_at(m, c >> 5, p.s_cols4)) |
+          static_cast<uint32_t>(__ldg(p.s + scale_at(m, (p.N + c) >> 5, p.s_cols4))) << 8;
+    } else {
+      const uint16_t* x = p.gu + m * 2 * p.N + c;
+      g = __ldg(reinterpret_cast<const uint4*>(x));
+      u = __ldg(reinterpret_cast<const uint4*>(x + p.N));
+    }
   }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) unpair(w[j], v[2 * j], v[2 * j + 1]);
-}
+  // Whether a gate may be low.
+  __device__ __forceinline__ bool get(const ProductParams& p, f32x2 (&gv)[4], f32x2 (&uv)[4]) const {
+    if (p.q) {
+      mx_get_pairs(make_uint2(g.x, g.y), s & 0xFFu, gv);
+      mx_get_pairs(make_uint2(u.x, u.y), s >> 8, uv);
+      return may_be_low(s & 0xFFu);
+    }
+    get_pairs(g, gv);
+    get_pairs(u, uv);
+    return any_low(lowest2(g));
+  }
+};
 
-// RUNS: the contraction in runs, as in mx_matmul.cu.
+// RUNS: the contraction in runs, as in mx_matmul.cu (fp32 results, and saved ones).
 template <bool FP4, int EPI, bool RUNS>
-__global__ void __launch_bounds__(kTileThreads, 1)
+__global__ void __launch_bounds__(kTileThreads<EPI>, 1)
     tile_kernel(const __grid_constant__ ProductMaps maps, const ProductParams p) {
   using S = Shape<FP4, EPI>;
-  static_assert(!RUNS || EPI == kPlain, "16-bit results need no runs");
+  static_assert(!RUNS || EPI != kSwigluBack, "16-bit results need no runs");
   static_assert(kBoxRows * kPitch * 4 <= kTileStages * S::kTileStride, "partial tile fits the ring");
   asm volatile("griddepcontrol.launch_dependents;");
   extern __shared__ uint8_t smem_raw[];
@@ -214,7 +236,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     if (RUNS)
       for (int j = 0; j < 2; ++j) {
         mbar_init(&ready[j], 1);
-        mbar_init(&drained[j], 4);            // the epilogue warps
+        mbar_init(&drained[j], kTileThreads<EPI> / 32 - 2);      // the epilogue warps
       }
     mbar_init(&done, 1);
     mbar_init(&stall_bar, 1);
@@ -239,8 +261,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const uint32_t t_sfa = tmem + kTmemCols / 2, t_sfb = t_sfa + 4 * S::kSf, t_sfu = t_sfb + 4 * S::kSf;
   const int quarter = warp & 3;
   const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-  // This lane's row of the runs before the last.
-  float sums[RUNS ? kBoxRows : 1] = {};
+  // This lane's row of the runs before the last: an epilogue warp's share of the columns.
+  constexpr int kShare = EPI == kPlain ? kBoxRows : kBoxRows / 2;
+  const int c0 = EPI == kPlain ? 0 : (warp - 2) / 4 * kShare;
+  float sums[RUNS ? kShare : 1] = {};
 
   if (warp == 0) {
     if (elect_one()) {
@@ -330,14 +354,27 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       tcgen05_commit<1>(&done);
       mbar_drain(&done, 0u, kWaitLimitNs);   // every MMA issued has finished
     }
+  } else if (EPI == kSwigluBack) {
+    // The tile's gates and ups into L2: whole rows by the warp, 128 bytes a lane.
+    const int size = p.q ? 1 : 2;
+    const uint8_t* from = p.q ? p.q : reinterpret_cast<const uint8_t*>(p.gu);
+    const int64_t left = p.N - n0 < width ? p.N - n0 : width;
+    const int lines = static_cast<int>((left * size + 127) / 128);        // of a half row: 1 or 2
+    const int64_t m1 = static_cast<int64_t>(mt) * kBoxRows + rank * (kBoxRows / p.split);
+    for (int i = threadIdx.x - 64; i < kBoxRows / p.split * 2 * lines; i += kTileThreads<EPI> - 64) {
+      const int64_t m = m1 + i / (2 * lines);
+      const int k = i % (2 * lines);
+      if (m < p.M)
+        prefetch_l2(from + (m * 2 * p.N + (k & 1) * p.N + n0) * size + (k >> 1) * 128);
+    }
   } else if (RUNS) {
     for (int run = 0; run < runs - 1; ++run) {
       if (!mbar_wait(&ready[run & 1], static_cast<uint32_t>(run >> 1) & 1u, &abort_flag)) break;
       tcgen05_fence_after();
-      const uint32_t at = tmem + lanes + (run & 1) * kBoxRows;
+      const uint32_t at = tmem + lanes + (run & 1) * kBoxRows + c0;
 #pragma unroll
-      for (int c = 0; c < kBoxRows; c += 16) {
-        if (c >= p.cols) break;
+      for (int c = 0; c < kShare; c += 16) {
+        if (c0 + c >= p.cols) break;
         uint32_t v[16];
         tmem_ld_16(at + c, v);
         tmem_ld_wait();
@@ -355,19 +392,26 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   tcgen05_fence_after();
   const bool ok = abort_flag == 0;
   const uint32_t last = tmem + lanes + ((runs - 1) & 1) * kBoxRows;
+  // Rows of the tile that this CTA finishes, in pieces of eight columns.
+  const int rows = kBoxRows / p.split;
+  const int64_t m0 = static_cast<int64_t>(mt) * kBoxRows + rank * rows;
+  const int pieces = width >> 3, shift = 31 - __clz(pieces);
+  const int total = m0 < p.M ? static_cast<int>(p.M - m0 < rows ? p.M - m0 : rows) << shift : 0;
   float* part = reinterpret_cast<float*>(ring);
   if (warp >= 2 && static_cast<int64_t>(mt) * kBoxRows + quarter * 32 < p.M) {
     const int row = quarter * 32 + lane;
     constexpr int kUnroll = RUNS ? 4 : 1;      // sums are registers: c must be a constant
+    // kSwiglu: gate in columns 0 .., up in 64 ..
 #pragma unroll kUnroll
-    for (int c = 0; c < kBoxRows; c += 32) {
-      if (c >= p.cols) break;                  // kSwiglu: gate in columns 0 .., up in 64 ..
+    for (int c1 = 0; c1 < kShare; c1 += 32) {
+      const int c = c0 + c1;
+      if (c >= p.cols) break;
       uint32_t v[32];
       tmem_ld_32(last + c, v);
       tmem_ld_wait();
       if constexpr (RUNS)
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(sums[c + j] + __uint_as_float(v[j]));
+        for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(sums[c1 + j] + __uint_as_float(v[j]));
       uint4* dst = reinterpret_cast<uint4*>(part + row * kPitch + c);
 #pragma unroll
       for (int j = 0; j < 8; ++j)
@@ -376,16 +420,41 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tcgen05_fence_before();
   }
   cluster_sync();
-  // Rows of the tile that this CTA finishes.
-  const int rows = kBoxRows / p.split;
-  const int64_t m0 = static_cast<int64_t>(mt) * kBoxRows + rank * rows;
-  if (ok && m0 < p.M) {
-    const int pieces = width >> 3;                       // of eight, a row
-    const int shift = 31 - __clz(pieces);
-    const int n_rows = static_cast<int>(p.M - m0 < rows ? p.M - m0 : rows);
-    const int total = n_rows << shift;
+  if constexpr (EPI == kSwigluBack) {
+    // Two pieces a thread at a time: their gates and ups, asked into L2 while the MMAs went
+    // on, are under way together.
+    constexpr int kFew = 2;
+    if (ok)
+      for (int i0 = threadIdx.x; i0 < total; i0 += kFew * kTileThreads<EPI>) {
+        Saved8 w[kFew];
+#pragma unroll
+        for (int k = 0; k < kFew; ++k) {
+          const int i = i0 + k * kTileThreads<EPI>;
+          const int64_t m = m0 + (i >> shift), n = n0 + (i & (pieces - 1)) * 8;
+          if (i < total && n < p.N) w[k].load(p, m, n);
+        }
+#pragma unroll
+        for (int k = 0; k < kFew; ++k) {
+          const int i = i0 + k * kTileThreads<EPI>;
+          const int r = i >> shift, c = (i & (pieces - 1)) * 8;
+          const int64_t m = m0 + r, n = n0 + c;
+          if (i >= total || n >= p.N) continue;
+          float v[8];
+          cluster_sum8(part + (rank * rows + r) * kPitch + c, p.split, v);
+          f32x2 d[4], g[4], u[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) d[j] = pair(v[2 * j], v[2 * j + 1]);
+          const bool low = w[k].get(p, g, u);
+          uint4 dg, du;
+          gated_back8(d, g, u, low, dg, du);
+          uint16_t* out = static_cast<uint16_t*>(p.out) + m * 2 * p.N + n;
+          if (in_span(p.sp_out, out, 16)) *reinterpret_cast<uint4*>(out) = dg;
+          if (in_span(p.sp_out, out + p.N, 16)) *reinterpret_cast<uint4*>(out + p.N) = du;
+        }
+      }
+  } else if (ok) {
     // Whole warps stay in the loop: four lanes share a block of 32.
-    for (int i0 = warp * 32; i0 < total; i0 += kTileThreads) {
+    for (int i0 = warp * 32; i0 < total; i0 += kTileThreads<EPI>) {
       const int i = i0 + lane < total ? i0 + lane : total - 1;
       const int r = i >> shift, c = (i & (pieces - 1)) * 8;
       const int64_t m = m0 + r, n = n0 + c;
@@ -399,26 +468,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           store_out8(p.out, p.out_f32, m * p.N + n, v,
                      vec ? 8 : static_cast<int>(p.N - n < 8 ? p.N - n : 8), vec, p.sp_out);
       } else if constexpr (EPI == kSwiglu) {
-        float u[8], h[8];
+        float u[8];
         cluster_sum8(at + 64, p.split, u);
+        f32x2 g2[4], u2[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) h[j] = gated(v[j], u[j]);
+        for (int j = 0; j < 4; ++j) {
+          g2[j] = pair(v[2 * j], v[2 * j + 1]);
+          u2[j] = pair(u[2 * j], u[2 * j + 1]);
+        }
         uint16_t* out = static_cast<uint16_t*>(p.out) + m * p.N + n;
-        if (in && in_span(p.sp_out, out, 16)) *reinterpret_cast<uint4*>(out) = pack8(h);
+        if (in && in_span(p.sp_out, out, 16)) *reinterpret_cast<uint4*>(out) = gated8(g2, u2);
         if (p.q) {
           save8(p, m, n, v, in);
           save8(p, m, p.N + n, u, in);
-        }
-      } else {
-        if (in) {
-          float g[8], u[8], dg[8], du[8];
-          saved8(p, m, n, g);
-          saved8(p, m, p.N + n, u);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) gated_back(v[j], g[j], u[j], dg[j], du[j]);
-          uint16_t* out = static_cast<uint16_t*>(p.out) + m * 2 * p.N + n;
-          if (in_span(p.sp_out, out, 16)) *reinterpret_cast<uint4*>(out) = pack8(dg);
-          if (in_span(p.sp_out, out + p.N, 16)) *reinterpret_cast<uint4*>(out + p.N) = pack8(du);
         }
       }
     }
@@ -430,10 +492,37 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
 // ---- CTA pairs -------------------------------------------------------------------
 
-constexpr int kPairStages = 5;
-constexpr int kPairThreads = 320;             // loads, MMA, eight epilogue warps
+// What a pair's epilogue does beside EPI (FLAG): kPlain, results in fp32; kSwiglu, gate and up
+// saved; kSwigluBack, gate and up from 8 bits.
+//
+// Stages of loads, and bytes of an epilogue warp's staging.  A stage counts: 16640 x 8192 x
+// 5120 e2m1 takes 199 us with five, 216 with four, 257 with three (six do not fit); h with
+// the save in e4m3 790 and 860, although with four the warps need not wait for the stores.
+// kSwigluBack does with four, as gates and ups come through shared memory: loads of a row a
+// lane touch 32 lines each, and took the load/store units as long as all else (8192 x 8192 x
+// 1024 e2m1 135 us with them, 117 without).
+template <int EPI>
+constexpr int kPairStages = EPI == kSwigluBack ? 4 : 5;
+template <int EPI>
+constexpr int kWarpStage = EPI == kSwigluBack ? 10 * 1024 : kStageOut;
 template <bool FP4, int EPI>
-constexpr int kPairSmem = kPairStages * Shape<FP4, EPI>::kPairStride + 8 * kStageOut + 1024;
+constexpr int kPairSmem = kPairStages<EPI> * Shape<FP4, EPI>::kPairStride + 8 * kWarpStage<EPI> + 1024;
+
+// Loads, MMA, eight epilogue warps.  kSwigluBack: two idle warps more, so that the first
+// warpgroup can hand registers to the two that hold 128 results and what they need beside
+// (168 a thread at launch: 56 x 128 + 224 x 256 are as many).
+template <int EPI>
+constexpr int kFirstEpilogueWarp = EPI == kSwigluBack ? 4 : 2;
+template <int EPI>
+constexpr int kPairThreads = 32 * (kFirstEpilogueWarp<EPI> + 8);
+template <int REGS>
+__device__ __forceinline__ void give_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+template <int REGS>
+__device__ __forceinline__ void take_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
+}
 
 // Bands of `band` M-tiles, walked along N, M fastest inside a band.
 struct Tiles {
@@ -453,51 +542,80 @@ __device__ __forceinline__ uint4* box64(uint8_t* box, int lane, int j) {
   return reinterpret_cast<uint4*>(box + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4));
 }
 
-// 32 values of [gate | up] of a row, column c on, as they lie in memory.
-template <bool SAVED8>
-struct Saved;
+// ---- kSwigluBack's gates and ups ---------------------------------------------------
+//
+// 32 rows of a warp, in blocks of 32 columns, copied into its staging by all lanes (whole
+// lines at a time) while the products are computed.
+//   8 bits: four blocks of 2 KB at once: gates, then ups, 32 bytes a row, the sixteens of rows
+//           4..7 of every eight exchanged (a row a lane is then free of bank conflicts).  A
+//           block's dg goes out through 2 KB behind them, its du through the block's own.
+//   bf16:   two blocks of 4 KB at a time, gates and ups in boxes of 64 bytes a row in the
+//           order of a 64-byte swizzle, replaced by dg and du in place.
+__device__ __forceinline__ void copy16(uint8_t* smem_dst, const void* g) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem_dst)), "l"(g) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
-template <>
-struct Saved<true> {
-  uint4 w[2];
-  uint32_t s;
-  __device__ __forceinline__ void load(const ProductParams& p, int64_t m, int64_t c) {
-    const uint4* q = reinterpret_cast<const uint4*>(p.q + m * 2 * p.N + c);
-    w[0] = __ldg(q);
-    w[1] = __ldg(q + 1);
-    s = __ldg(p.s + scale_at(m, c >> 5, p.s_cols4));
-  }
-  // Values 8 j .. 8 j + 7.
-  __device__ __forceinline__ void get(int j, f32x2 (&v)[4]) const {
-    const uint4& b = w[j >> 1];
-    mx_get_pairs((j & 1) ? make_uint2(b.z, b.w) : make_uint2(b.x, b.y), s, v);
-  }
-};
-
-template <>
-struct Saved<false> {
-  uint4 w[4];
-  __device__ __forceinline__ void load(const ProductParams& p, int64_t m, int64_t c) {
-    const uint4* g = reinterpret_cast<const uint4*>(p.gu + m * 2 * p.N + c);
+// Rows m .. m + 31, columns n .. n + 127, of both halves.
+__device__ __forceinline__ void copy_saved8(const ProductParams& p, uint8_t* to, int64_t m, int64_t n,
+                                            int lane) {
+  const int c = lane & 7;                    // sixteen bytes of a row's 128
+  if (n + 16 * c >= p.N) return;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = __ldg(g + j);
+  for (int k = 0; k < 8; ++k) {
+    const int r = 4 * k + (lane >> 3);
+    if (m + r >= p.M) break;
+    const uint8_t* q = p.q + (m + r) * 2 * p.N + n + 16 * c;
+    uint8_t* dst = to + (c >> 1) * 2048 + r * 32 + (((c ^ (r >> 2)) & 1) << 4);
+    copy16(dst, q);
+    copy16(dst + 1024, q + p.N);
   }
-  __device__ __forceinline__ void get(int j, f32x2 (&v)[4]) const { get_pairs(w[j], v); }
+}
+
+// A row's share of one of those blocks.
+struct SavedBlock {
+  uint4 g[2], u[2];
+  __device__ __forceinline__ void load(const uint8_t* block, int lane) {
+    const uint8_t* at = block + lane * 32;
+    const int x = ((lane >> 2) & 1) << 4;
+    g[0] = *reinterpret_cast<const uint4*>(at + x);
+    g[1] = *reinterpret_cast<const uint4*>(at + (x ^ 16));
+    u[0] = *reinterpret_cast<const uint4*>(at + 1024 + x);
+    u[1] = *reinterpret_cast<const uint4*>(at + 1024 + (x ^ 16));
+  }
 };
 
-// FLAG: kPlain, results in fp32; kSwigluBack, gate and up from 8 bits.
+// ... columns c .. c + 31 of bf16.
+__device__ __forceinline__ void copy_saved16(const ProductParams& p, uint8_t* to, int64_t m, int64_t c,
+                                             int lane) {
+  const int j = lane & 3;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int r = 8 * k + (lane >> 2);
+    if (m + r >= p.M) break;
+    const uint16_t* x = p.gu + (m + r) * 2 * p.N + c + 8 * j;
+    uint8_t* dst = reinterpret_cast<uint8_t*>(box64(to, r, j));
+    copy16(dst, x);
+    copy16(dst + 2048, x + p.N);
+  }
+}
+
 template <bool FP4, int EPI, bool FLAG>
-__global__ void __launch_bounds__(kPairThreads, 1)
+__global__ void __launch_bounds__(kPairThreads<EPI>, 1)
     pair_kernel(const __grid_constant__ ProductMaps maps, const ProductParams p) {
   using S = Shape<FP4, EPI>;
+  constexpr int kStages = kPairStages<EPI>;
   asm volatile("griddepcontrol.launch_dependents;");
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t full[kPairStages], empty[kPairStages], ready, drained, done,
-      stall_bar;
+  __shared__ __align__(8) uint64_t full[kStages], empty[kStages], ready, drained, done, stall_bar;
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag, issued;
   uint8_t* ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  uint8_t* stage_out = ring + kPairStages * S::kPairStride;
+  uint8_t* stage_out = ring + kStages * S::kPairStride;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_rank());
   const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
@@ -506,7 +624,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   constexpr uint32_t kSfaCol = 256, kSfbCol = kSfaCol + 4 * S::kSf;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kPairStages; ++s) {
+    for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);                 // in the leader, for both CTAs' loads
       mbar_init(&empty[s], 1);
     }
@@ -535,99 +653,106 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   tcgen05_fence_after();
   const uint32_t tmem = tmem_base;
 
-  if (warp == 0) {
-    if (elect_one()) {
-      int i = 0;
-      bool ok = true;
-      for (int t = first; ok && t < n_tiles; t += stride) {
-        int mt, nt;
-        tiles.at(t, mt, nt);
-        const int m = (2 * mt + rank) * kBoxRows;
-        // kSwiglu: gate's rows in the leader, up's in its peer.
-        const int n = EPI == kSwiglu ? nt * kBoxRows : (2 * nt + rank) * kBoxRows;
-        const CUtensorMap* map_b = EPI == kSwiglu && rank ? &maps.b2 : &maps.b;
-        for (int kb = 0; kb < p.k_blocks; ++kb, ++i) {
-          const int s = i % kPairStages;
-          if (kDiagStall && blockIdx.x == 0 && i == p.stall_at) {
-            mbar_wait(&stall_bar, 0u, &abort_flag, p.stall_ns);
-            ok = false;
-            break;
-          }
-          if (i >= kPairStages &&
-              !mbar_wait(&empty[s], static_cast<uint32_t>((i / kPairStages - 1) & 1), &abort_flag)) {
-            ok = false;
-            break;
-          }
-          uint8_t* st = ring + s * S::kPairStride;
-          uint8_t* sf = st + 2 * kBoxBytes;
-          const uint32_t bar = map_to_rank(smem_u32(&full[s]), 0);
-          const int x = kb * kBoxCols, sx = kb * 128 * S::kSf;
-          constexpr int kSfTile = S::kSf * kSfBytes;
-          // The leader alone announces both CTAs' bytes.
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * S::kPairBytes);
-          tma_load_2d_pair(st, &maps.a, x, m, bar);
-          tma_load_2d_pair(st + kBoxBytes, map_b, x, n, bar);
-          tma_load_2d_pair(sf, &maps.sa, sx, 2 * mt + rank, bar);
-          if (EPI == kSwiglu) {
-            tma_load_2d_pair(sf + kSfTile, &maps.sb, sx, nt, bar);
-            tma_load_2d_pair(sf + 2 * kSfTile, &maps.sb2, sx, nt, bar);
-          } else {
-            tma_load_2d_pair(sf + kSfTile, &maps.sb, sx, 2 * nt, bar);
+  // One branch a warpgroup, so that the compiler sees which registers either has.
+  constexpr int kFirst = kFirstEpilogueWarp<EPI>;
+  if (warp < kFirst) {
+    if (EPI == kSwigluBack) give_registers<56>();
+    if (warp == 0) {
+      if (elect_one()) {
+        int i = 0;
+        bool ok = true;
+        for (int t = first; ok && t < n_tiles; t += stride) {
+          int mt, nt;
+          tiles.at(t, mt, nt);
+          const int m = (2 * mt + rank) * kBoxRows;
+          // kSwiglu: gate's rows in the leader, up's in its peer.
+          const int n = EPI == kSwiglu ? nt * kBoxRows : (2 * nt + rank) * kBoxRows;
+          const CUtensorMap* map_b = EPI == kSwiglu && rank ? &maps.b2 : &maps.b;
+          for (int kb = 0; kb < p.k_blocks; ++kb, ++i) {
+            const int s = i % kStages;
+            if (kDiagStall && blockIdx.x == 0 && i == p.stall_at) {
+              mbar_wait(&stall_bar, 0u, &abort_flag, p.stall_ns);
+              ok = false;
+              break;
+            }
+            if (i >= kStages &&
+                !mbar_wait(&empty[s], static_cast<uint32_t>((i / kStages - 1) & 1), &abort_flag)) {
+              ok = false;
+              break;
+            }
+            uint8_t* st = ring + s * S::kPairStride;
+            uint8_t* sf = st + 2 * kBoxBytes;
+            const uint32_t bar = map_to_rank(smem_u32(&full[s]), 0);
+            const int x = kb * kBoxCols, sx = kb * 128 * S::kSf;
+            constexpr int kSfTile = S::kSf * kSfBytes;
+            // The leader alone announces both CTAs' bytes.
+            if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * S::kPairBytes);
+            tma_load_2d_pair(st, &maps.a, x, m, bar);
+            tma_load_2d_pair(st + kBoxBytes, map_b, x, n, bar);
+            tma_load_2d_pair(sf, &maps.sa, sx, 2 * mt + rank, bar);
+            if (EPI == kSwiglu) {
+              tma_load_2d_pair(sf + kSfTile, &maps.sb, sx, nt, bar);
+              tma_load_2d_pair(sf + 2 * kSfTile, &maps.sb2, sx, nt, bar);
+            } else {
+              tma_load_2d_pair(sf + kSfTile, &maps.sb, sx, 2 * nt, bar);
+            }
           }
         }
+        issued = i;
       }
-      issued = i;
-    }
-  } else if (warp == 1) {
-    if (rank == 0 && elect_one()) {
-      const uint32_t idesc = idesc_of<FP4>(256, 256);
-      const uint32_t sfa = tmem + kSfaCol, sfb = tmem + kSfbCol;
-      int i = 0, item = 0;
-      bool ok = true;
-      for (int t = first; ok && t < n_tiles; t += stride) {
-        for (int k0 = 0; ok && k0 < p.k_blocks; k0 += p.run, ++item) {
-          if (item > 0 && !mbar_wait_cluster(&drained, static_cast<uint32_t>((item - 1) & 1), &abort_flag)) {
-            ok = false;
-            break;
-          }
-          tcgen05_fence_after();
-          const int k1 = min(k0 + p.run, p.k_blocks);
-          for (int kb = k0; kb < k1; ++kb, ++i) {
-            const int s = i % kPairStages;
-            if (!mbar_wait_cluster(&full[s], static_cast<uint32_t>((i / kPairStages) & 1), &abort_flag)) {
+    } else if (warp == 1) {
+      if (rank == 0 && elect_one()) {
+        const uint32_t idesc = idesc_of<FP4>(256, 256);
+        const uint32_t sfa = tmem + kSfaCol, sfb = tmem + kSfbCol;
+        int i = 0, item = 0;
+        bool ok = true;
+        for (int t = first; ok && t < n_tiles; t += stride) {
+          for (int k0 = 0; ok && k0 < p.k_blocks; k0 += p.run, ++item) {
+            if (item > 0 && !mbar_wait_cluster(&drained, static_cast<uint32_t>((item - 1) & 1), &abort_flag)) {
               ok = false;
               break;
             }
             tcgen05_fence_after();
-            const uint32_t st = smem_u32(ring + s * S::kPairStride);
-            const uint32_t sf = st + 2 * kBoxBytes;
-#pragma unroll
-            for (int j = 0; j < S::kSf; ++j) {
-              auto tile = [&](int row) { return scale_desc(sf + (row * S::kSf + j) * kSfBytes); };
-              tcgen05_cp_scales<2>(sfa + 4 * j, tile(0));
-              tcgen05_cp_scales<2>(sfb + 8 * j, tile(1));
-              tcgen05_cp_scales<2>(sfb + 8 * j + 4, tile(2));
-            }
-            const uint64_t da = operand_desc(st), db = operand_desc(st + kBoxBytes);
-            const int mmas = kb == p.k_blocks - 1 ? p.last_mmas : 4;
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (k < mmas) {
-                const int j = FP4 ? k >> 1 : 0;
-                mma<FP4, 2>(tmem, da + kStepK * k, db + kStepK * k, idesc, k, sfa + 4 * j,
-                            sfb + 8 * j, kb > k0 || k > 0);
+            const int k1 = min(k0 + p.run, p.k_blocks);
+            for (int kb = k0; kb < k1; ++kb, ++i) {
+              const int s = i % kStages;
+              if (!mbar_wait_cluster(&full[s], static_cast<uint32_t>((i / kStages) & 1), &abort_flag)) {
+                ok = false;
+                break;
               }
-            tcgen05_commit<2>(&empty[s]);
+              tcgen05_fence_after();
+              const uint32_t st = smem_u32(ring + s * S::kPairStride);
+              const uint32_t sf = st + 2 * kBoxBytes;
+#pragma unroll
+              for (int j = 0; j < S::kSf; ++j) {
+                auto tile = [&](int row) { return scale_desc(sf + (row * S::kSf + j) * kSfBytes); };
+                tcgen05_cp_scales<2>(sfa + 4 * j, tile(0));
+                tcgen05_cp_scales<2>(sfb + 8 * j, tile(1));
+                tcgen05_cp_scales<2>(sfb + 8 * j + 4, tile(2));
+              }
+              const uint64_t da = operand_desc(st), db = operand_desc(st + kBoxBytes);
+              const int mmas = kb == p.k_blocks - 1 ? p.last_mmas : 4;
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (k < mmas) {
+                  const int j = FP4 ? k >> 1 : 0;
+                  mma<FP4, 2>(tmem, da + kStepK * k, db + kStepK * k, idesc, k, sfa + 4 * j,
+                              sfb + 8 * j, kb > k0 || k > 0);
+                }
+              tcgen05_commit<2>(&empty[s]);
+            }
+            if (ok) tcgen05_commit<2>(&ready);
           }
-          if (ok) tcgen05_commit<2>(&ready);
         }
+        tcgen05_commit<2>(&done);
+        mbar_drain(&done, 0u, kWaitLimitNs);     // every MMA issued has finished
       }
-      tcgen05_commit<2>(&done);
-      mbar_drain(&done, 0u, kWaitLimitNs);     // every MMA issued has finished
     }
   } else {
-    const int quarter = warp & 3, half = (warp - 2) >> 2;
-    uint8_t* so = stage_out + (warp - 2) * kStageOut;
+    if (EPI == kSwigluBack) take_registers<224>();
+    // A quarter of the lanes, and a share of the columns.
+    const int quarter = warp & 3, share = (warp - kFirst) >> 2;
+    uint8_t* so = stage_out + (warp - kFirst) * kWarpStage<EPI>;
     const uint32_t drained_bar = map_to_rank(smem_u32(&drained), 0);
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     int item = 0;
@@ -654,7 +779,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             break;
           }
           tcgen05_fence_after();
-          const uint32_t at = tmem + lanes + half * 128;
+          const uint32_t at = tmem + lanes + share * 128;
           if constexpr (!F32) {
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
@@ -688,7 +813,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         if (!ok) break;
         // 32 rows x 128 columns through shared memory, a box at a time, in the
         // swizzled order the tensor map expects.
-        const int n = 2 * nt * kBoxRows + half * 128;
+        const int n = 2 * nt * kBoxRows + share * 128;
         if (m >= p.M || n >= p.N) continue;
         uint8_t* row = so + lane * 128;
 #pragma unroll
@@ -711,23 +836,41 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
       } else {
         const int64_t row = m + lane;
+        const bool in = row < p.M;
         // kSwiglu: 64 gate columns and their up columns; kSwigluBack: 128 columns of dh.
         uint32_t v[4][32];
-        const int n = EPI == kSwiglu ? nt * kBoxRows + half * 64 : 2 * nt * kBoxRows + half * 128;
-        // The first block's gate and up are under way before the products are ready.
-        Saved<FLAG> g, u;
-        const bool in = row < p.M;
-        if (EPI == kSwigluBack && in && n < p.N) {
-          g.load(p, row, n);
-          u.load(p, row, p.N + n);
+        const int n = EPI == kSwiglu ? nt * kBoxRows + share * 64 : 2 * nt * kBoxRows + share * 128;
+        uint32_t scales[2] = {};                 // kSwigluBack from 8 bits: of four blocks
+        if (lane == 0) bulk_wait_read<0>();      // the last tile's results have left the staging
+        __syncwarp();
+        if (EPI == kSwigluBack && m < p.M && n < p.N) {
+          if constexpr (FLAG) {
+            copy_saved8(p, so, m, n, lane);
+            copies_commit();
+            if (in)
+#pragma unroll
+              for (int b = 0; b < 4; ++b)
+                if (n + 32 * b < p.N) {
+                  const int64_t c = n / 32 + b;
+                  scales[0] |= static_cast<uint32_t>(__ldg(p.s + scale_at(row, c, p.s_cols4))) << (8 * b);
+                  scales[1] |=
+                      static_cast<uint32_t>(__ldg(p.s + scale_at(row, p.N / 32 + c, p.s_cols4))) << (8 * b);
+                }
+          } else {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              if (n + 32 * b < p.N) copy_saved16(p, so + 4096 * b, m, n + 32 * b, lane);
+              copies_commit();
+            }
+          }
         }
+        const uint32_t at = tmem + lanes + share * (EPI == kSwiglu ? 64 : 128);
+        constexpr int kNext = EPI == kSwiglu ? 128 : 64;      // where the second 64 columns are
         if (!mbar_wait(&ready, static_cast<uint32_t>(item++ & 1), &abort_flag)) {
           ok = false;
           break;
         }
         tcgen05_fence_after();
-        const uint32_t at = tmem + lanes + half * (EPI == kSwiglu ? 64 : 128);
-        constexpr int kNext = EPI == kSwiglu ? 128 : 64;      // where the second 64 columns are
         tmem_ld_32(at, v[0]);
         tmem_ld_32(at + 32, v[1]);
         tmem_ld_32(at + kNext, v[2]);
@@ -736,19 +879,46 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         tcgen05_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_remote(drained_bar);
+        if constexpr (EPI == kSwiglu && FLAG) {
+          // The other runs.
+          for (int k0 = p.run; k0 < p.k_blocks; k0 += p.run, ++item) {
+            if (!mbar_wait(&ready, static_cast<uint32_t>(item & 1), &abort_flag)) {
+              ok = false;
+              break;
+            }
+            tcgen05_fence_after();
+#pragma unroll
+            for (int b = 0; b < 8; ++b) {
+              uint32_t w[16];
+              tmem_ld_16(at + (b >> 2) * kNext + 16 * (b & 3), w);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                uint32_t& x = v[b >> 1][(b & 1) * 16 + j];
+                x = __float_as_uint(__uint_as_float(x) + __uint_as_float(w[j]));
+              }
+            }
+            tcgen05_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(drained_bar);
+          }
+          if (!ok) break;
+        }
         if (m >= p.M || n >= p.N) continue;
         if constexpr (EPI == kSwiglu) {
-          if (lane == 0) bulk_wait_read<0>();
-          __syncwarp();
+          auto value = [&](int b, int j) {
+            return pair(__uint_as_float(v[b][2 * j]), __uint_as_float(v[b][2 * j + 1]));
+          };
           uint8_t* dst = so + lane * 128;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            float h[8];
+            f32x2 g[4], u[4];
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              h[k] = gated(__uint_as_float(v[j >> 2][(j & 3) * 8 + k]),
-                           __uint_as_float(v[2 + (j >> 2)][(j & 3) * 8 + k]));
-            *reinterpret_cast<uint4*>(dst + ((j ^ (lane & 7)) << 4)) = pack8(h);
+            for (int k = 0; k < 4; ++k) {
+              g[k] = value(j >> 2, (j & 3) * 4 + k);
+              u[k] = value(2 + (j >> 2), (j & 3) * 4 + k);
+            }
+            *reinterpret_cast<uint4*>(dst + ((j ^ (lane & 7)) << 4)) = gated8(g, u);
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -756,7 +926,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             tma_store_2d(&maps.out, n, m, so);
             bulk_commit();
           }
-          if (p.q) {
+          if constexpr (FLAG) {
             if (lane == 0) bulk_wait_read<0>();
             __syncwarp();
 #pragma unroll
@@ -789,44 +959,101 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             }
           }
         } else {
-#pragma unroll
+          // 32 columns at a time, in a loop whose registers move up: written out four times
+          // the code does not stay in the instruction cache.
+          SavedBlock ahead;
+#pragma unroll 1
           for (int b = 0; b < 4; ++b) {
             const int64_t c = n + 32 * b;
             if (c >= p.N) break;
-            if (lane == 0) bulk_wait_read<0>();
-            __syncwarp();
+            uint8_t *out_g, *out_u;
+            auto dh8 = [&](int j, f32x2 (&d)[4]) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              f32x2 gv[4], uv[4];
-              float dg[8], du[8];
-              g.get(j, gv);
-              u.get(j, uv);
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                float g0, g1, u0, u1;
-                unpair(gv[k >> 1], g0, g1);
-                unpair(uv[k >> 1], u0, u1);
-                gated_back(__uint_as_float(v[b][8 * j + k]), k & 1 ? g1 : g0, k & 1 ? u1 : u0, dg[k],
-                           du[k]);
+              for (int k = 0; k < 4; ++k)
+                d[k] = pair(__uint_as_float(v[0][8 * j + 2 * k]), __uint_as_float(v[0][8 * j + 2 * k + 1]));
+            };
+            if constexpr (FLAG) {
+              // A block ahead in registers, so that two places are free for the results: those
+              // of the blocks read, and 2 KB behind them.
+              //   block   0          1        2        3
+              //   dg, du  behind, 0  1, 2     behind, 3   0, 1
+              if (b == 0) {
+                copies_wait<0>();
+                __syncwarp();
+                ahead.load(so, lane);
               }
-              *box64(so, lane, j) = pack8(dg);
-              *box64(so + 2048, lane, j) = pack8(du);
-            }
-            if (b < 3 && in && c + 32 < p.N) {
-              g.load(p, row, c + 32);
-              u.load(p, row, p.N + c + 32);
+              const SavedBlock w = ahead;
+              if (b < 3) ahead.load(so + 2048 * (b + 1), lane);
+              if (lane == 0) bulk_wait_read<1>();
+              __syncwarp();
+              out_g = so + 2048 * (b & 1 ? (b == 1 ? 1 : 0) : 4);
+              out_u = so + 2048 * (b == 0 ? 0 : b == 3 ? 1 : b + 1);
+              const uint32_t sg = scales[0] >> (8 * b) & 0xFFu, su = scales[1] >> (8 * b) & 0xFFu;
+              auto eight = [&](int j, bool low) {
+                f32x2 d[4], gv[4], uv[4];
+                dh8(j, d);
+                const uint4 &wg = w.g[j >> 1], &wu = w.u[j >> 1];
+                mx_get_pairs((j & 1) ? make_uint2(wg.z, wg.w) : make_uint2(wg.x, wg.y), sg, gv);
+                mx_get_pairs((j & 1) ? make_uint2(wu.z, wu.w) : make_uint2(wu.x, wu.y), su, uv);
+                uint4 dg, du;
+                gated_back8(d, gv, uv, low, dg, du);
+                *box64(out_g, lane, j) = dg;
+                *box64(out_u, lane, j) = du;
+              };
+              const bool low = may_be_low(sg);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) eight(j, low);
+            } else {
+              // Copies of the first two blocks are in flight together, then of the others.
+              if (b & 1) copies_wait<0>();
+              else copies_wait<1>();
+              __syncwarp();
+              out_g = so + 4096 * (b & 1);
+              out_u = out_g + 2048;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                f32x2 d[4], gv[4], uv[4];
+                dh8(j, d);
+                const uint4 g = *box64(out_g, lane, j), u = *box64(out_u, lane, j);
+                get_pairs(g, gv);
+                get_pairs(u, uv);
+                uint4 dg, du;
+                gated_back8(d, gv, uv, any_low(lowest2(g)), dg, du);
+                *box64(out_g, lane, j) = dg;
+                *box64(out_u, lane, j) = du;
+              }
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-              tma_store_2d(&maps.gate, static_cast<int>(c), m, so);
-              tma_store_2d(&maps.up, static_cast<int>(c), m, so + 2048);
+              tma_store_2d(&maps.gate, static_cast<int>(c), m, out_g);
+              tma_store_2d(&maps.up, static_cast<int>(c), m, out_u);
               bulk_commit();
+            }
+            if (!FLAG && b == 1) {
+              // The next two blocks, as soon as the first two's results have left.
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                if (lane == 0) {
+                  if (k == 0) bulk_wait_read<1>();
+                  else bulk_wait_read<0>();
+                }
+                __syncwarp();
+                if (c + 32 * (k + 1) < p.N) copy_saved16(p, so + 4096 * k, m, c + 32 * (k + 1), lane);
+                copies_commit();
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              v[0][j] = v[1][j];
+              v[1][j] = v[2][j];
+              v[2][j] = v[3][j];
             }
           }
         }
       }
     }
+    if (EPI == kSwigluBack) copies_wait<0>();
     if (lane == 0) bulk_wait<0>();
     tcgen05_fence_before();
   }
@@ -843,12 +1070,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       const int lo = min(issued, other), hi = max(issued, other);
       for (int j = lo; j < hi; ++j) {
         if (issued > other)
-          mbar_complete_tx(&full[j % kPairStages], S::kPairBytes);
+          mbar_complete_tx(&full[j % kStages], S::kPairBytes);
         else
-          mbar_arrive_expect_tx(&full[j % kPairStages], S::kPairBytes);
+          mbar_arrive_expect_tx(&full[j % kStages], S::kPairBytes);
       }
-      for (int j = max(0, hi - kPairStages); j < hi; ++j)
-        mbar_drain(&full[j % kPairStages], static_cast<uint32_t>((j / kPairStages) & 1),
+      for (int j = max(0, hi - kStages); j < hi; ++j)
+        mbar_drain(&full[j % kStages], static_cast<uint32_t>((j / kStages) & 1),
                    100000000ull);
     }
     __syncthreads();
@@ -858,6 +1085,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   if (warp == 1) tmem_dealloc<2>(tmem, 512);
   if (threadIdx.x == 0 && failed) atomicOr(&g_product_watchdog, 1);
 }
+
+// Steps summed in tensor memory at a time, where it matters, at most.  fp32 results: as
+// mx_matmul.  Saved ones: fewer, so that as few of them as of a plain fp32 product's go to the
+// other neighbour in e4m3, or whole blocks to the other scale (5120 steps in one run are 3e-7
+// off in the 2-norm, in two 1.6e-7, a plain fp32 product 1.05e-7).
+constexpr int kRunSteps = 4096, kSavedRunSteps = 2560;
 
 // ---- launches ----------------------------------------------------------------------
 
@@ -894,7 +1127,7 @@ int launch_pair_kernel(const ProductMaps& maps, const ProductParams& p, int num_
   if (tiles > 0x3fffffff) return static_cast<int>(cudaErrorInvalidConfiguration);
   cudaLaunchAttribute at[2];
   const cudaLaunchConfig_t cfg =
-      cluster_config(at, 2 * pairs, kPairThreads, kPairSmem<FP4, EPI>, 2, stream);
+      cluster_config(at, 2 * pairs, kPairThreads<EPI>, kPairSmem<FP4, EPI>, 2, stream);
   return static_cast<int>(cudaLaunchKernelEx(&cfg, pair_kernel<FP4, EPI, FLAG>, maps, p));
 }
 
@@ -911,7 +1144,7 @@ int launch_tile_kernel(const ProductMaps& maps, const ProductParams& p, cudaStre
   if (ctas > 0x7fffffff) return static_cast<int>(cudaErrorInvalidConfiguration);
   cudaLaunchAttribute at[2];
   const cudaLaunchConfig_t cfg =
-      cluster_config(at, ctas, kTileThreads, kSmem, static_cast<unsigned>(p.split), stream);
+      cluster_config(at, ctas, kTileThreads<EPI>, kSmem, static_cast<unsigned>(p.split), stream);
   return static_cast<int>(cudaLaunchKernelEx(&cfg, tile_kernel<FP4, EPI, RUNS>, maps, p));
 }
 

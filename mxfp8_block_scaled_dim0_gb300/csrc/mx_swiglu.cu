@@ -39,26 +39,6 @@ struct SwigluParams {
   Span sp_out, sp_q, sp_s;
 };
 
-__device__ __forceinline__ f32x2 sigmoid2(f32x2 g) {
-  float lo, hi;
-  unpair(g, lo, hi);
-  return pair(sigmoid(lo), sigmoid(hi));
-}
-
-// The largest of words of two bf16 gates each, halves apart.  As unsigned numbers the
-// negative ones lie above the positive ones, in order of their size.
-__device__ __forceinline__ uint32_t lowest2(const uint4& w) {
-  return __vmaxu2(__vmaxu2(w.x, w.y), __vmaxu2(w.z, w.w));
-}
-__device__ __forceinline__ bool any_low(uint32_t lowest) {
-  constexpr uint32_t kBits = 0xC2A0u << 16;              // kLow
-  return lowest > (kBits | 0xFFFFu) || lowest << 16 > kBits;
-}
-
-// Whether a block with this scale byte can hold a gate below kLow: at 2^-3 its largest
-// magnitude, 448, stands for 56.
-__device__ __forceinline__ bool may_be_low(uint32_t sbyte) { return sbyte >= 127 - 2; }
-
 // A warp's place: row r, piece `run` of the row, walked in steps of the whole
 // grid without a division.  Rows in 32 bits (M < 2^31), so that an address is one
 // wide multiplication.

@@ -131,6 +131,15 @@ def test_forward_of_8_bits_with_odd_blocks(M, F, K):
 
 
 @pytest.mark.parametrize("bits", BITS)
+@pytest.mark.parametrize("M,F,K", [(70, 96, 16640), (1, 64, 65536), (200, 128, 8256), (1200, 2080, 8256),
+                                   (2304, 2304, 16640)])
+def test_long_sums_saved(M, F, K, bits):
+    """Contractions in several runs."""
+    forward(M, F, K, bits, True)
+    forward(M, F, K, bits, False)
+
+
+@pytest.mark.parametrize("bits", BITS)
 @pytest.mark.parametrize("M,F", [(40, 256), (2304, 2304)])
 def test_steep_gates(M, F, bits):
     """Gates far beyond where the sigmoid leaves fp32's normal range."""

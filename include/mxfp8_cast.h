@@ -489,7 +489,8 @@ int mx_selftest_watchdog(int64_t wait_ns, void* stream);
  * bulk-staged kernel of mx_cast_rowwise, used for K <= 24576; the tiled
  * kernel of mx_dequant_blocked, used for C >= 1024; the kernels of mx_matmul,
  * mx_matmul_fp4, mx_matmul_swiglu, mx_matmul_swiglu_backward, mx_cast_fp4_dim1,
- * mx_cast_fp4_dim0_dim1, mx_layer_norm and the first of mx_layer_norm_backward).  In that launch the
+ * mx_cast_fp4_dim0_dim1, the tiled ones of mx_cast_fp4_dim0 and mx_dequant_fp4 (used
+ * where there is a tile of 128 x 128 for every SM), mx_layer_norm and the first of mx_layer_norm_backward).  In that launch the
  * thread of CTA 0 that issues its loads waits, at its `at`-th tile (rowwise:
  * step; products: block of 128 contraction bytes; layer norm: row of its first
  * group), on a barrier that nothing completes, for at most `wait_ns` nanoseconds

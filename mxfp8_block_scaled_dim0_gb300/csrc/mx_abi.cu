@@ -704,9 +704,10 @@ int mx_matmul_swiglu(const void* qx, const void* sx_blk, const void* qg, const v
   if (int rc = encode_operand(&maps.a, &maps.sa, qx, sx_blk, M, K, fp4,
                               pairs ? 128 : mx::matmul_box_rows(M, false, 128), 1))
     return rc;
-  if (int rc = encode_operand(&maps.b, &maps.sb, qg, sg_blk, F, K, fp4, pairs ? 128 : 64, 1)) return rc;
-  if (int rc = encode_operand(&maps.b2, &maps.sb2, qu, su_blk, F, K, fp4, pairs ? 128 : 64, 1))
-    return rc;
+  const int cols = mx::matmul_swiglu_tile_cols(M, F, K, fp4, false, sms);
+  const int rows_w = pairs ? 128 : mx::matmul_box_rows(F, false, cols);
+  if (int rc = encode_operand(&maps.b, &maps.sb, qg, sg_blk, F, K, fp4, rows_w, 1)) return rc;
+  if (int rc = encode_operand(&maps.b2, &maps.sb2, qu, su_blk, F, K, fp4, rows_w, 1)) return rc;
   if (int rc = encode_result(&maps.out, h, M, F, false)) return rc;
   maps.gate = maps.up = maps.out;
   if (q0) {
@@ -736,7 +737,7 @@ int mx_matmul_swiglu_backward(const void* qdy, const void* sdy_blk, const void* 
   int sms = 0;
   if (int rc = current_sm_count(&sms)) return rc;
   const bool fp4 = format == MX_E2M1, pairs = mx::product_pairs(M, F, sms);
-  const int cols = mx::matmul_swiglu_back_tile_cols(M, F, K, fp4, sms);
+  const int cols = mx::matmul_swiglu_tile_cols(M, F, K, fp4, true, sms);
   mx::ProductMaps maps;
   if (int rc = encode_operand(&maps.a, &maps.sa, qdy, sdy_blk, M, K, fp4,
                               pairs ? 128 : mx::matmul_box_rows(M, false, 128), 1))

@@ -424,6 +424,14 @@ __global__ void __launch_bounds__(kTileThreads, kTileCtas)
     fence_mbar_init();
     prefetch_tmap(&maps.x);
     if (DIM1) prefetch_tmap(&maps.q1);
+    // While earlier grids finish, ask L2 for the first tiles (a hint: nothing is read).
+    for (int64_t i = 0; i < kStages; ++i) {
+      const int64_t t = blockIdx.x + i * gridDim.x;
+      if (t >= tiles) break;
+      const int m = static_cast<int>(t / p.tiles_k * kTile), k = static_cast<int>(t % p.tiles_k * kTile);
+      tma_prefetch_2d(&maps.x, k, m);
+      tma_prefetch_2d(&maps.x, k + 64, m);
+    }
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   __syncthreads();

@@ -129,8 +129,7 @@ int read_matmul_watchdog(int* out, bool clear);
 // Products with 4-bit operands (mx_matmul_fp4.cu) or joined with the gated SiLU
 // (mx_matmul_swiglu.cu), both by the kernels of mx_product.cuh.  a, b, sa, sb: as in
 // MatmulMaps, a stage's scales (two 512-byte tiles for 4-bit operands) a box.  The forward
-// gated product: b, sb gate and b2, sb2 up, in boxes of 128 rows (pairs) or 64 and of one
-// row tile.  out: as in MatmulMaps, bf16 boxes for the gated product.  gate, up: the
+// gated product: b, sb gate and b2, sb2 up, sb in boxes of one row tile.  out: as in MatmulMaps, bf16 boxes for the gated product.  gate, up: the
 // halves of the rows [gate | up]: boxes of 64 bytes x 32 rows, 64B swizzle, of the saved
 // bytes (forward) or of the gradient in bf16 (backward).
 struct ProductMaps {
@@ -152,7 +151,7 @@ struct MatmulSwigluArgs {
   void* s;
   const void* gu;
 };
-int matmul_swiglu_back_tile_cols(int64_t M, int64_t F, int64_t K, bool fp4, int num_sms);
+int matmul_swiglu_tile_cols(int64_t M, int64_t F, int64_t K, bool fp4, bool backward, int num_sms);
 int launch_matmul_swiglu(const ProductMaps& maps, const MatmulSwigluArgs& a, int num_sms,
                          cudaStream_t stream);
 int launch_matmul_swiglu_backward(const ProductMaps& maps, const MatmulSwigluArgs& a, int num_sms,

@@ -30,9 +30,9 @@ int launch_matmul_fp4(const ProductMaps& maps, int64_t M, int64_t N, int64_t K, 
     p.run = (p.k_blocks + runs - 1) / runs;
     return launch_pair_kernel<true, kPlain, true>(maps, p, num_sms, stream);
   }
-  const TileChoice t = choose_tiles(M, N, p.k_blocks, num_sms);
+  const TileChoice t = choose_tiles(M, N, p.k_blocks, num_sms, 1);
   p.cols = t.cols;
-  p.split = t.split;
+  p.split = p.cluster = t.split;
   p.m_tiles = static_cast<int>((M + 127) / 128);
   p.n_tiles = static_cast<int>((N + t.cols - 1) / t.cols);
   p.load_bytes = (matmul_box_rows(M, false, 128) + matmul_box_rows(N, false, t.cols)) * kBoxCols +
@@ -44,7 +44,7 @@ int launch_matmul_fp4(const ProductMaps& maps, int64_t M, int64_t N, int64_t K, 
 }
 
 int matmul_fp4_tile_cols(int64_t M, int64_t N, int64_t K, int num_sms) {
-  return choose_tiles(M, N, (K + 255) / 256, num_sms).cols;
+  return choose_tiles(M, N, (K + 255) / 256, num_sms, 1).cols;
 }
 
 int out_of_bounds_matmul_fp4(bool clear) { return read_out_of_bounds(clear); }

@@ -23,13 +23,14 @@ int launch_forward(const ProductMaps& maps, ProductParams& p, int num_sms,
     return p.q ? launch_pair_kernel<FP4, kSwiglu, true>(maps, p, num_sms, stream)
                : launch_pair_kernel<FP4, kSwiglu, false>(maps, p, num_sms, stream);
   }
-  const TileChoice t = choose_tiles(p.M, 2 * p.N, p.k_blocks, num_sms, 128);
+  const TileChoice t = choose_tiles(p.M, p.N, p.k_blocks, num_sms, 2);
   p.cols = t.cols;
   p.split = t.split;
+  p.cluster = 2 * t.split;
   p.m_tiles = static_cast<int>((p.M + 127) / 128);
-  p.n_tiles = static_cast<int>((2 * p.N + t.cols - 1) / t.cols);
-  p.load_bytes = (matmul_box_rows(p.M, false, 128) + t.cols) * kBoxCols +
-                 3 * Shape<FP4, kSwiglu>::kSf * kSfBytes;
+  p.n_tiles = static_cast<int>((p.N + t.cols - 1) / t.cols);
+  p.load_bytes = (matmul_box_rows(p.M, false, 128) + matmul_box_rows(p.N, false, t.cols)) * kBoxCols +
+                 2 * Shape<FP4, kSwiglu>::kSf * kSfBytes;
   p.run = kRun;
   return p.q && (p.k_blocks + p.split - 1) / p.split > kRun
              ? launch_tile_kernel<FP4, kSwiglu, true>(maps, p, stream)
@@ -44,9 +45,9 @@ int launch_backward(const ProductMaps& maps, ProductParams& p, int num_sms, cuda
     return p.q ? launch_pair_kernel<FP4, kSwigluBack, true>(maps, p, num_sms, stream)
                : launch_pair_kernel<FP4, kSwigluBack, false>(maps, p, num_sms, stream);
   }
-  const TileChoice t = choose_tiles(p.M, p.N, p.k_blocks, num_sms);
+  const TileChoice t = choose_tiles(p.M, p.N, p.k_blocks, num_sms, 1);
   p.cols = t.cols;
-  p.split = t.split;
+  p.split = p.cluster = t.split;
   p.m_tiles = static_cast<int>((p.M + 127) / 128);
   p.n_tiles = static_cast<int>((p.N + t.cols - 1) / t.cols);
   p.load_bytes = (matmul_box_rows(p.M, false, 128) + matmul_box_rows(p.N, false, t.cols)) * kBoxCols +
@@ -69,8 +70,8 @@ ProductParams params_of(const MatmulSwigluArgs& a) {
 
 }  // namespace
 
-int matmul_swiglu_back_tile_cols(int64_t M, int64_t F, int64_t K, bool fp4, int num_sms) {
-  return choose_tiles(M, F, (K + (fp4 ? 255 : 127)) / (fp4 ? 256 : 128), num_sms).cols;
+int matmul_swiglu_tile_cols(int64_t M, int64_t F, int64_t K, bool fp4, bool backward, int num_sms) {
+  return choose_tiles(M, F, (K + (fp4 ? 255 : 127)) / (fp4 ? 256 : 128), num_sms, backward ? 1 : 2).cols;
 }
 
 int launch_matmul_swiglu(const ProductMaps& maps, const MatmulSwigluArgs& a, int num_sms,

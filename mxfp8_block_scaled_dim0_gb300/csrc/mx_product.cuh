@@ -14,7 +14,9 @@
 // ahead of the MMAs; the epilogue warps take a tile's results into registers at once, and
 // the next tile's MMAs run while they work on them.
 // tile_kernel: 128 x 128 (or 64) results by a cluster of S CTAs that share the
-// contraction; each sums and finishes 128 / S of the tile's rows, in rank order.
+// contraction; each sums and finishes 128 / S of the tile's rows, in rank order.  kSwiglu: 2 S
+// CTAs, every other one on gate and on up (both in one CTA, as two MMAs of 64 columns, took
+// 12.0 us where one MMA of 128 takes 10.3: 44 MB of weights for one token).
 //
 // What happens to the results (EPI):
 //   kPlain       out = P in bf16 or fp32
@@ -54,9 +56,7 @@ struct Shape {
   // One row tile of A's scales, two of B's.
   static constexpr int kPairBytes = 2 * kBoxBytes + 3 * kSf * kSfBytes;
   static constexpr int kPairStride = (kPairBytes + 1023) / 1024 * 1024;
-  // B's row tiles of scales in the tile kernel: one, or gate's and up's.
-  static constexpr int kTileSfRows = EPI == kSwiglu ? 2 : 1;
-  static constexpr int kTileBytes = 2 * kBoxBytes + (1 + kTileSfRows) * kSf * kSfBytes;
+  static constexpr int kTileBytes = 2 * kBoxBytes + 2 * kSf * kSfBytes;
   static constexpr int kTileStride = (kTileBytes + 1023) / 1024 * 1024;
 };
 
@@ -67,12 +67,13 @@ struct ProductParams {
   int last_mmas;       // of the last stage, 1..4
   int m_tiles, n_tiles;
   int split;           // CTAs of a cluster along the contraction (tile kernel)
+  int cluster;         // of the tile kernel: split, or twice that (kSwiglu)
   int out_f32;
   int run;             // stages summed in tensor memory at a time, at most
   int band;            // M-tiles of a band (pair kernel)
   int mapped;          // maps.out describes the result's rows
   int load_bytes;      // of a stage (tile kernel)
-  int cols;            // of a tile, 64 or 128 (tile kernel; kSwiglu: 128, gate and up)
+  int cols;            // of a tile, 64 or 128 (tile kernel)
   // The gated SiLU's saved input: written (kSwiglu, or null) or read (kSwigluBack: q and s,
   // or gu).
   uint8_t* q;
@@ -122,22 +123,26 @@ template <int EPI>
 constexpr int kTileThreads = EPI == kPlain ? 192 : 320;
 constexpr int kPitch = 132;                 // floats a row of the partial tile
 
-// Sums of eight neighbouring columns over the cluster's partial tiles, in rank order; the
-// loads of all CTAs' values are under way before the first is added.
-__device__ __forceinline__ void cluster_sum8(const float* part, int split, float (&v)[8]) {
+// Sums of eight neighbouring columns over the partial tiles of the cluster's CTAs first,
+// first + step .., in rank order; the loads of all values are under way before the first is
+// added.
+template <int STEP>
+__device__ __forceinline__ void cluster_sum8(const float* part, int split, uint32_t first,
+                                             float (&v)[8]) {
+  constexpr int kMost = 8 / STEP;
   const uint32_t at = smem_u32(part);
-  float4 lo[8], hi[8];
+  float4 lo[kMost], hi[kMost];
 #pragma unroll
-  for (int q = 0; q < 8; ++q)
+  for (int q = 0; q < kMost; ++q)
     if (q < split) {
-      const uint32_t a = map_to_rank(at, static_cast<uint32_t>(q));
+      const uint32_t a = map_to_rank(at, first + STEP * q);
       lo[q] = ld_cluster_f4(a);
       hi[q] = ld_cluster_f4(a + 16);
     }
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] = 0.0f;
 #pragma unroll
-  for (int q = 0; q < 8; ++q)
+  for (int q = 0; q < kMost; ++q)
     if (q < split) {
       v[0] += lo[q].x; v[1] += lo[q].y; v[2] += lo[q].z; v[3] += lo[q].w;
       v[4] += hi[q].x; v[5] += hi[q].y; v[6] += hi[q].z; v[7] += hi[q].w;
@@ -216,14 +221,16 @@ __global__ void __launch_bounds__(kTileThreads<EPI>, 1)
   uint8_t* ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_rank());
-  const int tile = blockIdx.x / p.split;
-  // kSwiglu: a tile's columns are half gate, half up.
-  const int width = EPI == kSwiglu ? p.cols / 2 : p.cols;
-  const int mt = tile % p.m_tiles, n0 = tile / p.m_tiles * width;
+  // kSwiglu: gate in the even CTAs of a cluster, up in the odd ones.
+  constexpr int kHalves = EPI == kSwiglu ? 2 : 1;
+  const bool up = EPI == kSwiglu && (rank & 1);
+  const int share = rank / kHalves;           // of the contraction
+  const int tile = blockIdx.x / p.cluster;
+  const int mt = tile % p.m_tiles, n0 = tile / p.m_tiles * p.cols;
   // Stages of this CTA: equal shares, the first ones one longer.
   const int per = p.k_blocks / p.split, more = p.k_blocks % p.split;
-  const int kb0 = rank * per + (rank < more ? rank : more);
-  const int nkb = per + (rank < more ? 1 : 0);
+  const int kb0 = share * per + (share < more ? share : more);
+  const int nkb = per + (share < more ? 1 : 0);
   const int runs = RUNS ? (nkb + p.run - 1) / p.run : 1;
   auto run_end = [&](int r) { return static_cast<int>(static_cast<int64_t>(nkb) * (r + 1) / runs); };
   constexpr uint32_t kTmemCols = RUNS ? 512 : 256;
@@ -243,13 +250,9 @@ __global__ void __launch_bounds__(kTileThreads<EPI>, 1)
     abort_flag = 0;
     fence_mbar_init();
     prefetch_tmap(&maps.a);
-    prefetch_tmap(&maps.b);
     prefetch_tmap(&maps.sa);
-    prefetch_tmap(&maps.sb);
-    if (EPI == kSwiglu) {
-      prefetch_tmap(&maps.b2);
-      prefetch_tmap(&maps.sb2);
-    }
+    prefetch_tmap(up ? &maps.b2 : &maps.b);
+    prefetch_tmap(up ? &maps.sb2 : &maps.sb);
   }
   if (warp == 1) tmem_alloc<1>(&tmem_base, kTmemCols);
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -257,8 +260,8 @@ __global__ void __launch_bounds__(kTileThreads<EPI>, 1)
   __syncthreads();
   tcgen05_fence_after();
   const uint32_t tmem = tmem_base;
-  // Scales: A's, B's (gate's), up's, for either half of a 4-bit stage.
-  const uint32_t t_sfa = tmem + kTmemCols / 2, t_sfb = t_sfa + 4 * S::kSf, t_sfu = t_sfb + 4 * S::kSf;
+  // Scales, A's and B's, for either half of a 4-bit stage.
+  const uint32_t t_sfa = tmem + kTmemCols / 2, t_sfb = t_sfa + 4 * S::kSf;
   const int quarter = warp & 3;
   const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
   // This lane's row of the runs before the last: an epilogue warp's share of the columns.
@@ -268,6 +271,7 @@ __global__ void __launch_bounds__(kTileThreads<EPI>, 1)
 
   if (warp == 0) {
     if (elect_one()) {
+      const CUtensorMap *map_b = up ? &maps.b2 : &maps.b, *map_sb = up ? &maps.sb2 : &maps.sb;
       int i = 0, s = 0;
       uint32_t turn = 0;                     // of the ring, mod 2
       for (; i < nkb; ++i) {
@@ -282,13 +286,9 @@ __global__ void __launch_bounds__(kTileThreads<EPI>, 1)
         constexpr int kSfTile = S::kSf * kSfBytes;
         mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(p.load_bytes));
         tma_load_2d(st, &maps.a, x, mt * kBoxRows, &full[s]);
-        tma_load_2d(st + kBoxBytes, &maps.b, x, n0, &full[s]);
+        tma_load_2d(st + kBoxBytes, map_b, x, n0, &full[s]);
         tma_load_2d(sf, &maps.sa, sx, mt, &full[s]);
-        tma_load_2d(sf + kSfTile, &maps.sb, sx, n0 / kBoxRows, &full[s]);
-        if (EPI == kSwiglu) {
-          tma_load_2d(st + kBoxBytes + kBoxBytes / 2, &maps.b2, x, n0, &full[s]);
-          tma_load_2d(sf + 2 * kSfTile, &maps.sb2, sx, n0 / kBoxRows, &full[s]);
-        }
+        tma_load_2d(sf + kSfTile, map_sb, sx, n0 / kBoxRows, &full[s]);
         if (++s == kTileStages) {
           s = 0;
           turn ^= 1u;
@@ -301,13 +301,11 @@ __global__ void __launch_bounds__(kTileThreads<EPI>, 1)
     }
   } else if (warp == 1) {
     if (elect_one()) {
-      const uint32_t idesc = idesc_of<FP4>(128, width);
-      // The scales of 32 rows of B take a column of tensor memory: 64 columns read the first
-      // or the last two of their rows' four.  (Never an odd one: an MMA of 32 columns whose
-      // scales began there ended in a misaligned address.)
+      const uint32_t idesc = idesc_of<FP4>(128, p.cols);
+      // The scales of 32 rows of B take a column of tensor memory: a tile of 64 columns reads
+      // the first or the last two of its rows' four.  (Never begin at an odd one: an MMA of 32
+      // columns that did ended in a misaligned address.)
       const uint32_t t_sfb_here = t_sfb + (n0 % kBoxRows) / 32;
-      const uint32_t t_sfu_here = t_sfu + (n0 % kBoxRows) / 32;
-      constexpr uint32_t kUpBox = kBoxBytes / 2 >> 4;
       int s = 0;
       uint32_t turn = 0;
       int run = 0, begin = 0, end = run_end(0);     // this run and its stages
@@ -330,8 +328,6 @@ __global__ void __launch_bounds__(kTileThreads<EPI>, 1)
         for (int j = 0; j < S::kSf; ++j) {
           tcgen05_cp_scales<1>(t_sfa + 4 * j, scale_desc(sf + j * kSfBytes));
           tcgen05_cp_scales<1>(t_sfb + 4 * j, scale_desc(sf + (S::kSf + j) * kSfBytes));
-          if (EPI == kSwiglu)
-            tcgen05_cp_scales<1>(t_sfu + 4 * j, scale_desc(sf + (2 * S::kSf + j) * kSfBytes));
         }
         const uint64_t da = operand_desc(st), db = operand_desc(st + kBoxBytes);
         const int mmas = kb0 + i == p.k_blocks - 1 ? p.last_mmas : 4;
@@ -341,9 +337,6 @@ __global__ void __launch_bounds__(kTileThreads<EPI>, 1)
             const int j = FP4 ? k >> 1 : 0;
             mma<FP4, 1>(d, da + kStepK * k, db + kStepK * k, idesc, k, t_sfa + 4 * j,
                         t_sfb_here + 4 * j, i > begin || k > 0);
-            if (EPI == kSwiglu)
-              mma<FP4, 1>(d + 64, da + kStepK * k, db + kUpBox + kStepK * k, idesc, k, t_sfa + 4 * j,
-                          t_sfu_here + 4 * j, i > begin || k > 0);
           }
         tcgen05_commit<1>(&empty[s]);
         if (++s == kTileStages) {
@@ -358,7 +351,7 @@ __global__ void __launch_bounds__(kTileThreads<EPI>, 1)
     // The tile's gates and ups into L2: whole rows by the warp, 128 bytes a lane.
     const int size = p.q ? 1 : 2;
     const uint8_t* from = p.q ? p.q : reinterpret_cast<const uint8_t*>(p.gu);
-    const int64_t left = p.N - n0 < width ? p.N - n0 : width;
+    const int64_t left = p.N - n0 < p.cols ? p.N - n0 : p.cols;
     const int lines = static_cast<int>((left * size + 127) / 128);        // of a half row: 1 or 2
     const int64_t m1 = static_cast<int64_t>(mt) * kBoxRows + rank * (kBoxRows / p.split);
     for (int i = threadIdx.x - 64; i < kBoxRows / p.split * 2 * lines; i += kTileThreads<EPI> - 64) {
@@ -393,15 +386,14 @@ __global__ void __launch_bounds__(kTileThreads<EPI>, 1)
   const bool ok = abort_flag == 0;
   const uint32_t last = tmem + lanes + ((runs - 1) & 1) * kBoxRows;
   // Rows of the tile that this CTA finishes, in pieces of eight columns.
-  const int rows = kBoxRows / p.split;
+  const int rows = kBoxRows / p.cluster;
   const int64_t m0 = static_cast<int64_t>(mt) * kBoxRows + rank * rows;
-  const int pieces = width >> 3, shift = 31 - __clz(pieces);
+  const int pieces = p.cols >> 3, shift = 31 - __clz(pieces);
   const int total = m0 < p.M ? static_cast<int>(p.M - m0 < rows ? p.M - m0 : rows) << shift : 0;
   float* part = reinterpret_cast<float*>(ring);
   if (warp >= 2 && static_cast<int64_t>(mt) * kBoxRows + quarter * 32 < p.M) {
     const int row = quarter * 32 + lane;
     constexpr int kUnroll = RUNS ? 4 : 1;      // sums are registers: c must be a constant
-    // kSwiglu: gate in columns 0 .., up in 64 ..
 #pragma unroll kUnroll
     for (int c1 = 0; c1 < kShare; c1 += 32) {
       const int c = c0 + c1;
@@ -440,7 +432,7 @@ __global__ void __launch_bounds__(kTileThreads<EPI>, 1)
           const int64_t m = m0 + r, n = n0 + c;
           if (i >= total || n >= p.N) continue;
           float v[8];
-          cluster_sum8(part + (rank * rows + r) * kPitch + c, p.split, v);
+          cluster_sum8<1>(part + (rank * rows + r) * kPitch + c, p.split, 0, v);
           f32x2 d[4], g[4], u[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) d[j] = pair(v[2 * j], v[2 * j + 1]);
@@ -461,7 +453,7 @@ __global__ void __launch_bounds__(kTileThreads<EPI>, 1)
       const bool in = i0 + lane < total && n < p.N;
       const float* at = part + (rank * rows + r) * kPitch + c;
       float v[8];
-      cluster_sum8(at, p.split, v);
+      cluster_sum8<kHalves>(at, p.split, 0, v);
       if constexpr (EPI == kPlain) {
         const bool vec = (p.N & 7) == 0;
         if (in)
@@ -469,7 +461,7 @@ __global__ void __launch_bounds__(kTileThreads<EPI>, 1)
                      vec ? 8 : static_cast<int>(p.N - n < 8 ? p.N - n : 8), vec, p.sp_out);
       } else if constexpr (EPI == kSwiglu) {
         float u[8];
-        cluster_sum8(at + 64, p.split, u);
+        cluster_sum8<kHalves>(at, p.split, 1, u);
         f32x2 g2[4], u2[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -1140,31 +1132,33 @@ int launch_tile_kernel(const ProductMaps& maps, const ProductParams& p, cudaStre
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
   });
   if (attr != 0) return attr;
-  const int64_t ctas = static_cast<int64_t>(p.m_tiles) * p.n_tiles * p.split;
+  const int64_t ctas = static_cast<int64_t>(p.m_tiles) * p.n_tiles * p.cluster;
   if (ctas > 0x7fffffff) return static_cast<int>(cudaErrorInvalidConfiguration);
   cudaLaunchAttribute at[2];
   const cudaLaunchConfig_t cfg =
-      cluster_config(at, ctas, kTileThreads<EPI>, kSmem, static_cast<unsigned>(p.split), stream);
+      cluster_config(at, ctas, kTileThreads<EPI>, kSmem, static_cast<unsigned>(p.cluster), stream);
   return static_cast<int>(cudaLaunchKernelEx(&cfg, tile_kernel<FP4, EPI, RUNS>, maps, p));
 }
 
-// The tile kernel's tiles: columns of B a tile, and CTAs that share its contraction; the
-// quickest as reckoned in ns (tile_shape in mx_matmul.cu has the measurements).
+// The tile kernel's tiles: columns, and CTAs that share the contraction; the quickest as
+// reckoned in ns (tile_shape in mx_matmul.cu has the measurements).  halves: clusters of twice
+// the CTAs, gate and up (kSwiglu).
 struct TileChoice {
   int cols, split;
 };
 
-inline TileChoice choose_tiles(int64_t M, int64_t rows_b, int64_t k_blocks, int num_sms,
-                               int least_cols = 64) {
+inline TileChoice choose_tiles(int64_t M, int64_t N, int64_t k_blocks, int num_sms, int halves) {
   TileChoice best = {128, 1};
   int64_t least = INT64_MAX;
-  for (int cols = 128; cols >= least_cols; cols /= 2) {
-    const int64_t tiles = (M + 127) / 128 * ((rows_b + cols - 1) / cols);
-    for (int s = 1; s <= 8 && s <= k_blocks; s *= 2) {
-      if (s > 1 && tiles * s > (s == 8 ? 96 : s == 4 ? 128 : num_sms)) break;
-      const int64_t rounds = (tiles * s + num_sms - 1) / num_sms;
+  for (int cols = 128; cols >= 64; cols /= 2) {
+    const int64_t tiles = (M + 127) / 128 * ((N + cols - 1) / cols);
+    for (int s = 1; s * halves <= 8 && s <= k_blocks; s *= 2) {
+      const int cluster = s * halves;
+      const int64_t ctas = tiles * cluster;
+      if (s > 1 && ctas > (cluster == 8 ? 96 : cluster == 4 ? 128 : num_sms)) break;
+      const int64_t rounds = (ctas + num_sms - 1) / num_sms;
       const int64_t cost = rounds * (500 + (cols == 128 ? 500 : 0) + (k_blocks + s - 1) / s * 220 +
-                                     (s > 1 ? 400 + 19 * (M < 128 ? M : 128) * cols / 128 : 0));
+                                     (cluster > 1 ? 400 + 19 * (M < 128 ? M : 128) * cols / 128 : 0));
       if (cost < least) {
         least = cost;
         best = {cols, s};
@@ -1183,7 +1177,7 @@ inline ProductParams product_params(int64_t M, int64_t N, int64_t K, bool fp4) {
   p.last_mmas = static_cast<int>((K - (p.k_blocks - 1) * steps + mma_steps - 1) / mma_steps);
   p.run = p.k_blocks;
   p.band = 8;
-  p.split = 1;
+  p.split = p.cluster = 1;
   const Stall stall = take_stall();
   p.stall_at = stall.at;
   p.stall_ns = stall.ns;

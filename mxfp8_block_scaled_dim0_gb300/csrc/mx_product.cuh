@@ -129,6 +129,12 @@ constexpr int kPitch = 132;                 // floats a row of the partial tile
 template <int STEP>
 __device__ __forceinline__ void cluster_sum8(const float* part, int split, uint32_t first,
                                              float (&v)[8]) {
+  if (STEP == 1 && split == 1) {               // this CTA's own
+    const float4 a = reinterpret_cast<const float4*>(part)[0], b = reinterpret_cast<const float4*>(part)[1];
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    return;
+  }
   constexpr int kMost = 8 / STEP;
   const uint32_t at = smem_u32(part);
   float4 lo[kMost], hi[kMost];
@@ -413,18 +419,25 @@ __global__ void __launch_bounds__(kTileThreads<EPI>, 1)
   }
   cluster_sync();
   if constexpr (EPI == kSwigluBack) {
-    // Two pieces a thread at a time: their gates and ups, asked into L2 while the MMAs went
-    // on, are under way together.
-    constexpr int kFew = 2;
-    if (ok)
-      for (int i0 = threadIdx.x; i0 < total; i0 += kFew * kTileThreads<EPI>) {
-        Saved8 w[kFew];
+    // Two pieces a thread at a time, their gates and ups (asked into L2 while the MMAs went
+    // on) a step ahead of the work.
+    constexpr int kFew = 2, kStep = kFew * kTileThreads<EPI>;
+    struct Few {
+      Saved8 w[kFew];
+    } next;
+    auto load = [&](int i0) {
 #pragma unroll
-        for (int k = 0; k < kFew; ++k) {
-          const int i = i0 + k * kTileThreads<EPI>;
-          const int64_t m = m0 + (i >> shift), n = n0 + (i & (pieces - 1)) * 8;
-          if (i < total && n < p.N) w[k].load(p, m, n);
-        }
+      for (int k = 0; k < kFew; ++k) {
+        const int i = i0 + k * kTileThreads<EPI>;
+        const int64_t m = m0 + (i >> shift), n = n0 + (i & (pieces - 1)) * 8;
+        if (i < total && n < p.N) next.w[k].load(p, m, n);
+      }
+    };
+    load(threadIdx.x);
+    if (ok)
+      for (int i0 = threadIdx.x; i0 < total; i0 += kStep) {
+        const Few now = next;
+        load(i0 + kStep);
 #pragma unroll
         for (int k = 0; k < kFew; ++k) {
           const int i = i0 + k * kTileThreads<EPI>;
@@ -436,7 +449,7 @@ __global__ void __launch_bounds__(kTileThreads<EPI>, 1)
           f32x2 d[4], g[4], u[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) d[j] = pair(v[2 * j], v[2 * j + 1]);
-          const bool low = w[k].get(p, g, u);
+          const bool low = now.w[k].get(p, g, u);
           uint4 dg, du;
           gated_back8(d, g, u, low, dg, du);
           uint16_t* out = static_cast<uint16_t*>(p.out) + m * 2 * p.N + n;

@@ -225,18 +225,20 @@ int cast_fp4(const void* x, int64_t M, int64_t K, void* q0, void* s0_blk, void* 
       !aligned(s1_blk, 16))
     return MX_ERR_ALIGN;
   if (int rc = check_device({x, q0, s0_blk, q1, s1_blk})) return rc;
+  int sms = 0;
+  if (int rc = current_sm_count(&sms)) return rc;
   mx::CastFp4Maps maps;
-  if (int rc = encode_2d(&maps.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x, K, M, K * 2, 64, 128,
-                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
-    return rc;
-  maps.q1 = maps.x;
+  if (q1 || mx::cast_fp4_tiles(M, K, sms)) {
+    if (int rc = encode_2d(&maps.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x, K, M, K * 2, 64, 128,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
+      return rc;
+    maps.q1 = maps.x;
+  }
   if (q1) {
     if (int rc = encode_2d(&maps.q1, CU_TENSOR_MAP_DATA_TYPE_UINT8, q1, M / 2, K, M / 2, 64, 128,
                            CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_SWIZZLE_64B))
       return rc;
   }
-  int sms = 0;
-  if (int rc = current_sm_count(&sms)) return rc;
   return launch_rc(mx::launch_cast_fp4(&maps, x, M, K, q0, s0_blk, s1_blk, sms,
                                        static_cast<cudaStream_t>(stream)));
 }
@@ -647,13 +649,15 @@ int mx_dequant_fp4(const void* q, int64_t R, int64_t C, const void* s_blk, void*
   int sms = 0;
   if (int rc = current_sm_count(&sms)) return rc;
   mx::DequantFp4Maps maps;
-  if (int rc = encode_2d(&maps.q, CU_TENSOR_MAP_DATA_TYPE_UINT8, q, C / 2, R, C / 2, 64, 128,
-                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_SWIZZLE_NONE))
-    return rc;
-  if (int rc = encode_2d(&maps.out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, out, C, R, 2 * C, 64, 128,
-                         CU_TENSOR_MAP_L2_PROMOTION_NONE))
-    return rc;
-  return launch_rc(mx::launch_dequant_fp4(maps, q, R, C, s_blk, out, sms, static_cast<cudaStream_t>(stream)));
+  if (mx::dequant_fp4_tiles(R, C, sms)) {
+    if (int rc = encode_2d(&maps.q, CU_TENSOR_MAP_DATA_TYPE_UINT8, q, C / 2, R, C / 2, 64, 128,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_SWIZZLE_NONE))
+      return rc;
+    if (int rc = encode_2d(&maps.out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, out, C, R, 2 * C, 64, 128,
+                           CU_TENSOR_MAP_L2_PROMOTION_NONE))
+      return rc;
+  }
+  return launch_rc(mx::launch_dequant_fp4(&maps, q, R, C, s_blk, out, sms, static_cast<cudaStream_t>(stream)));
 }
 
 int mx_matmul_fp4(const void* qa, const void* sa_blk, const void* qb, const void* sb_blk, int64_t M,

@@ -13,8 +13,8 @@
 // staging tile by a TMA store.  A tile gives one 512-byte scale tile a direction.
 // dequant_tile_kernel: 128 x 128 tiles too, in four stages and out through two staging tiles,
 // two CTAs an SM; dequant_kernel: eight values a thread, four of these under way at once.
-// All are bound by memory: 16640 x 5120 both directions 44 us (0.88 of the copy bandwidth),
-// dim1 34.6 (0.92), dim0 34.6 (0.92), dequantisation 37.0 (0.86), 8192 x 5120 17.3 (0.90).
+// All are bound by memory: 16640 x 5120 both directions 40.3 us (0.96 of the copy bandwidth),
+// dim1 33.6 (0.95), dim0 33.5 (0.95), dequantisation 36.3 (0.88), 8192 x 5120 17.3 (0.90).
 #include <cuda_runtime.h>
 
 #include "mx_common.cuh"
@@ -583,14 +583,24 @@ int launch_tiles(const CastFp4Maps& maps, const TileParams& p, int num_sms, cuda
 
 }  // namespace
 
+// Rows alone: tiles as soon as there is one for every SM (16640 x 5120 45.2 us in rows, 33.5 in
+// tiles, 512 x 5120 4.0 and 3.2; 128 x 5120, 40 tiles, 1.9 and 2.0).
+bool cast_fp4_tiles(int64_t M, int64_t K, int num_sms) {
+  return (M + 127) / 128 * ((K + 127) / 128) >= num_sms;
+}
+
+// Tiles as soon as there is one for every SM and none is half empty (16640 x 5120 46.9 us in
+// rows, 36.3 in tiles, 512 x 5120 3.9 and 3.6; 128 x 5120 1.8 and 2.9, 100000 x 64 5.5 and 6.2).
+bool dequant_fp4_tiles(int64_t R, int64_t C, int num_sms) {
+  return cast_fp4_tiles(R, C, num_sms) && C > 64;
+}
+
 int launch_cast_fp4(const CastFp4Maps* maps, const void* x, int64_t M, int64_t K, void* q0, void* s0,
                     void* s1, int num_sms, cudaStream_t stream) {
   const uint64_t values = static_cast<uint64_t>(M) * static_cast<uint64_t>(K);
   const int64_t m4 = (M + 127) / 128 * 128, k4 = (K + 127) / 128 * 128;
   const int64_t c = K / 32, c4 = (c + 3) / 4 * 4;
-  // Rows alone: tiles as soon as there is one for every SM (16640 x 5120 45.2 us in rows, 34.6
-  // in tiles, 512 x 5120 4.0 and 3.2; 128 x 5120, 40 tiles, 1.9 and 2.0).
-  if (!s1 && m4 / 128 * (k4 / 128) < num_sms) {
+  if (!s1 && !cast_fp4_tiles(M, K, num_sms)) {
     RowsParams p = {static_cast<const uint16_t*>(x), static_cast<uint8_t*>(q0),
                     static_cast<uint8_t*>(s0), M, K, pieces_of(M, K), static_cast<int>(c),
                     static_cast<int>(c4), make_span(q0, values / 2),
@@ -616,16 +626,13 @@ int launch_cast_fp4(const CastFp4Maps* maps, const void* x, int64_t M, int64_t K
             : launch_tiles<false, true>(*maps, p, num_sms, stream);
 }
 
-int launch_dequant_fp4(const DequantFp4Maps& maps, const void* q, int64_t R, int64_t C, const void* s_blk, void* out, int num_sms,
+int launch_dequant_fp4(const DequantFp4Maps* maps, const void* q, int64_t R, int64_t C, const void* s_blk, void* out, int num_sms,
                        cudaStream_t stream) {
-  // Tiles as soon as there is one for every SM and none is half empty (16640 x 5120 46.9 us in
-  // rows, 37.0 in tiles, 512 x 5120 3.9 and 3.6; 128 x 5120 1.8 and 2.9, 100000 x 64 5.5 and
-  // 6.2).
-  const int64_t tiles_c = (C + 127) / 128, tiles = (R + 127) / 128 * tiles_c;
-  if (tiles >= num_sms && C > 64) {
+  if (dequant_fp4_tiles(R, C, num_sms)) {
+    const int64_t tiles_c = (C + 127) / 128, tiles = (R + 127) / 128 * tiles_c;
     const Stall stall = take_stall();
     const DqTileParams t = {static_cast<const uint8_t*>(s_blk), R, C, tiles_c, tiles, stall.at, stall.ns};
-    return launch_dequant_tiles(maps, t, num_sms, stream);
+    return launch_dequant_tiles(*maps, t, num_sms, stream);
   }
   DequantParams p = {static_cast<const uint8_t*>(q), static_cast<const uint8_t*>(s_blk),
                      static_cast<uint16_t*>(out), R, C, pieces_of(R, C),

@@ -159,7 +159,8 @@ int launch_matmul_swiglu_backward(const ProductMaps& maps, const MatmulSwigluArg
 int read_matmul_swiglu_watchdog(int* out, bool clear);
 int out_of_bounds_matmul_swiglu(bool clear);
 // MX-FP4 casts and dequantisation (mx_fp4.cu).  q0 / s0 null: dim1 only; q1 / s1 null:
-// dim0 only.  x, out: boxes of 64 columns x 128 rows, 128B swizzle; q1: boxes of 64 bytes x
+// dim0 only, which needs its maps only where cast_fp4_tiles(), as dequantisation where
+// dequant_fp4_tiles().  x, out: boxes of 64 columns x 128 rows, 128B swizzle; q1: boxes of 64 bytes x
 // 128 rows, 64B swizzle; q: the same without a swizzle.
 struct CastFp4Maps {
   CUtensorMap x, q1;
@@ -169,7 +170,9 @@ struct DequantFp4Maps {
 };
 int launch_cast_fp4(const CastFp4Maps* maps, const void* x, int64_t M, int64_t K, void* q0, void* s0,
                     void* s1, int num_sms, cudaStream_t stream);
-int launch_dequant_fp4(const DequantFp4Maps& maps, const void* q, int64_t R, int64_t C, const void* s_blk, void* out, int num_sms,
+bool cast_fp4_tiles(int64_t M, int64_t K, int num_sms);
+bool dequant_fp4_tiles(int64_t R, int64_t C, int num_sms);
+int launch_dequant_fp4(const DequantFp4Maps* maps, const void* q, int64_t R, int64_t C, const void* s_blk, void* out, int num_sms,
                        cudaStream_t stream);
 int read_fp4_watchdog(int* out, bool clear);
 int out_of_bounds_fp4(bool clear);

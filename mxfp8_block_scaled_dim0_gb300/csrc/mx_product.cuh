@@ -520,6 +520,7 @@ template <int EPI>
 constexpr int kFirstEpilogueWarp = EPI == kSwigluBack ? 4 : 2;
 template <int EPI>
 constexpr int kPairThreads = 32 * (kFirstEpilogueWarp<EPI> + 8);
+constexpr int kGiven = 56, kTaken = 224;
 template <int REGS>
 __device__ __forceinline__ void give_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
@@ -661,7 +662,7 @@ __global__ void __launch_bounds__(kPairThreads<EPI>, 1)
   // One branch a warpgroup, so that the compiler sees which registers either has.
   constexpr int kFirst = kFirstEpilogueWarp<EPI>;
   if (warp < kFirst) {
-    if (EPI == kSwigluBack) give_registers<56>();
+    if (EPI == kSwigluBack) give_registers<kGiven>();
     if (warp == 0) {
       if (elect_one()) {
         int i = 0;
@@ -754,7 +755,7 @@ __global__ void __launch_bounds__(kPairThreads<EPI>, 1)
       }
     }
   } else {
-    if (EPI == kSwigluBack) take_registers<224>();
+    if (EPI == kSwigluBack) take_registers<kTaken>();
     // A quarter of the lanes, and a share of the columns.
     const int quarter = warp & 3, share = (warp - kFirst) >> 2;
     uint8_t* so = stage_out + (warp - kFirst) * kWarpStage<EPI>;
@@ -1122,6 +1123,11 @@ int launch_pair_kernel(const ProductMaps& maps, const ProductParams& p, int num_
                        cudaStream_t stream) {
   static DeviceCache attr_cache;
   const int attr = attr_cache.get([] {
+    // The warpgroups' shares must be there at launch: one that asked for more would wait.
+    cudaFuncAttributes fa;
+    if (const cudaError_t e = cudaFuncGetAttributes(&fa, pair_kernel<FP4, EPI, FLAG>)) return static_cast<int>(e);
+    if (EPI == kSwigluBack && fa.numRegs * kPairThreads<EPI> < 128 * kGiven + 256 * kTaken)
+      return static_cast<int>(cudaErrorInvalidConfiguration);
     return static_cast<int>(cudaFuncSetAttribute(pair_kernel<FP4, EPI, FLAG>,
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  kPairSmem<FP4, EPI>));

@@ -557,8 +557,25 @@ __device__ __forceinline__ uint4* box64(uint8_t* box, int lane, int j) {
 //           block's dg goes out through 2 KB behind them, its du through the block's own.
 //   bf16:   two blocks of 4 KB at a time, gates and ups in boxes of 64 bytes a row in the
 //           order of a 64-byte swizzle, replaced by dg and du in place.
-__device__ __forceinline__ void copy16(uint8_t* smem_dst, const void* g) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem_dst)), "l"(g) : "memory");
+// What is read or written once is the first to leave L2, where the operands are read again:
+// 16640 x 8192 x 5120 e4m3 485 -> 477 us.
+__device__ __forceinline__ uint64_t once_policy() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ void copy16(uint8_t* smem_dst, const void* g, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(smem_u32(smem_dst)),
+               "l"(g), "l"(policy)
+               : "memory");
+}
+__device__ __forceinline__ void tma_store_2d_once(const CUtensorMap* m, int32_t x, int32_t y,
+                                                  const void* smem_src, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group.L2::cache_hint [%0, {%1, %2}], [%3], %4;" ::
+          "l"(reinterpret_cast<uint64_t>(m)),
+      "r"(x), "r"(y), "r"(smem_u32(smem_src)), "l"(policy)
+      : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -568,7 +585,7 @@ __device__ __forceinline__ void copies_wait() {
 
 // Rows m .. m + 31, columns n .. n + 127, of both halves.
 __device__ __forceinline__ void copy_saved8(const ProductParams& p, uint8_t* to, int64_t m, int64_t n,
-                                            int lane) {
+                                            int lane, uint64_t policy) {
   const int c = lane & 7;                    // sixteen bytes of a row's 128
   if (n + 16 * c >= p.N) return;
 #pragma unroll
@@ -577,8 +594,8 @@ __device__ __forceinline__ void copy_saved8(const ProductParams& p, uint8_t* to,
     if (m + r >= p.M) break;
     const uint8_t* q = p.q + (m + r) * 2 * p.N + n + 16 * c;
     uint8_t* dst = to + (c >> 1) * 2048 + r * 32 + (((c ^ (r >> 2)) & 1) << 4);
-    copy16(dst, q);
-    copy16(dst + 1024, q + p.N);
+    copy16(dst, q, policy);
+    copy16(dst + 1024, q + p.N, policy);
   }
 }
 
@@ -597,7 +614,7 @@ struct SavedBlock {
 
 // ... columns c .. c + 31 of bf16.
 __device__ __forceinline__ void copy_saved16(const ProductParams& p, uint8_t* to, int64_t m, int64_t c,
-                                             int lane) {
+                                             int lane, uint64_t policy) {
   const int j = lane & 3;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -605,8 +622,8 @@ __device__ __forceinline__ void copy_saved16(const ProductParams& p, uint8_t* to
     if (m + r >= p.M) break;
     const uint16_t* x = p.gu + (m + r) * 2 * p.N + c + 8 * j;
     uint8_t* dst = reinterpret_cast<uint8_t*>(box64(to, r, j));
-    copy16(dst, x);
-    copy16(dst + 2048, x + p.N);
+    copy16(dst, x, policy);
+    copy16(dst + 2048, x + p.N, policy);
   }
 }
 
@@ -761,6 +778,7 @@ __global__ void __launch_bounds__(kPairThreads<EPI>, 1)
     uint8_t* so = stage_out + (warp - kFirst) * kWarpStage<EPI>;
     const uint32_t drained_bar = map_to_rank(smem_u32(&drained), 0);
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint64_t once = once_policy();
     int item = 0;
     bool ok = true;
     for (int t = first; ok && t < n_tiles; t += stride) {
@@ -851,7 +869,7 @@ __global__ void __launch_bounds__(kPairThreads<EPI>, 1)
         __syncwarp();
         if (EPI == kSwigluBack && m < p.M && n < p.N) {
           if constexpr (FLAG) {
-            copy_saved8(p, so, m, n, lane);
+            copy_saved8(p, so, m, n, lane, once);
             copies_commit();
             if (in)
 #pragma unroll
@@ -865,7 +883,7 @@ __global__ void __launch_bounds__(kPairThreads<EPI>, 1)
           } else {
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-              if (n + 32 * b < p.N) copy_saved16(p, so + 4096 * b, m, n + 32 * b, lane);
+              if (n + 32 * b < p.N) copy_saved16(p, so + 4096 * b, m, n + 32 * b, lane, once);
               copies_commit();
             }
           }
@@ -1032,8 +1050,8 @@ __global__ void __launch_bounds__(kPairThreads<EPI>, 1)
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-              tma_store_2d(&maps.gate, static_cast<int>(c), m, out_g);
-              tma_store_2d(&maps.up, static_cast<int>(c), m, out_u);
+              tma_store_2d_once(&maps.gate, static_cast<int>(c), m, out_g, once);
+              tma_store_2d_once(&maps.up, static_cast<int>(c), m, out_u, once);
               bulk_commit();
             }
             if (!FLAG && b == 1) {
@@ -1045,7 +1063,8 @@ __global__ void __launch_bounds__(kPairThreads<EPI>, 1)
                   else bulk_wait_read<0>();
                 }
                 __syncwarp();
-                if (c + 32 * (k + 1) < p.N) copy_saved16(p, so + 4096 * k, m, c + 32 * (k + 1), lane);
+                if (c + 32 * (k + 1) < p.N)
+                  copy_saved16(p, so + 4096 * k, m, c + 32 * (k + 1), lane, once);
                 copies_commit();
               }
             }

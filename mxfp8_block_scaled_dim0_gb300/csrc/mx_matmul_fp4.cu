@@ -1,5 +1,7 @@
 // mx_matmul_fp4.cu -- the product of two MX-FP4 operands (e2m1, blocks of 32, e8m0 scales):
-// the kernels of mx_product.cuh with results in bf16 or fp32.
+// the kernels of mx_product.cuh with results in bf16 or fp32.  16640 x 8192 x 5120 to bf16 takes
+// 199 us (7.0 PFLOP/s; repeated without a pause 214, at the power limit), bound by the operands'
+// way from L2 (about 20 TB/s); 8192 x 5120 x 16640 to fp32 217; 1 x 8192 x 5120 7.1, by its bytes.
 #include "mx_product.cuh"
 
 namespace mx {

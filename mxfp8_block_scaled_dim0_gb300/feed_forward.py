@@ -19,8 +19,9 @@ the block can be differentiated once; a second derivative raises an error.
 With fused=True the first projection and the activation are one kernel, as are the
 activation's backward pass and the gradient through the second projection: neither the
 activation's input nor the gradient of its output reaches memory in bf16.  bits=4 then
-takes every product's operands in MX-FP4 (the saved input stays in 8 bits); T, D and F
-are multiples of 64.
+takes every product's operands in MX-FP4, and keeps their dim1 casts (17/32 of a byte a
+value; the norm's and the activation's inputs stay in 8 bits); T, D and F are multiples
+of 64.
 
 Run as a program, it trains the block for a few steps on the current GPU and prints the
 loss and the bytes kept.

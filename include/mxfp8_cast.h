@@ -399,6 +399,8 @@ int mx_matmul_fp4(const void* qa, const void* sa_blk, const void* qb, const void
  *   h = g u / (1 + exp(-g)), from the sums, rounded once to bf16
  * g and u do not reach memory unless they are saved for the backward pass, in 8 bits: the
  * layout of mx_swiglu's save, (M x 2F) rows [g | u], each value rounded once from its sum.
+ * Sums as mx_matmul's for bf16; where they are saved, over at most 2560 steps in the tensor
+ * core's accumulator, and those in fp32.
  * The pages have no counterpart (see mx_layer_norm).
  *   qx      M x K elements of `format`, blocks of 32 along rows (mx_cast_dim0 or
  *           mx_cast_fp4_dim0 of X)                          [in]

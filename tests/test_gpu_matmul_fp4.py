@@ -141,3 +141,15 @@ def test_repeats_itself():
     want = run(a, b, torch.float32)
     for _ in range(3):
         assert torch.equal(run(a, b, torch.float32), want)
+
+
+@pytest.mark.parametrize("N", [40960, 40963])
+def test_offsets_past_32_bits(N):
+    """Results past 2^31 values and 2^33 bytes, through tensor maps and rows, on sampled rows."""
+    M, K = 65536, 64
+    a, b = operand(M, K, 1), operand(N, K, 2)
+    got = mx.matmul_fp4(*a, *b, torch.float32)
+    rows = torch.tensor([0, 1, 32767, 52427, 52428, 52429, 65535], device="cuda")
+    part = a[0][rows].contiguous(), mx.scales_to_blocked(a[1][blocked_at(M, K // 32, "cuda")[rows]])
+    want, _, tol = product(part, b, 4)
+    assert bool(((got[rows].double() - want).abs() <= tol).all())

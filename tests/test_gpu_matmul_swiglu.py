@@ -234,3 +234,24 @@ def test_wrappers(M, F, K, bits):
     for stream in (None, torch.cuda.current_stream()):
         assert torch.equal(mx.matmul_swiglu(*x, *joint, bits=bits, stream=stream), h)
     assert torch.equal(mx.matmul_swiglu(*x, [gate[0], up[0]], [gate[1], up[1]], bits=bits), h)
+
+
+def test_offsets_past_32_bits():
+    """131200 x 16640 gates and ups: saved bytes, h and gradients past 2^31 and 2^32, on
+    sampled rows."""
+    M, F, K = 131200, 16640, 64
+    x, gate, up = operand(M, K, 8, 1), operand(F, K, 8, 2, 0.2), operand(F, K, 8, 3, 0.2)
+    h, q, s = mx.matmul_swiglu(*x, *zip(gate, up), save=True)
+    rows = torch.tensor([0, 1, 127, 64528, 64529, 65535, 65536, 129056, 129057, 131199], device="cuda")
+    at = blocked_at(M, K // 32, "cuda")[rows]
+    part = x[0][rows], mx.scales_to_blocked(x[1][at])
+    pg, pu = product(part, gate, 8), product(part, up, 8)
+    p, tol = torch.cat([pg[0], pu[0]], 1), torch.cat([pg[2], pu[2]], 1)
+    off(h[rows], *swiglu_of(p, tol))
+    del h
+    saved_at = blocked_at(M, 2 * F // 32, "cuda")[rows]
+    saved = q[rows].contiguous(), mx.scales_to_blocked(s[saved_at])
+    check_saved(*saved, p, tol)
+    d = mx.matmul_swiglu_backward(*x, *gate, (q, s))
+    dh, _, tol = product(part, gate, 8)
+    off(d[rows], *swiglu_back_of(dh, tol, mx_values(*saved)))

@@ -714,16 +714,8 @@ int mx_matmul_swiglu(const void* qx, const void* sx_blk, const void* qg, const v
   if (int rc = encode_operand(&maps.b2, &maps.sb2, qu, su_blk, F, K, fp4, rows_w, 1)) return rc;
   if (int rc = encode_result(&maps.out, h, M, F, false)) return rc;
   maps.gate = maps.up = maps.out;
-  if (q0) {
+  if (q0)
     if (int rc = encode_halves(&maps, q0, M, F, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1)) return rc;
-    if (M % 128 != 0 || F % 64 != 0) {
-      // The kernel writes the scales that there are; the padding is cleared first.
-      const cudaError_t e =
-          cudaMemsetAsync(s0_blk, 0, static_cast<size_t>(mx_blocked_bytes(M, 2 * F / 32)),
-                          static_cast<cudaStream_t>(stream));
-      if (e != cudaSuccess) return cuda_fail(static_cast<int>(e));
-    }
-  }
   const mx::MatmulSwigluArgs a = {M, F, K, fp4, h, q0, s0_blk, nullptr};
   return launch_rc(mx::launch_matmul_swiglu(maps, a, sms, static_cast<cudaStream_t>(stream)));
 }

@@ -1049,10 +1049,8 @@ __global__ void __launch_bounds__(kPairThreads<EPI>, 1)
             }
           }
         } else {
-          // 32 columns at a time, in a loop whose registers move up: written out four times
-          // the code does not stay in the instruction cache.
           SavedBlock ahead;
-#pragma unroll 1
+#pragma unroll
           for (int b = 0; b < 4; ++b) {
             const int64_t c = n + 32 * b;
             if (c >= p.N) break;
@@ -1060,7 +1058,7 @@ __global__ void __launch_bounds__(kPairThreads<EPI>, 1)
             auto dh8 = [&](int j, f32x2 (&d)[4]) {
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                d[k] = pair(__uint_as_float(v[0][8 * j + 2 * k]), __uint_as_float(v[0][8 * j + 2 * k + 1]));
+                d[k] = pair(__uint_as_float(v[b][8 * j + 2 * k]), __uint_as_float(v[b][8 * j + 2 * k + 1]));
             };
             if constexpr (FLAG) {
               // A block ahead in registers, so that two places are free for the results: those
@@ -1133,12 +1131,6 @@ __global__ void __launch_bounds__(kPairThreads<EPI>, 1)
                   copy_saved16(p, so + 4096 * k, m, c + 32 * (k + 1), lane, once);
                 copies_commit();
               }
-            }
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              v[0][j] = v[1][j];
-              v[1][j] = v[2][j];
-              v[2][j] = v[3][j];
             }
           }
         }

@@ -5,7 +5,7 @@
 // The kernels are those of mx_product.cuh, for operands of 8 and of 4 bits.  Gate and up in one
 // launch read X once and store neither; 16640 x 8192 x 5120 e4m3 with the save takes 800 us
 // (the product of that size alone, to bf16, 757; its gated SiLU with the save 171), the
-// backward 477 (product 390, gated SiLU backward 169).  The tensor cores are the bound (busy in
+// backward 472 (product 390, gated SiLU backward 169).  The tensor cores are the bound (busy in
 // 68% of all cycles at 4096 x 4096 x 4096 with the save), the backward shares the memory with
 // 817 MB of saved values and results; few tokens are bound by the weights' bytes: one token,
 // 1 x 8192 x 5120 e2m1, 10.7 us for 44 MB.

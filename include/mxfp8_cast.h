@@ -399,8 +399,8 @@ int mx_matmul_fp4(const void* qa, const void* sa_blk, const void* qb, const void
  *   h = g u / (1 + exp(-g)), from the sums, rounded once to bf16
  * g and u do not reach memory unless they are saved for the backward pass, in 8 bits: the
  * layout of mx_swiglu's save, (M x 2F) rows [g | u], each value rounded once from its sum.
- * Sums as mx_matmul's for bf16; where they are saved, over at most 2560 steps in the tensor
- * core's accumulator, and those in fp32.
+ * Sums as mx_matmul's for bf16; where they are saved, over at most 1792 steps (MX_E2M1:
+ * 2560) in the tensor core's accumulator, and those in fp32.
  * The pages have no counterpart (see mx_layer_norm).
  *   qx      M x K elements of `format`, blocks of 32 along rows (mx_cast_dim0 or
  *           mx_cast_fp4_dim0 of X)                          [in]
@@ -492,8 +492,8 @@ int mx_selftest_watchdog(int64_t wait_ns, void* stream);
  * kernel of mx_dequant_blocked, used for C >= 1024; the kernels of mx_matmul,
  * mx_matmul_fp4, mx_matmul_swiglu, mx_matmul_swiglu_backward, mx_cast_fp4_dim1,
  * mx_cast_fp4_dim0_dim1, the tiled ones of mx_cast_fp4_dim0 and mx_dequant_fp4 (used
- * where there is a tile of 128 x 128 for every SM), mx_layer_norm and the first of mx_layer_norm_backward).  In that launch the
- * thread of CTA 0 that issues its loads waits, at its `at`-th tile (rowwise:
+ * where there is a tile of 128 x 128 for every SM), mx_layer_norm and the first of
+ * mx_layer_norm_backward).  In that launch the thread of CTA 0 that issues its loads waits, at its `at`-th tile (rowwise:
  * step; products: block of 128 contraction bytes; layer norm: row of its first
  * group), on a barrier that nothing completes, for at most `wait_ns` nanoseconds
  * (1e3 .. 1e10).  The wait gives up, the CTA stops every role, lets the

@@ -3,7 +3,7 @@
 // and the gradient of the projections' results from that of the layer's output.
 //
 // The kernels are those of mx_product.cuh, for operands of 8 and of 4 bits.  Gate and up in one
-// launch read X once and store neither; 16640 x 8192 x 5120 e4m3 with the save takes 800 us
+// launch read X once and store neither; 16640 x 8192 x 5120 e4m3 with the save takes 819 us
 // (the product of that size alone, to bf16, 757; its gated SiLU with the save 171), the
 // backward 472 (product 390, gated SiLU backward 169).  The tensor cores are the bound (busy in
 // 68% of all cycles at 4096 x 4096 x 4096 with the save), the backward shares the memory with
@@ -18,7 +18,7 @@ template <bool FP4>
 int launch_forward(const ProductMaps& maps, ProductParams& p, int num_sms,
                    cudaStream_t stream) {
   // Saved sums go in runs.
-  constexpr int kRun = kSavedRunSteps / Shape<FP4, kSwiglu>::kSteps;
+  constexpr int kRun = kSavedRunSteps<FP4> / Shape<FP4, kSwiglu>::kSteps;
   if (product_pairs(p.M, 2 * p.N, num_sms)) {
     p.m_tiles = static_cast<int>((p.M + 255) / 256);
     p.n_tiles = static_cast<int>((p.N + 127) / 128);

@@ -1173,8 +1173,12 @@ __global__ void __launch_bounds__(kPairThreads<EPI>, 1)
 // Steps summed in tensor memory at a time, where it matters, at most.  fp32 results: as
 // mx_matmul.  Saved ones: fewer, so that as few of them as of a plain fp32 product's go to the
 // other neighbour in e4m3, or whole blocks to the other scale (5120 steps in one run are 3e-7
-// off in the 2-norm, in two 1.6e-7, a plain fp32 product 1.05e-7).
-constexpr int kRunSteps = 4096, kSavedRunSteps = 2560;
+// off in the 2-norm, in two 1.6e-7, in three 1.14e-7, a plain fp32 product 1.05e-7).  A run is
+// to outlast the epilogue of the tile before: 16640 x 8192 x 5120 e4m3 takes 800 us in one run,
+// 819 in three, 870 in four; e2m1, at twice the rate, 420 in one, 450 to 510 in two, 505 in three.
+constexpr int kRunSteps = 4096;
+template <bool FP4>
+constexpr int kSavedRunSteps = FP4 ? 2560 : 1792;
 
 // ---- launches ----------------------------------------------------------------------
 
@@ -1203,7 +1207,8 @@ int launch_pair_kernel(const ProductMaps& maps, const ProductParams& p, int num_
   const int attr = attr_cache.get([] {
     // The warpgroups' shares must be there at launch: one that asked for more would wait.
     cudaFuncAttributes fa;
-    if (const cudaError_t e = cudaFuncGetAttributes(&fa, pair_kernel<FP4, EPI, FLAG>)) return static_cast<int>(e);
+    if (const cudaError_t e = cudaFuncGetAttributes(&fa, pair_kernel<FP4, EPI, FLAG>))
+      return static_cast<int>(e);
     if (EPI == kSwigluBack && fa.numRegs * kPairThreads<EPI> < 128 * kGiven + 256 * kTaken)
       return static_cast<int>(cudaErrorInvalidConfiguration);
     return static_cast<int>(cudaFuncSetAttribute(pair_kernel<FP4, EPI, FLAG>,

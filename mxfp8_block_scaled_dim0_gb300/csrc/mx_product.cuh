@@ -559,13 +559,15 @@ __global__ void __launch_bounds__(kTileThreads<EPI>, 1)
 // Stages of loads, and bytes of an epilogue warp's staging.  A stage counts: 16640 x 8192 x
 // 5120 e2m1 takes 199 us with five, 216 with four, 257 with three (six do not fit); h with
 // the save in e4m3 790 and 860, although with four the warps need not wait for the stores.
+// Beside five fit 6 KB a warp for kSwiglu: gate's bytes go behind h and only up's wait until
+// h has left (13766 x 5344 x 1088 e2m1 with the save 121 us with 4 KB, 114 with 6).
 // kSwigluBack does with four, as gates and ups come through shared memory: loads of a row a
 // lane touch 32 lines each, and took the load/store units as long as all else (8192 x 8192 x
 // 1024 e2m1 135 us with them, 111 without).
 template <int EPI>
 constexpr int kPairStages = EPI == kSwigluBack ? 4 : 5;
 template <int EPI>
-constexpr int kWarpStage = EPI == kSwigluBack ? 10 * 1024 : kStageOut;
+constexpr int kWarpStage = EPI == kSwigluBack ? 10 * 1024 : EPI == kSwiglu ? 6 * 1024 : kStageOut;
 template <bool FP4, int EPI>
 constexpr int kPairSmem = kPairStages<EPI> * Shape<FP4, EPI>::kPairStride + 8 * kWarpStage<EPI> + 1024;
 
@@ -1021,11 +1023,15 @@ __global__ void __launch_bounds__(kPairThreads<EPI>, 1)
             bulk_commit();
           }
           if constexpr (FLAG) {
-            if (lane == 0) bulk_wait_read<0>();
-            __syncwarp();
+            // Gate's bytes behind h, up's in its place when it has left.
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
               // Block b: gate's two, up's two.
+              if (b == 2) {
+                if (lane == 0) bulk_wait_read<0>();
+                __syncwarp();
+              }
+              uint8_t* saved = b < 2 ? so + kStageOut : so;
               const int64_t c = n + (b & 1) * 32;
               uint32_t a = 0;
 #pragma unroll
@@ -1037,15 +1043,15 @@ __global__ void __launch_bounds__(kPairThreads<EPI>, 1)
               auto four = [&](int j) { return e4m3x4(f(j), f(j + 1), f(j + 2), f(j + 3), mult); };
 #pragma unroll
               for (int j = 0; j < 2; ++j)
-                *box64(so + (b >> 1) * 2048, lane, (b & 1) * 2 + j) =
+                *box64(saved, lane, (b & 1) * 2 + j) =
                     make_uint4(four(16 * j), four(16 * j + 4), four(16 * j + 8), four(16 * j + 12));
               if (in && c < p.N) store_scale(p, row, ((b >> 1) ? p.N + c : c) >> 5, sbyte);
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-              tma_store_2d(&maps.gate, n, m, so);
-              tma_store_2d(&maps.up, n, m, so + 2048);
+              tma_store_2d(&maps.gate, n, m, so + kStageOut);
+              tma_store_2d(&maps.up, n, m, so);
               bulk_commit();
             }
           }

@@ -14,7 +14,10 @@ everything that the backward pass needs of the forward pass is kept as MX bytes:
     the norm's statistics                                   8
 
 half of what bf16 would take (4 D + 6 F).  The operators' results carry no graph, so
-the block can be differentiated once; a second derivative raises an error.
+the block can be differentiated once; a second derivative raises an error.  A step of it can
+be captured into a CUDA graph; no result of an earlier forward pass that still holds its
+graph may live then, as autograd adds to a parameter's gradient on the stream of the oldest
+graph that lives.
 
 With fused=True the first projection and the activation are one kernel, as are the
 activation's backward pass and the gradient through the second projection: neither the

@@ -147,6 +147,36 @@ def test_a_step_in_a_graph(bits):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("bits", [8, 4])
+def test_autograds_step_in_a_graph(bits):
+    """The block's own forward and backward pass captured, replayed on other tokens."""
+    T, D, F = 320, 256, 640
+    block, eager = block_of(D, F, bits), block_of(D, F, bits)
+    x, dy = rnd(T, D, seed=1), rnd(T, D, seed=2)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            block.zero_grad(set_to_none=True)
+            block(x).backward(dy)               # its graph is gone before the capture
+    torch.cuda.current_stream().wait_stream(side)
+    block.zero_grad(set_to_none=True)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = block(x)
+        y.backward(dy)
+    for seed in (3, 5):
+        x.copy_(rnd(T, D, seed=seed))
+        dy.copy_(rnd(T, D, seed=seed + 1))
+        graph.replay()
+        eager.zero_grad(set_to_none=True)
+        want = eager(x)
+        want.backward(dy)
+        assert torch.equal(y, want)
+        for a, b in zip(block.parameters(), eager.parameters()):
+            assert torch.equal(a.grad, b.grad)
+
+
 def test_two_streams_at_once():
     """The same operators on two streams: nothing is shared between calls."""
     streams, want, got = [torch.cuda.Stream() for _ in range(2)], [], []

@@ -289,7 +289,9 @@ int mx_cast_rowwise(const void* x, int64_t M, int64_t K, void* q, void* scale, v
  * fp32 would round; for an fp32 output over 4096 steps at most, and those are added
  * up in fp32 (2.3e-7 of the 2-norm after 131072 steps, 1.4e-6 where all terms have
  * one sign, at any size of the output).
- * A call gives the same bits every time. */
+ * A call gives the same bits every time.  The sizes choose where a sum is cut, so a
+ * row's last bits may be others in a batch of another M; at one M they do not depend
+ * on what the other rows hold. */
 int mx_matmul(const void* qa, const void* sa_blk, const void* qb, const void* sb_blk, int64_t M,
               int64_t N, int64_t K, int32_t orders, void* out, int32_t out_type, void* stream);
 
@@ -389,7 +391,7 @@ int mx_dequant_fp4(const void* q, int64_t R, int64_t C, const void* s_blk, void*
  *   M, N    >= 1 (any); K % 64 == 0 (the tensor cores take 64 steps at a time), K >= 64;
  *           all <= 2^31 - 256
  *   out     M x N values of out_type (MX_BF16 or MX_F32)    [out]
- * Sums, NaN scales and ranges as mx_matmul. */
+ * Sums, their dependence on the sizes, NaN scales and ranges as mx_matmul. */
 int mx_matmul_fp4(const void* qa, const void* sa_blk, const void* qb, const void* sb_blk, int64_t M,
                   int64_t N, int64_t K, void* out, int32_t out_type, void* stream);
 
@@ -400,7 +402,9 @@ int mx_matmul_fp4(const void* qa, const void* sa_blk, const void* qb, const void
  * g and u do not reach memory unless they are saved for the backward pass, in 8 bits: the
  * layout of mx_swiglu's save, (M x 2F) rows [g | u], each value rounded once from its sum.
  * Sums as mx_matmul's for bf16; where they are saved, over at most 1792 steps (MX_E2M1:
- * 2560) in the tensor core's accumulator, and those in fp32.
+ * 2560) in the tensor core's accumulator, and those in fp32.  So over more steps than that
+ * h with the save and h without it may differ in the last bits, as may a row's results in
+ * batches of another M.
  * The pages have no counterpart (see mx_layer_norm).
  *   qx      M x K elements of `format`, blocks of 32 along rows (mx_cast_dim0 or
  *           mx_cast_fp4_dim0 of X)                          [in]

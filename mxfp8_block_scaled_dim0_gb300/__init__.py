@@ -898,7 +898,8 @@ def dequant_fp4(q, s_blk, stream=None):
 
 
 def matmul_fp4(qa, sa_blk, qb, sb_blk, out_dtype=torch.bfloat16, stream=None):
-    """A B^T of MX-FP4 operands as a (M, N) tensor of out_dtype."""
+    """A B^T of MX-FP4 operands as a (M, N) tensor of out_dtype.  A row's last bits may be
+    others in a batch of another M."""
     if stream is not None:
         with _on_stream(stream, qa):
             return matmul_fp4(qa, sa_blk, qb, sb_blk, out_dtype)
@@ -930,7 +931,8 @@ def matmul_swiglu(qx, sx_blk, qw, sw_blk, save=False, bits=8, stream=None):
     """h = silu(g) u, g = X Wg^T, u = X Wu^T, of MX operands with elements of `bits` (8 or 4):
     X (M, K), and either Wg and Wu (F, K) as pairs (gate, up) of bytes and of scales, or,
     with F a multiple of 128, [Wg; Wu] (2F, K) in one.  Returns h (M, F), with save=True
-    (h, q0, s0_blk): [g | u] saved in 8 bits for the backward pass."""
+    (h, q0, s0_blk): [g | u] saved in 8 bits for the backward pass.  A row's last bits may be
+    others in a batch of another M and, past 1792 steps K (in 4 bits 2560), with the save."""
     if stream is not None:
         with _on_stream(stream, qx):
             return matmul_swiglu(qx, sx_blk, qw, sw_blk, save, bits)

@@ -1,5 +1,6 @@
-"""The sums of the joined products that are saved: as exact as runs of their documented length
-make them, which no worst-case tolerance of an uncut contraction shows."""
+"""The sums of the joined products: those that are saved are as exact as runs of their documented
+length make them, which no worst-case tolerance of an uncut contraction shows; and what they
+depend on."""
 import pytest
 import torch
 
@@ -77,3 +78,33 @@ def test_saved_sums_of_one_sign(M, F, bits):
     least, most = (e4m3_of(v.reshape(M, -1, 32) / scale) for v in (lo, hi))
     bad = (got < least) | (got > most)
     assert not bool(bad.any()), "%d of %d saved values off" % (int(bad.sum()), bad.numel())
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("M,F,K", [(7, 320, 1088), (300, 160, 4160), (130, 4096, 192), (2304, 2208, 320)])
+def test_rows_at_one_batch_size(M, F, K, bits):
+    """At one number of rows a row's results do not depend on what the others hold, numbers
+    or not.  (Another number of rows may cut the contraction elsewhere.)"""
+    x, gate, up = operand(M, K, bits, 1), operand(F, K, bits, 2), operand(F, K, bits, 3)
+    keep = torch.tensor([0, M // 2, M - 1], device="cuda")
+    others = torch.ones(M, dtype=torch.bool, device="cuda")
+    others[keep] = False
+    q, s = operand(M, K, bits, 4)
+    q[keep] = x[0][keep]
+    at = blocked_at(M, K // 32, "cuda")
+    s[at[keep]] = x[1][at[keep]]
+    nan = others.nonzero()[:2, 0]
+    s[at[nan]] = 255
+    w = tuple(zip(gate, up))
+
+    def results(a):
+        h, sq, ss = mx.matmul_swiglu(*a, *w, save=True, bits=bits)
+        saved_at = blocked_at(M, 2 * F // 32, "cuda")[keep]
+        out = [h[keep], sq[keep], ss[saved_at], mx.matmul_swiglu(*a, *w, bits=bits)[keep]]
+        gu = mx.dequant_blocked(sq, ss)
+        out.append(mx.matmul_swiglu_backward(*a, *gate, (sq, ss), bits=bits)[keep])
+        out.append(mx.matmul_swiglu_backward(*a, *gate, gu, bits=bits)[keep])
+        out.append((mx.matmul if bits == 8 else mx.matmul_fp4)(*a, *gate)[keep])
+        return out
+    for a, b in zip(results(x), results((q, s))):
+        assert torch.equal(a, b)

@@ -242,7 +242,7 @@ constexpr int kDqSmem = kDqStages * kDqStage + 2 * kDqOut + 1024;
 
 struct DqTileParams {
   const uint8_t* s;
-  int64_t R, C, tiles_c, tiles;
+  int64_t C, tiles_c, tiles;
   int64_t stall_at;
   uint64_t stall_ns;
 };
@@ -631,7 +631,7 @@ int launch_dequant_fp4(const DequantFp4Maps* maps, const void* q, int64_t R, int
   if (dequant_fp4_tiles(R, C, num_sms)) {
     const int64_t tiles_c = (C + 127) / 128, tiles = (R + 127) / 128 * tiles_c;
     const Stall stall = take_stall();
-    const DqTileParams t = {static_cast<const uint8_t*>(s_blk), R, C, tiles_c, tiles, stall.at, stall.ns};
+    const DqTileParams t = {static_cast<const uint8_t*>(s_blk), C, tiles_c, tiles, stall.at, stall.ns};
     return launch_dequant_tiles(*maps, t, num_sms, stream);
   }
   DequantParams p = {static_cast<const uint8_t*>(q), static_cast<const uint8_t*>(s_blk),

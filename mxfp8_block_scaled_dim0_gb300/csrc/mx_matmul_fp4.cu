@@ -23,7 +23,7 @@ int launch_matmul_fp4(const ProductMaps& maps, int64_t M, int64_t N, int64_t K, 
   p.mapped = matmul_mapped(N, out_f32);
   p.sp_out = make_span(out, static_cast<uint64_t>(M) * static_cast<uint64_t>(N) * (out_f32 ? 4 : 2));
   // Longer fp32 sums go in runs.
-  constexpr int kRun = kRunSteps / Shape<true, kPlain>::kSteps;
+  constexpr int kRun = kRunSteps / Shape<true>::kSteps;
   if (product_pairs(M, N, num_sms)) {
     p.m_tiles = static_cast<int>((M + 255) / 256);
     p.n_tiles = static_cast<int>((N + 255) / 256);
@@ -38,7 +38,7 @@ int launch_matmul_fp4(const ProductMaps& maps, int64_t M, int64_t N, int64_t K, 
   p.m_tiles = static_cast<int>((M + 127) / 128);
   p.n_tiles = static_cast<int>((N + t.cols - 1) / t.cols);
   p.load_bytes = (matmul_box_rows(M, false, 128) + matmul_box_rows(N, false, t.cols)) * kBoxCols +
-                 2 * Shape<true, kPlain>::kSf * kSfBytes;
+                 2 * Shape<true>::kSf * kSfBytes;
   p.run = kRun;
   return out_f32 && (p.k_blocks + p.split - 1) / p.split > kRun
              ? launch_tile_kernel<true, kPlain, true>(maps, p, stream)

@@ -18,7 +18,7 @@ template <bool FP4>
 int launch_forward(const ProductMaps& maps, ProductParams& p, int num_sms,
                    cudaStream_t stream) {
   // Saved sums go in runs.
-  constexpr int kRun = kSavedRunSteps<FP4> / Shape<FP4, kSwiglu>::kSteps;
+  constexpr int kRun = kSavedRunSteps<FP4> / Shape<FP4>::kSteps;
   if (product_pairs(p.M, 2 * p.N, num_sms)) {
     p.m_tiles = static_cast<int>((p.M + 255) / 256);
     p.n_tiles = static_cast<int>((p.N + 127) / 128);
@@ -36,7 +36,7 @@ int launch_forward(const ProductMaps& maps, ProductParams& p, int num_sms,
   p.m_tiles = static_cast<int>((p.M + 127) / 128);
   p.n_tiles = static_cast<int>((p.N + t.cols - 1) / t.cols);
   p.load_bytes = (matmul_box_rows(p.M, false, 128) + matmul_box_rows(p.N, false, t.cols)) * kBoxCols +
-                 2 * Shape<FP4, kSwiglu>::kSf * kSfBytes;
+                 2 * Shape<FP4>::kSf * kSfBytes;
   p.run = kRun;
   return p.q && (p.k_blocks + p.split - 1) / p.split > kRun
              ? launch_tile_kernel<FP4, kSwiglu, true>(maps, p, stream)
@@ -57,7 +57,7 @@ int launch_backward(const ProductMaps& maps, ProductParams& p, int num_sms, cuda
   p.m_tiles = static_cast<int>((p.M + 127) / 128);
   p.n_tiles = static_cast<int>((p.N + t.cols - 1) / t.cols);
   p.load_bytes = (matmul_box_rows(p.M, false, 128) + matmul_box_rows(p.N, false, t.cols)) * kBoxCols +
-                 2 * Shape<FP4, kSwigluBack>::kSf * kSfBytes;
+                 2 * Shape<FP4>::kSf * kSfBytes;
   return launch_tile_kernel<FP4, kSwigluBack, false>(maps, p, stream);
 }
 

@@ -49,7 +49,7 @@ constexpr int kStageOut = 4096;             // a warp's results on their way out
 
 enum Epilogue { kPlain, kSwiglu, kSwigluBack };
 
-template <bool FP4, int EPI>
+template <bool FP4>
 struct Shape {
   static constexpr int kSteps = FP4 ? 256 : 128;        // contraction steps of a stage
   static constexpr int kSf = FP4 ? 2 : 1;               // scale tiles of 128 rows in a stage
@@ -97,11 +97,6 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t da, uint64_t db, uint32
 template <bool FP4>
 __device__ __forceinline__ uint32_t idesc_of(int m, int n) {
   return FP4 ? mxf4_idesc(m, n) : mxf8_idesc(m, n, false, false);
-}
-
-// Where scale (row m, column c) lies in a blocked matrix of cols4 padded columns.
-__device__ __forceinline__ int64_t scale_at(int64_t m, int64_t c, int64_t cols4) {
-  return blocked_offset(m, c, cols4);
 }
 
 // Scale byte and multiplier of a block from the bits of its largest magnitude in fp32.
@@ -156,7 +151,7 @@ __device__ __forceinline__ void cluster_sum8(const float* part, int split, uint3
 }
 
 __device__ __forceinline__ void store_scale(const ProductParams& p, int64_t m, int64_t c, uint32_t v) {
-  uint8_t* s = p.s + scale_at(m, c, p.s_cols4);
+  uint8_t* s = p.s + blocked_offset(m, c, p.s_cols4);
   if (in_span(p.sp_s, s, 1)) *s = static_cast<uint8_t>(v);
 }
 
@@ -192,8 +187,8 @@ struct Saved8 {
       g.y = a.y;
       u.x = b.x;
       u.y = b.y;
-      s = __ldg(p.s + scale_at(m, c >> 5, p.s_cols4)) |
-          static_cast<uint32_t>(__ldg(p.s + scale_at(m, (p.N + c) >> 5, p.s_cols4))) << 8;
+      s = __ldg(p.s + blocked_offset(m, c >> 5, p.s_cols4)) |
+          static_cast<uint32_t>(__ldg(p.s + blocked_offset(m, (p.N + c) >> 5, p.s_cols4))) << 8;
     } else {
       const uint16_t* x = p.gu + m * 2 * p.N + c;
       g = __ldg(reinterpret_cast<const uint4*>(x));
@@ -217,7 +212,7 @@ struct Saved8 {
 template <bool FP4, int EPI, bool RUNS>
 __global__ void __launch_bounds__(kTileThreads<EPI>, 1)
     tile_kernel(const __grid_constant__ ProductMaps maps, const ProductParams p) {
-  using S = Shape<FP4, EPI>;
+  using S = Shape<FP4>;
   static_assert(!RUNS || EPI != kSwigluBack, "16-bit results need no runs");
   static_assert(kBoxRows * kPitch * 4 <= kTileStages * S::kTileStride, "partial tile fits the ring");
   asm volatile("griddepcontrol.launch_dependents;");
@@ -569,7 +564,7 @@ constexpr int kPairStages = EPI == kSwigluBack ? 4 : 5;
 template <int EPI>
 constexpr int kWarpStage = EPI == kSwigluBack ? 10 * 1024 : EPI == kSwiglu ? 6 * 1024 : kStageOut;
 template <bool FP4, int EPI>
-constexpr int kPairSmem = kPairStages<EPI> * Shape<FP4, EPI>::kPairStride + 8 * kWarpStage<EPI> + 1024;
+constexpr int kPairSmem = kPairStages<EPI> * Shape<FP4>::kPairStride + 8 * kWarpStage<EPI> + 1024;
 
 // Loads, MMA, eight epilogue warps.  kSwigluBack: two idle warps more, so that the first
 // warpgroup can hand registers to the two that hold 128 results and what they need beside
@@ -689,7 +684,7 @@ __device__ __forceinline__ void copy_saved16(const ProductParams& p, uint8_t* to
 template <bool FP4, int EPI, bool FLAG>
 __global__ void __launch_bounds__(kPairThreads<EPI>, 1)
     pair_kernel(const __grid_constant__ ProductMaps maps, const ProductParams p) {
-  using S = Shape<FP4, EPI>;
+  using S = Shape<FP4>;
   constexpr int kStages = kPairStages<EPI>;
   asm volatile("griddepcontrol.launch_dependents;");
   extern __shared__ uint8_t smem_raw[];
@@ -935,9 +930,10 @@ __global__ void __launch_bounds__(kPairThreads<EPI>, 1)
               for (int b = 0; b < 4; ++b)
                 if (n + 32 * b < p.N) {
                   const int64_t c = n / 32 + b;
-                  scales[0] |= static_cast<uint32_t>(__ldg(p.s + scale_at(row, c, p.s_cols4))) << (8 * b);
-                  scales[1] |=
-                      static_cast<uint32_t>(__ldg(p.s + scale_at(row, p.N / 32 + c, p.s_cols4))) << (8 * b);
+                  const uint32_t sg = __ldg(p.s + blocked_offset(row, c, p.s_cols4));
+                  const uint32_t su = __ldg(p.s + blocked_offset(row, p.N / 32 + c, p.s_cols4));
+                  scales[0] |= sg << (8 * b);
+                  scales[1] |= su << (8 * b);
                 }
           } else {
 #pragma unroll
@@ -1233,7 +1229,7 @@ int launch_pair_kernel(const ProductMaps& maps, const ProductParams& p, int num_
 
 template <bool FP4, int EPI, bool RUNS>
 int launch_tile_kernel(const ProductMaps& maps, const ProductParams& p, cudaStream_t stream) {
-  constexpr int kSmem = kTileStages * Shape<FP4, EPI>::kTileStride + 1024;
+  constexpr int kSmem = kTileStages * Shape<FP4>::kTileStride + 1024;
   static DeviceCache attr_cache;
   const int attr = attr_cache.get([] {
     return static_cast<int>(cudaFuncSetAttribute(tile_kernel<FP4, EPI, RUNS>,

@@ -5,7 +5,8 @@
 //   dg = dh u sg (1 + g (1 - sg)),  du = dh g sg
 //
 // The exponential and the division go through the fast hardware functions, whose error
-// (a few units of 2^-22) is far below the rounding of the results to 16 or 8 bits.
+// (a few units of 2^-22, and |g| 2^-24 as the exponent is rounded) is far below the rounding
+// of the results to 16 or 8 bits.
 #pragma once
 
 #include "mx_rows.cuh"

@@ -1,7 +1,9 @@
 // mx_matmul_fp4.cu -- the product of two MX-FP4 operands (e2m1, blocks of 32, e8m0 scales):
 // the kernels of mx_product.cuh with results in bf16 or fp32.  16640 x 8192 x 5120 to bf16 takes
-// 199 us (7.0 PFLOP/s; repeated without a pause 214, at the power limit), bound by the operands'
-// way from L2 (about 20 TB/s); 8192 x 5120 x 16640 to fp32 217; 1 x 8192 x 5120 7.1, by its bytes.
+// 199 us (7.0 PFLOP/s; repeated without a pause 214, at the power limit), bound by how long
+// the operands' loads are under way (3.0 GB from L2, 15 TB/s, is not its bandwidth, but four and
+// three stages of loads ahead instead of five take 216 and 257); 8192 x 5120 x 16640 to fp32
+// 218; 1 x 8192 x 5120 7.1 (22 MB, 3.1 TB/s): a CTA on 128 of 152 SMs.
 #include "mx_product.cuh"
 
 namespace mx {

@@ -3,12 +3,14 @@
 // and the gradient of the projections' results from that of the layer's output.
 //
 // The kernels are those of mx_product.cuh, for operands of 8 and of 4 bits.  Gate and up in one
-// launch read X once and store neither; 16640 x 8192 x 5120 e4m3 with the save takes 819 us
-// (the product of that size alone, to bf16, 757; its gated SiLU with the save 171), the
-// backward 472 (product 390, gated SiLU backward 169).  The tensor cores are the bound (busy in
-// 68% of all cycles at 4096 x 4096 x 4096 with the save), the backward shares the memory with
-// 817 MB of saved values and results; few tokens are bound by the weights' bytes: one token,
-// 1 x 8192 x 5120 e2m1, 10.7 us for 44 MB.
+// launch read X once and store neither; 16640 x 8192 x 5120 e4m3 with the save takes 820 us
+// (the product of that size alone, to bf16, 769; its gated SiLU with the save 171), the
+// backward 470 (product 390, gated SiLU backward 169).  Those are a few calls after a pause:
+// repeated without one, the power limit makes them 950 and 525.  The tensor cores are the bound
+// (busy in 68% of all cycles at 4096 x 4096 x 4096 with the save), the backward shares the
+// memory with 817 MB of saved values and results.  In e2m1 the epilogue outlasts short
+// contractions: 367 us without the save, 440 with it, 280 backward, and 76, 114 at 13766 x 5344
+// x 1088.  One token, 1 x 8192 x 5120: e2m1 10.6 us for 45 MB of weights, e4m3 16.9 for 87.
 #include "mx_product.cuh"
 
 namespace mx {

@@ -16,7 +16,7 @@
 // tile_kernel: 128 x 128 (or 64) results by a cluster of S CTAs that share the
 // contraction; each sums and finishes 128 / S of the tile's rows, in rank order.  kSwiglu: 2 S
 // CTAs, every other one on gate and on up (both in one CTA, as two MMAs of 64 columns, took
-// 12.0 us where one MMA of 128 takes 10.3: 44 MB of weights for one token).
+// 12.0 us where one MMA of 128 takes 10.6: 45 MB of weights for one token).
 //
 // What happens to the results (EPI):
 //   kPlain       out = P in bf16 or fp32
@@ -553,7 +553,8 @@ __global__ void __launch_bounds__(kTileThreads<EPI>, 1)
 //
 // Stages of loads, and bytes of an epilogue warp's staging.  A stage counts: 16640 x 8192 x
 // 5120 e2m1 takes 199 us with five, 216 with four, 257 with three (six do not fit); h with
-// the save in e4m3 790 and 860, although with four the warps need not wait for the stores.
+// the save in e4m3, its sums in one run, 790 and 860, although with four the warps need not
+// wait for the stores.
 // Beside five fit 6 KB a warp for kSwiglu: gate's bytes go behind h and only up's wait until
 // h has left (13766 x 5344 x 1088 e2m1 with the save 121 us with 4 KB, 114 with 6).
 // kSwigluBack does with four, as gates and ups come through shared memory: loads of a row a
@@ -568,7 +569,8 @@ constexpr int kPairSmem = kPairStages<EPI> * Shape<FP4>::kPairStride + 8 * kWarp
 
 // Loads, MMA, eight epilogue warps.  kSwigluBack: two idle warps more, so that the first
 // warpgroup can hand registers to the two that hold 128 results and what they need beside
-// (168 a thread at launch: 56 x 128 + 224 x 256 are as many).
+// (168 a thread at launch: 56 x 128 + 224 x 256 are as many).  Of 168 and 224, kSwiglu with
+// the save spills 12 words a thread and kSwigluBack from 8 bits 24; no other kernel spills.
 template <int EPI>
 constexpr int kFirstEpilogueWarp = EPI == kSwigluBack ? 4 : 2;
 template <int EPI>
@@ -1173,11 +1175,17 @@ __global__ void __launch_bounds__(kPairThreads<EPI>, 1)
 }
 
 // Steps summed in tensor memory at a time, where it matters, at most.  fp32 results: as
-// mx_matmul.  Saved ones: fewer, so that as few of them as of a plain fp32 product's go to the
-// other neighbour in e4m3, or whole blocks to the other scale (5120 steps in one run are 3e-7
-// off in the 2-norm, in two 1.6e-7, in three 1.14e-7, a plain fp32 product 1.05e-7).  A run is
-// to outlast the epilogue of the tile before: 16640 x 8192 x 5120 e4m3 takes 800 us in one run,
-// 819 in three, 870 in four; e2m1, at twice the rate, 420 in one, 450 to 510 in two, 505 in three.
+// mx_matmul.  Saved ones: fewer, so that about as few of them as of a plain fp32 product's go
+// to the other neighbour in e4m3, or whole blocks to the other scale.  e4m3 operands, 5120
+// steps: one run is 3e-7 off in the 2-norm, two 1.64e-7, three 1.14e-7, four 9.3e-8, a plain
+// fp32 product 1.05e-7.  Of 67 million saved values 98, 221, 379 and 428 are not those of the
+// sums in 64 bits at 1024, 2560, 5120 and 8192 steps, of a plain fp32 product's 196, 233, 352
+// and 431.  e2m1 operands need it less: products of elements are quarters of whole numbers, so
+// that sums under scales near each other fit 24 bits (none of the values differed, in runs of
+// 256 to 4096 steps); runs count where a row's scales spread over many powers of two.  A run is
+// to outlast the epilogue of the tile before: 16640 x 8192 x 5120 e4m3 takes 797 us in one run,
+// 820 to 835 in three, 870 in four; e2m1, at twice the rate, 411 in one, 440 to 450 in two, 497
+// in three.
 constexpr int kRunSteps = 4096;
 template <bool FP4>
 constexpr int kSavedRunSteps = FP4 ? 2560 : 1792;

@@ -144,6 +144,9 @@ class _Fused(torch.autograd.Function):
 class FeedForward(torch.nn.Module):
     """The block.  Norm parameters in float32, weights in bf16."""
 
+    # What a module that was saved whole before it had these choices runs with.
+    fused, bits, step = False, 8, 32
+
     def __init__(self, dim, hidden, eps=1e-5, device="cuda", fused=False, bits=8):
         super().__init__()
         if bits not in _OPERANDS or (bits == 4 and not fused):
